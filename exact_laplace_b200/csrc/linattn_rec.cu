@@ -1,0 +1,459 @@
+// linattn_rec.cu -- decayed linear attention as a recurrence over tokens, for
+// every type (16-bit and fp32 rows computed in fp32, fp64 rows in fp64).
+//
+// The anchors of a causal sequence are a_t = -lam t, so the printed recurrence
+// L_{i+1} = x_{i+1} + exp(a_i - a_{i+1}) L_i (summary §2.2) runs over the tokens
+// in order; x_t is the outer product k_t v_t^T, and the output reads the running
+// sum through q_t:
+//     S_t = e^lam S_{t-1} + k_t v_t^T,      o_t = scale S_t^T q_t.
+// A block holds 64 columns of one head's state in registers (8 row groups x 4
+// columns per thread) and walks a segment of the sequence.  Tokens are taken in
+// blocks of n <= 32: the state is scaled by e^{lam n} once, and inside the block
+// k_tau carries e^{lam (n - 1 - tau)} and q_tau its inverse, so that a token
+// costs two multiply-adds per state element and the rounding of e^lam enters
+// once per n tokens (a product of 2000 rounded e^lam would be off by 6e-5).  n is
+// at most 4 / |lam|: neither factor leaves [e^-4, e^4].
+//
+// Bound by those multiply-adds (4 dk dv flops a token and head): 65536 fp32
+// values of q, k, v and o a microsecond and SM at dk = dv = 128.  Long sequences
+// are cut into segments (see LinSeqs): a first pass sums each segment's own
+// state, carry_run joins them, and the product starts each segment from its
+// state.
+#include <algorithm>
+
+#include "devcache.h"
+#include "elem.cuh"
+#include "seqop.h"
+
+namespace lx {
+
+constexpr int REC_NT = 128;
+constexpr int REC_COLS = 64;  // state columns of a block
+constexpr int REC_ROWS = 32;  // rows of k, v, q in shared memory: tokens times heads of a group
+
+struct RecArgs {
+    LinRole R;
+    LinSeqs S;
+    int H;
+    const void* lam;
+    LinRows dout;        // derivative: the output's cotangent
+    const void* w_in;    // derivative: by slot, or NULL (zero)
+    const void* dstate;  // derivative: the last state's cotangent, or NULL
+    double* part;        // derivative: one sum per block
+};
+
+// rows (token tau of the block, head g) of X, weighted, into dst[row][PITCH]; c0: first column
+template <typename T, typename A, int PITCH>
+__device__ __forceinline__ void rec_load(A* dst, const LinRows& X, int heads, int h, int64_t t0, int len, int base,
+                                         int n, bool rev, int dim, int c0, A lam, A scale, int sign) {
+    constexpr int VN = VecOf<T>::N;
+    const int cols = min(PITCH, dim - c0);  // a multiple of 8
+    const int per = cols / VN;
+    for (int i = threadIdx.x; i < n * heads * per; i += REC_NT) {
+        const int row = i / per, c = (i - row * per) * VN;
+        const int tau = row / heads, g = row - tau * heads;
+        const int64_t t = t0 + (rev ? len - 1 - base - tau : base + tau);
+        const T* src = static_cast<const T*>(X.p) + t * X.ts + (int64_t)(h * heads + g) * X.hs + c0 + c;
+        const Pack<T, VN> v = *reinterpret_cast<const Pack<T, VN>*>(src);
+        const A w = sign == 0 ? scale : scale * decay(lam, (A)(sign * (n - 1 - tau)));
+#pragma unroll
+        for (int e = 0; e < VN; ++e) dst[row * PITCH + c + e] = to_acc<A, T>(v.v[e]) * w;
+    }
+}
+
+template <typename A, int RPT>
+__device__ __forceinline__ void rec_state_io(A (&S)[RPT][4], const LinRole& R, A* mem, int64_t at, int rg, int col,
+                                             bool store) {
+    const int64_t ri = R.transposed ? 1 : R.dv, ci = R.transposed ? R.dk : 1;
+    A* p = mem + at * R.dk * R.dv;
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int i = (r / 4) * 32 + rg * 4 + (r % 4), j = col + c;
+            if (i < R.dk && j < R.dv) {
+                if (store) p[i * ri + j * ci] = S[r][c];
+                else S[r][c] = p[i * ri + j * ci];
+            }
+        }
+}
+
+// READ 0: states only; 1: outputs; 2: the decay's derivative.  DER: also run the
+// states' derivative in lam, W_t = e^lam (W_{t-1} + S_{t-1}).
+template <typename T, int RPT, int READ, bool DER>
+__global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs P) {
+    using A = typename AccOf<T>::A;
+    constexpr int DKP = RPT * 8;
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    A* ks = reinterpret_cast<A*>(smem_raw);
+    A* vs = ks + REC_ROWS * DKP;
+    A* qs = vs + REC_ROWS * REC_COLS;
+    A* os = qs + (READ ? REC_ROWS * DKP : 0);  // outputs, or their cotangents
+    const LinRole& R = P.R;
+    const int slot = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * REC_COLS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int rg = lane & 7, cl = warp * 16 + (lane >> 3) * 4, col = c0 + cl;
+    int seq, len;
+    int64_t t0;
+    const bool used = P.S.find(slot, &seq, &t0, &len);
+    if (READ == 2 && !used && threadIdx.x == 0)
+        P.part[((int64_t)slot * P.H + h) * gridDim.z + blockIdx.z] = 0.0;
+    if (!used) return;
+    const A lam = clamp_lam(static_cast<const A*>(P.lam)[h]);
+    const int heads = R.nq > R.nk ? R.nq : R.nk;
+    int nb = REC_ROWS / heads;
+    const A al = lam < 0 ? -lam : lam;
+    if (al * nb > (A)4) nb = max(1, (int)((A)4 / al));
+
+    for (int i = threadIdx.x; i < REC_ROWS * DKP; i += REC_NT) {  // rows past dk stay 0
+        ks[i] = 0;
+        if (READ) qs[i] = 0;
+    }
+    for (int i = threadIdx.x; i < REC_ROWS * REC_COLS; i += REC_NT) {
+        vs[i] = 0;
+        if (READ == 2) os[i] = 0;
+    }
+    A S[RPT][4], W[DER ? RPT : 1][4];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            S[r][c] = 0;
+            if constexpr (DER) W[r][c] = 0;
+        }
+    const int64_t by_slot = (int64_t)slot * P.H + h, by_seq = (int64_t)seq * P.H + h;
+    if (R.state_in)
+        rec_state_io<A, RPT>(S, R, (A*)const_cast<void*>(R.state_in), R.in_by_slot ? by_slot : by_seq, rg, col, false);
+    if constexpr (DER)
+        if (P.w_in) rec_state_io<A, RPT>(W, R, (A*)const_cast<void*>(P.w_in), by_slot, rg, col, false);
+    A dsum = 0;
+    const bool rev = R.reverse;
+    for (int base = 0; base < len; base += nb) {
+        const int n = min(nb, len - base);
+        __syncthreads();  // the last block's rows have been read
+        rec_load<T, A, DKP>(ks, R.k, R.nk, h, t0, len, base, n, rev, R.dk, 0, lam, (A)R.sk, 1);
+        rec_load<T, A, REC_COLS>(vs, R.v, R.nk, h, t0, len, base, n, rev, R.dv, c0, lam, (A)1, 0);
+        if constexpr (READ != 0) rec_load<T, A, DKP>(qs, R.q, R.nq, h, t0, len, base, n, rev, R.dk, 0, lam, (A)R.sq, -1);
+        if constexpr (READ == 2)
+            rec_load<T, A, REC_COLS>(os, P.dout, R.nq, h, t0, len, base, n, rev, R.dv, c0, lam, (A)1, 0);
+        __syncthreads();
+        const A pre = decay(lam, (A)(rev ? n - 1 : n));
+#pragma unroll
+        for (int r = 0; r < RPT; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                S[r][c] *= pre;
+                if constexpr (DER) W[r][c] *= pre;
+            }
+        for (int tau = 0; tau < n; ++tau) {
+            if constexpr (DER) {
+#pragma unroll
+                for (int r = 0; r < RPT; ++r)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) W[r][c] += S[r][c];
+            }
+            for (int g = 0; g < R.nk; ++g) {
+                const A* kr = ks + (tau * R.nk + g) * DKP;
+                const A* vr = vs + (tau * R.nk + g) * REC_COLS + cl;
+                const Pack<A, 4> vv = *reinterpret_cast<const Pack<A, 4>*>(vr);
+#pragma unroll
+                for (int m = 0; m < RPT / 4; ++m) {
+                    const Pack<A, 4> kk = *reinterpret_cast<const Pack<A, 4>*>(kr + m * 32 + rg * 4);
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) S[m * 4 + r][c] = dfma(kk.v[r], vv.v[c], S[m * 4 + r][c]);
+                }
+            }
+            if constexpr (READ != 0) {
+                for (int g = 0; g < R.nq; ++g) {
+                    const int row = tau * R.nq + g;
+                    const A* qr = qs + row * DKP;
+                    A p[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int m = 0; m < RPT / 4; ++m) {
+                        const Pack<A, 4> qq = *reinterpret_cast<const Pack<A, 4>*>(qr + m * 32 + rg * 4);
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                if constexpr (READ == 2) p[c] = dfma(qq.v[r], W[m * 4 + r][c], p[c]);
+                                else p[c] = dfma(qq.v[r], S[m * 4 + r][c], p[c]);
+                            }
+                    }
+                    if constexpr (READ == 2) {
+                        const Pack<A, 4> d = *reinterpret_cast<const Pack<A, 4>*>(os + row * REC_COLS + cl);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) dsum = dfma(d.v[c], p[c], dsum);
+                    } else {
+                        // sum over the 8 row groups (lane bits 0-2), halving the columns kept at each step
+                        const bool b0 = lane & 1, b1 = lane & 2;
+                        A u0 = b0 ? p[2] : p[0], u1 = b0 ? p[3] : p[1];
+                        u0 += __shfl_xor_sync(FULL, b0 ? p[0] : p[2], 1);
+                        u1 += __shfl_xor_sync(FULL, b0 ? p[1] : p[3], 1);
+                        A w = b1 ? u1 : u0;
+                        w += __shfl_xor_sync(FULL, b1 ? u0 : u1, 2);
+                        w += __shfl_xor_sync(FULL, w, 4);
+                        if (rg < 4) os[row * REC_COLS + cl + (b0 ? 2 : 0) + (b1 ? 1 : 0)] = w;
+                    }
+                }
+            }
+        }
+        if (rev) {
+            const A post = decay(lam, (A)1);
+#pragma unroll
+            for (int r = 0; r < RPT; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) S[r][c] *= post;
+        }
+        if constexpr (READ == 1) {
+            __syncthreads();
+            const int cols = min(REC_COLS, R.dv - c0);
+            for (int i = threadIdx.x; i < n * R.nq * REC_COLS; i += REC_NT) {
+                const int row = i / REC_COLS, c = i - row * REC_COLS;
+                if (c >= cols) continue;
+                const int tau = row / R.nq, g = row - tau * R.nq;
+                const int64_t t = t0 + (rev ? len - 1 - base - tau : base + tau);
+                static_cast<T*>(R.o)[t * R.o_ts + (int64_t)(h * R.nq + g) * R.o_hs + c0 + c] = from_acc<T, A>(os[i]);
+            }
+        }
+    }
+    if (R.state_out)
+        rec_state_io<A, RPT>(S, R, (A*)R.state_out, R.out_by_slot ? by_slot : by_seq, rg, col, true);
+    if constexpr (DER && READ == 0) rec_state_io<A, RPT>(W, R, (A*)R.w_out, by_slot, rg, col, true);
+    if constexpr (READ == 2) {
+        // the last segment of a sequence: <dstate, W_last>
+        const bool last = t0 + len >= P.S.at(seq + 1);
+        if (P.dstate && last) {
+            A D[RPT][4];
+#pragma unroll
+            for (int r = 0; r < RPT; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) D[r][c] = 0;
+            rec_state_io<A, RPT>(D, R, (A*)const_cast<void*>(P.dstate), by_seq, rg, col, false);
+#pragma unroll
+            for (int r = 0; r < RPT; ++r)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) dsum = dfma(D[r][c], W[r][c], dsum);
+        }
+        double* red = reinterpret_cast<double*>(smem_raw);
+        __syncthreads();
+        red[threadIdx.x] = (double)dsum;
+        __syncthreads();
+        for (int s = REC_NT / 2; s > 0; s >>= 1) {  // a fixed order: the result does not vary from run to run
+            if ((int)threadIdx.x < s) red[threadIdx.x] += red[threadIdx.x + s];
+            __syncthreads();
+        }
+        if (threadIdx.x == 0) P.part[by_slot * gridDim.z + blockIdx.z] = red[0];
+    }
+}
+
+// dlam[h]: the blocks' sums of head h, in a fixed order
+template <typename A>
+__global__ void __launch_bounds__(256) k_dlam_join(const double* __restrict__ part, int64_t slots, int H, int cb,
+                                                   A* __restrict__ dlam) {
+    __shared__ double red[256];
+    const int h = blockIdx.x;
+    double s = 0;
+    for (int64_t i = threadIdx.x; i < slots * cb; i += 256) s += part[(i / cb * H + h) * cb + i % cb];
+    red[threadIdx.x] = s;
+    __syncthreads();
+    for (int w = 128; w > 0; w >>= 1) {
+        if ((int)threadIdx.x < w) red[threadIdx.x] += red[threadIdx.x + w];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) dlam[h] = (A)red[0];
+}
+
+// States before each segment from the segments' own: per element a serial walk
+// over the segments of a sequence, four segments' loads in flight.
+//     X_in(j + 1) = e^{lam len_j} X_in(j) + X_j            (reverse: towards smaller j)
+//     W_in(j + 1) = e^{lam len_j} (W_in(j) + len_j X_in(j)) + W_j
+// Bound by its traffic: each segment's state is read and written once.
+template <typename A, bool DER>
+__global__ void __launch_bounds__(256) k_carry(const __grid_constant__ LinCarry C) {
+    const int seq = blockIdx.y, h = blockIdx.z;
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= C.len) return;
+    const A lam = clamp_lam(static_cast<const A*>(C.lam)[h]);
+    const int64_t total = C.S.at(seq + 1) - C.S.at(seq);
+    int64_t count = total <= 0 ? 1 : (total + C.S.seg - 1) / C.S.seg;
+    const int s0 = C.S.first_slot(seq);
+    if (count > C.S.slots - s0) count = C.S.slots - s0;  // (bounds that do not ascend)
+    const int64_t by_seq = ((int64_t)seq * C.H + h) * C.len + e;
+    A x = C.init ? static_cast<const A*>(C.init)[by_seq] : (A)0, w = 0;
+    const A full = decay(lam, (A)C.S.seg), part = decay(lam, (A)(total - (count - 1) * C.S.seg));
+    A* st = static_cast<A*>(C.states);
+    A* wt = static_cast<A*>(C.w);
+    constexpr int U = 4;
+    for (int64_t i0 = 0; i0 < count; i0 += U) {
+        A own[U], wown[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + u;
+            const int64_t j = C.reverse ? count - 1 - i : i;
+            const int64_t at = ((int64_t)(s0 + j) * C.H + h) * C.len + e;
+            own[u] = i < count ? st[at] : (A)0;
+            wown[u] = DER && i < count ? wt[at] : (A)0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = i0 + u;
+            if (i >= count) break;
+            const int64_t j = C.reverse ? count - 1 - i : i;
+            const int64_t at = ((int64_t)(s0 + j) * C.H + h) * C.len + e;
+            const A d = j == count - 1 ? part : full;
+            const A n = (A)(j == count - 1 ? total - (count - 1) * C.S.seg : (int64_t)C.S.seg);
+            st[at] = x;
+            if constexpr (DER) {
+                wt[at] = w;
+                w = dfma(d, dfma(n, x, w), wown[u]);
+            }
+            x = dfma(d, x, own[u]);
+        }
+    }
+    if (C.last) static_cast<A*>(C.last)[by_seq] = x;
+}
+
+// ---------------------------------------------------------------- host side
+
+// Tokens per segment.  Enough blocks for two rounds of the resident ones (148
+// SMs x 4); not under 256 tokens, below which the extra pass over k and v and
+// the states' traffic cost more than they spread.  Sequences of one known length
+// that fill the GPU by themselves are not cut.
+int rec_segment(int64_t T, int N, int H, int dv, bool equal) {
+    const int64_t cb = (dv + REC_COLS - 1) / REC_COLS;
+    const int64_t whole = std::max<int64_t>(T, 1) + 1;
+    if (equal && (int64_t)N * H * cb >= 592) return (int)std::min<int64_t>(whole, INT32_MAX);
+    int64_t seg = (T * H * cb / 1184 + 63) / 64 * 64;
+    seg = std::max<int64_t>(seg, 256);
+    return (int)std::min<int64_t>(seg >= T ? whole : seg, INT32_MAX);
+}
+
+template <typename T, int RPT, int READ, bool DER>
+static cudaError_t rec_launch(const RecArgs& P, cudaStream_t st) {
+    using A = typename AccOf<T>::A;
+    constexpr auto kern = k_rec<T, RPT, READ, DER>;
+    constexpr size_t smem = sizeof(A) * REC_ROWS * (RPT * 8 * (READ ? 2 : 1) + REC_COLS * (READ ? 2 : 1));
+    int dev = 0, sms = 0, per = 0;
+    cudaError_t e = current_device_sms(&dev, &sms);
+    if (e == cudaSuccess) e = blocks_per_sm<kern>(dev, REC_NT, smem, &per);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)P.S.slots, (unsigned)P.H, (unsigned)((P.R.dv + REC_COLS - 1) / REC_COLS));
+    if (grid.x == 0) return cudaSuccess;
+    kern<<<grid, REC_NT, smem, st>>>(P);
+    return cudaGetLastError();
+}
+
+template <typename T, int READ, bool DER>
+static cudaError_t rec_dim(const RecArgs& P, cudaStream_t st) {
+    return P.R.dk <= 64 ? rec_launch<T, 8, READ, DER>(P, st) : rec_launch<T, 16, READ, DER>(P, st);
+}
+
+template <typename F>
+static cudaError_t with_type(laplex_dtype dt, F f) {
+    switch (dt) {
+        case LAPLEX_F32: return f(float());
+        case LAPLEX_F64: return f(double());
+        case LAPLEX_F16: return f(__half());
+        case LAPLEX_BF16: return f(__nv_bfloat16());
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t rec_run(laplex_dtype dt, const LinRole& R, const LinSeqs& S, int H, const void* lam, bool state_only,
+                    cudaStream_t st) {
+    RecArgs P = {};
+    P.R = R;
+    P.S = S;
+    P.H = H;
+    P.lam = lam;
+    return with_type(dt, [&](auto t) {
+        using T = decltype(t);
+        return state_only ? rec_dim<T, 0, false>(P, st) : rec_dim<T, 1, false>(P, st);
+    });
+}
+
+cudaError_t carry_run(laplex_dtype dt, const LinCarry& C, cudaStream_t st) {
+    if (C.S.N == 0 || C.H == 0) return cudaSuccess;
+    // sequences ride in grid.y (at most 65535): the C boundary checks their number
+    const dim3 grid((unsigned)((C.len + 255) / 256), (unsigned)C.S.N, (unsigned)C.H);
+    if (dt == LAPLEX_F64) {
+        if (C.w) k_carry<double, true><<<grid, 256, 0, st>>>(C);
+        else k_carry<double, false><<<grid, 256, 0, st>>>(C);
+    } else {
+        if (C.w) k_carry<float, true><<<grid, 256, 0, st>>>(C);
+        else k_carry<float, false><<<grid, 256, 0, st>>>(C);
+    }
+    return cudaGetLastError();
+}
+
+static LinSeqs dlam_seqs(int64_t T, int N, const int32_t* cu, int Hkv, int dv) {
+    LinSeqs S;
+    S.cu = cu;
+    S.T = T;
+    S.N = N;
+    S.seg = rec_segment(T, N, Hkv, dv, cu == nullptr);
+    S.slots = (int)(T / S.seg) + N;
+    return S;
+}
+
+size_t dlam_ws_bytes(laplex_dtype dt, int64_t T, int N, int Hkv, int dk, int dv, bool equal) {
+    const int seg = rec_segment(T, N, Hkv, dv, equal);
+    const int64_t slots = T / seg + N;
+    const int64_t cb = (dv + REC_COLS - 1) / REC_COLS;
+    const size_t part = (size_t)((slots * Hkv * cb * 8 + 255) / 256 * 256);
+    if (seg > T) return part;
+    return part + 2 * (size_t)((slots * Hkv * dk * dv * (int64_t)acc_bytes(dt) + 255) / 256 * 256);
+}
+
+cudaError_t dlam_run(laplex_dtype dt, LinRole fwd, LinRows dout, LinSeqs S0, int H, const void* lam,
+                     const void* state, const void* dstate, void* dlam, void* ws, size_t ws_bytes, cudaStream_t st) {
+    const LinSeqs S = dlam_seqs(S0.T, S0.N, S0.cu, H, fwd.dv);
+    const int cb = (fwd.dv + REC_COLS - 1) / REC_COLS;
+    const size_t need = dlam_ws_bytes(dt, S.T, S.N, H, fwd.dk, fwd.dv, S.cu == nullptr);
+    if (ws_bytes < need) return cudaErrorInvalidValue;
+    char* base = static_cast<char*>(ws);
+    RecArgs P = {};
+    P.S = S;
+    P.H = H;
+    P.lam = lam;
+    P.part = reinterpret_cast<double*>(base);
+    base += ((size_t)S.slots * H * cb * 8 + 255) / 256 * 256;
+    P.R = fwd;
+    P.R.state_in = state;
+    P.R.in_by_slot = 0;
+    P.R.state_out = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (S.seg <= S.T) {
+        const size_t sb = ((size_t)S.slots * H * fwd.dk * fwd.dv * acc_bytes(dt) + 255) / 256 * 256;
+        RecArgs Q = P;
+        Q.R.state_in = nullptr;
+        Q.R.state_out = base;
+        Q.R.out_by_slot = 1;
+        Q.R.w_out = base + sb;
+        e = with_type(dt, [&](auto t) { return rec_dim<decltype(t), 0, true>(Q, st); });
+        if (e != cudaSuccess) return e;
+        LinCarry C = {};
+        C.S = S;
+        C.H = H;
+        C.len = (int64_t)fwd.dk * fwd.dv;
+        C.lam = lam;
+        C.init = state;
+        C.states = base;
+        C.w = base + sb;
+        if ((e = carry_run(dt, C, st)) != cudaSuccess) return e;
+        P.R.state_in = base;
+        P.R.in_by_slot = 1;
+        P.w_in = base + sb;
+    }
+    P.dout = dout;
+    P.dstate = dstate;
+    e = with_type(dt, [&](auto t) { return rec_dim<decltype(t), 2, true>(P, st); });
+    if (e != cudaSuccess) return e;
+    if (dt == LAPLEX_F64) k_dlam_join<double><<<H, 256, 0, st>>>(P.part, S.slots, H, cb, (double*)dlam);
+    else k_dlam_join<float><<<H, 256, 0, st>>>(P.part, S.slots, H, cb, (float*)dlam);
+    return cudaGetLastError();
+}
+
+}  // namespace lx

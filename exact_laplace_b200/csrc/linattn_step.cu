@@ -1,0 +1,169 @@
+// linattn_step.cu -- decayed linear attention for one token per row, against a
+// cache of states updated in place:
+//     S <- e^lam S + k v^T,      o = scale S^T q.
+//
+// Bound by memory: a state of dk dv values is read and written once (8 dk dv
+// bytes in fp32), against 3 + 2 (q-heads per state) flops a value.  A block
+// holds a [dk, TC] piece of one state in registers: all of its loads are in
+// flight before the first is used, and the state is not read again for the
+// outputs.  TC = 128 columns (32 lanes x 16 bytes) where there are enough blocks
+// to fill the GPU, 32 where there are few, so that one token's states spread
+// over more SMs.
+#include <algorithm>
+
+#include "devcache.h"
+#include "elem.cuh"
+#include "seqop.h"
+
+namespace lx {
+
+constexpr int STEP_NT = 256;
+constexpr int STEP_GB = 4;  // q-heads whose partial sums are joined at a time
+constexpr int STEP_DK = 128;
+
+// LANES lanes across the columns, STEP_NT / LANES row groups
+template <typename T, int LANES>
+__global__ void __launch_bounds__(STEP_NT) k_step(const __grid_constant__ LinStep P) {
+    using A = typename AccOf<T>::A;
+    constexpr int VN = 16 / (int)sizeof(A), TC = LANES * VN, RG = STEP_NT / LANES, RPT = STEP_DK / RG;
+    constexpr int NW = STEP_NT / 32;
+    __shared__ A ks[STEP_DK], qs[STEP_GB][STEP_DK], vs[TC];
+    __shared__ __align__(16) A red[STEP_GB][NW][TC];
+    __shared__ int next;
+    const int tid = threadIdx.x, h = blockIdx.y, c0 = blockIdx.z * TC;
+    const int lane = tid % LANES, rg = tid / LANES, col = c0 + lane * VN;
+    const bool in = col < P.dv;  // dv is a multiple of 8: a thread's columns are all in or all out
+    int64_t row = blockIdx.x;
+    int64_t slot = row;
+    if (P.slot) slot = P.slot[row];
+    const int G = P.hq / P.hkv;
+    if (slot < 0 || slot >= P.slots) {  // no state: a row of zeros
+        for (int g = 0; g < G; ++g)
+            for (int c = c0 + tid; c < min(P.dv, c0 + TC); c += STEP_NT)
+                static_cast<T*>(P.o)[row * P.o_ts + (int64_t)(h * G + g) * P.o_hs + c] = from_acc<T, A>((A)0);
+        return;
+    }
+    A* st = static_cast<A*>(P.states) + ((slot * P.hkv + h) * P.dk) * (int64_t)P.dv + col;
+    Pack<A, VN> S[RPT];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+        const int i = r * RG + rg;
+#pragma unroll
+        for (int c = 0; c < VN; ++c) S[r].v[c] = 0;
+        if (in && i < P.dk) S[r] = *reinterpret_cast<const Pack<A, VN>*>(st + (int64_t)i * P.dv);
+    }
+    // Rows that name one slot are applied in row order: the first one's block
+    // takes them all, the others leave.
+    if (P.slot) {
+        int earlier = 0;
+        for (int64_t m = tid; m < row; m += STEP_NT) earlier |= P.slot[m] == (int32_t)slot;
+        if (__syncthreads_or(earlier)) return;
+    }
+    // e^lam as a sum of two values: rounded once to fp32, its error would add
+    // up over the tokens that a slow decay remembers
+    const double g2 = decay((double)clamp_lam(static_cast<const A*>(P.lam)[h]), 1.0);
+    const A ghi = (A)g2, glo = (A)(g2 - (double)ghi);
+    const A scale = (A)P.scale;
+    while (true) {
+        for (int i = tid; i < STEP_DK; i += STEP_NT)
+            ks[i] = i < P.dk ? to_acc<A, T>(static_cast<const T*>(P.k.p)[row * P.k.ts + (int64_t)h * P.k.hs + i]) : (A)0;
+        for (int i = tid; i < TC; i += STEP_NT)
+            vs[i] = c0 + i < P.dv ? to_acc<A, T>(static_cast<const T*>(P.v.p)[row * P.v.ts + (int64_t)h * P.v.hs + c0 + i])
+                                  : (A)0;
+        if (tid == 0) next = INT32_MAX;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < RPT; ++r) {
+            const A kk = ks[r * RG + rg];
+#pragma unroll
+            for (int c = 0; c < VN; ++c)
+                S[r].v[c] = dfma(ghi, S[r].v[c], dfma(glo, S[r].v[c], kk * vs[lane * VN + c]));
+        }
+        for (int g0 = 0; g0 < G; g0 += STEP_GB) {
+            const int gn = min(STEP_GB, G - g0);
+            for (int i = tid; i < gn * STEP_DK; i += STEP_NT) {
+                const int g = i / STEP_DK, c = i % STEP_DK;
+                qs[g][c] = c < P.dk ? to_acc<A, T>(static_cast<const T*>(
+                                          P.q.p)[row * P.q.ts + (int64_t)(h * G + g0 + g) * P.q.hs + c])
+                                    : (A)0;
+            }
+            __syncthreads();
+            for (int g = 0; g < gn; ++g) {
+                A p[VN];
+#pragma unroll
+                for (int c = 0; c < VN; ++c) p[c] = 0;
+#pragma unroll
+                for (int r = 0; r < RPT; ++r) {
+                    const A qq = qs[g][r * RG + rg];
+#pragma unroll
+                    for (int c = 0; c < VN; ++c) p[c] = dfma(qq, S[r].v[c], p[c]);
+                }
+                if constexpr (LANES < 32) {  // the row groups inside the warp
+#pragma unroll
+                    for (int s = LANES; s < 32; s <<= 1)
+#pragma unroll
+                        for (int c = 0; c < VN; ++c) p[c] += __shfl_xor_sync(FULL, p[c], s);
+                }
+                if (tid % 32 < LANES) {
+#pragma unroll
+                    for (int c = 0; c < VN; ++c) red[g][tid / 32][lane * VN + c] = p[c];
+                }
+            }
+            __syncthreads();
+            for (int i = tid; i < gn * TC; i += STEP_NT) {
+                const int g = i / TC, c = i % TC;
+                A s = 0;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) s += red[g][w][c];
+                if (c0 + c < P.dv)
+                    static_cast<T*>(P.o)[row * P.o_ts + (int64_t)(h * G + g0 + g) * P.o_hs + c0 + c] =
+                        from_acc<T, A>(s * scale);
+            }
+        }
+        if (!P.slot) break;
+        int mine = INT32_MAX;
+        for (int64_t m = row + 1 + tid; m < P.rows; m += STEP_NT)
+            if (P.slot[m] == (int32_t)slot) { mine = (int)m; break; }
+        if (!__syncthreads_or(mine != INT32_MAX)) break;
+        if (mine != INT32_MAX) atomicMin(&next, mine);
+        __syncthreads();
+        row = next;
+        __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+        const int i = r * RG + rg;
+        if (in && i < P.dk) *reinterpret_cast<Pack<A, VN>*>(st + (int64_t)i * P.dv) = S[r];
+    }
+}
+
+template <typename T>
+static cudaError_t step_launch(const LinStep& P, cudaStream_t st) {
+    using A = typename AccOf<T>::A;
+    constexpr int VN = 16 / (int)sizeof(A);
+    int dev = 0, sms = 0;
+    cudaError_t e = current_device_sms(&dev, &sms);
+    if (e != cudaSuccess) return e;
+    const int64_t wide = P.rows * P.hkv * ((P.dv + 32 * VN - 1) / (32 * VN));
+    if (wide >= 2 * sms) {
+        const dim3 grid((unsigned)P.rows, (unsigned)P.hkv, (unsigned)((P.dv + 32 * VN - 1) / (32 * VN)));
+        k_step<T, 32><<<grid, STEP_NT, 0, st>>>(P);
+    } else {
+        const dim3 grid((unsigned)P.rows, (unsigned)P.hkv, (unsigned)((P.dv + 8 * VN - 1) / (8 * VN)));
+        k_step<T, 8><<<grid, STEP_NT, 0, st>>>(P);
+    }
+    return cudaGetLastError();
+}
+
+cudaError_t step_run(laplex_dtype dt, const LinStep& P, cudaStream_t st) {
+    if (P.rows == 0) return cudaSuccess;
+    switch (dt) {
+        case LAPLEX_F32: return step_launch<float>(P, st);
+        case LAPLEX_F64: return step_launch<double>(P, st);
+        case LAPLEX_F16: return step_launch<__half>(P, st);
+        case LAPLEX_BF16: return step_launch<__nv_bfloat16>(P, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace lx

@@ -37,6 +37,7 @@
 #include "common.cuh"
 #include "devcache.h"
 #include "laplex_impl.h"
+#include "seqop.h"
 
 // ranking of equal digits in a warp: 0 = warp match, 1 = eight ballots,
 // 3 = shared-memory match masks; 2 = chosen per pass from the digit histogram
@@ -1079,6 +1080,46 @@ cudaError_t permute_run(const V* src, const int32_t* idx, int64_t n, V* dst, voi
     };
     return vio ? place(std::integral_constant<decltype(&k_place_group<V, GB, true>), &k_place_group<V, GB, true>>{})
                : place(std::integral_constant<decltype(&k_place_group<V, GB, false>), &k_place_group<V, GB, false>>{});
+}
+
+// -------------------------------------------------------------- integer keys
+// Stable ascending order of n keys in [0, top] with their positions: the digit
+// passes over the bytes that `top` has, without a key map.
+size_t sort_keys_ws_bytes(int64_t n) {
+    const int64_t ntiles = std::max<int64_t>(1, (n + sort_tile<float>() - 1) / sort_tile<float>());
+    return 2 * Carve::need((size_t)n, 4) + pass_ws_bytes(ntiles);
+}
+
+cudaError_t sort_keys_run(const uint32_t* keys, int64_t n, uint32_t top, uint32_t* skeys, int32_t* perm, void* ws,
+                          size_t ws_bytes, uint32_t* status, cudaStream_t st) {
+    if (n == 0) return cudaSuccess;
+    constexpr int KPT = SortShape<float>::KPT, S = SortShape<float>::S;
+    const int64_t ntiles = (n + sort_tile<float>() - 1) / sort_tile<float>();
+    Carve cv(ws, ws_bytes);
+    uint32_t* kws = cv.take<uint32_t>(n);
+    int32_t* vws = cv.take<int32_t>(n);
+    const PassWs W = pass_carve(cv, ntiles);
+    if (!cv.ok) return cudaErrorInvalidValue;
+    int dev = 0, sms = 0;
+    cudaError_t e = current_device_sms(&dev, &sms);
+    if (e != cudaSuccess) return e;
+    int P = 1;
+    while (P < 4 && (top >> (8 * P)) != 0) ++P;
+    const uint32_t* ksrc = keys;
+    const int32_t* vsrc = nullptr;
+    for (int pass = 0; pass < P; ++pass) {
+        const bool to_out = ((P - 1 - pass) % 2) == 0;  // the last pass lands in the outputs
+        uint32_t* kdst = to_out ? skeys : kws;
+        int32_t* vdst = to_out ? perm : vws;
+        if (pass == 0)
+            e = digit_pass<uint32_t, int32_t, KPT, S, F_IOTA>(ksrc, vsrc, kdst, vdst, n, 0, W, status, dev, sms, st);
+        else
+            e = digit_pass<uint32_t, int32_t, KPT, S, 0>(ksrc, vsrc, kdst, vdst, n, 8 * pass, W, status, dev, sms, st);
+        if (e != cudaSuccess) return e;
+        ksrc = kdst;
+        vsrc = vdst;
+    }
+    return cudaSuccess;
 }
 
 template cudaError_t permute_run<int32_t>(const int32_t*, const int32_t*, int64_t, int32_t*, void*, size_t,

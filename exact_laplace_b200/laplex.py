@@ -12,9 +12,11 @@ path a user without device buffers takes).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -23,9 +25,11 @@ LIB_PATH = os.path.join(_HERE, "liblaplex.so")
 
 OK, EINVAL, ENONFINITE, EWORKSPACE, ECUDA, ETIMEOUT = range(6)
 BUILD_ACCURATE_EXP = 1  # laplex_build_flags() bit
-F32, F64 = 0, 1
+F32, F64, F16, BF16 = range(4)
 (OP_SORT, OP_SYM, OP_GENERAL, OP_PHASED, OP_GRAM, OP_BACKWARD, OP_BACKWARD_GENERAL, OP_GRAM_MATRIX,
  OP_BACKWARD_PHASED, OP_PERMUTE, OP_SYM_PLANNED, OP_SORT_CARRY, OP_SYM_UNSORTED) = range(13)
+
+LINATTN_FORWARD, LINATTN_BACKWARD, LINATTN_BACKWARD_DECAY = range(3)
 
 _lib = None
 _lock = threading.Lock()
@@ -42,6 +46,22 @@ class LaplexError(RuntimeError):
 _STATUS_NAMES = {OK: "LAPLEX_OK", EINVAL: "LAPLEX_EINVAL", ENONFINITE: "LAPLEX_ENONFINITE",
                  EWORKSPACE: "LAPLEX_EWORKSPACE", ECUDA: "LAPLEX_ECUDA",
                  ETIMEOUT: "LAPLEX_ETIMEOUT"}
+
+
+class _Rows(ctypes.Structure):
+    """laplex_rows"""
+    _fields_ = [("ptr", _P), ("token_stride", _I64), ("head_stride", _I64)]
+
+
+class _LinattnShape(ctypes.Structure):
+    """laplex_linattn_shape"""
+    _fields_ = [("tokens", _I64), ("seqs", _I64), ("cu_seqlens", _P), ("hq", ctypes.c_int32), ("hkv", ctypes.c_int32),
+                ("dk", ctypes.c_int32), ("dv", ctypes.c_int32), ("log_decay", _P), ("scale", ctypes.c_double),
+                ("dtype", ctypes.c_int)]
+
+
+_R = ctypes.POINTER(_Rows)
+_S = ctypes.POINTER(_LinattnShape)
 
 #: every symbol include/laplex.h declares, with its ctypes signature
 SIGNATURES = {
@@ -81,6 +101,17 @@ SIGNATURES = {
                                   ctypes.c_int),
     "laplex_matvec_sym_unsorted": ([_P, _P, _I64, ctypes.c_int, _P, _P, _P, _P, ctypes.c_size_t, _P],
                                    ctypes.c_int),
+    "laplex_linattn_workspace_size": ([_S, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)], ctypes.c_int),
+    "laplex_linattn": ([_S, _R, _R, _R, _P, _R, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
+    "laplex_linattn_backward": ([_S, _R, _R, _R, _R, _P, _P, _R, _R, _R, _P, _P, _P, ctypes.c_size_t, _P],
+                                ctypes.c_int),
+    "laplex_linattn_step": ([_S, _R, _R, _R, _P, _I64, _P, _R, _P], ctypes.c_int),
+    "laplex_embed": ([_P, _I64, _I64, _I64, _P, ctypes.c_int, _I64, ctypes.c_double, _P, _I64, ctypes.c_int, _P],
+                     ctypes.c_int),
+    "laplex_embed_backward_workspace_size": ([_I64, _I64, _I64, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)],
+                                             ctypes.c_int),
+    "laplex_embed_backward": ([_P, ctypes.c_int, _I64, _P, _I64, _I64, _I64, ctypes.c_double, ctypes.c_int, _P, _I64,
+                               ctypes.c_int, ctypes.c_int, _P, ctypes.c_size_t, _P], ctypes.c_int),
 }
 
 
@@ -438,6 +469,278 @@ def matvec_sym_noalloc(sorted_anchors: torch.Tensor, x: torch.Tensor, perm=None,
     _check(lib().laplex_matvec_sym_noalloc(_ptr(sorted_anchors), _ptr(perm), n, _ptr(x), _ptr(y),
                                            _stream(dev)))
     return y
+
+
+# ----------------------------------------------------------------------------- sequence operators
+
+_SEQ_DTYPES = {torch.float32: F32, torch.float64: F64, torch.float16: F16, torch.bfloat16: BF16}
+
+
+class LinattnGrads(NamedTuple):
+    """Gradients of linattn; dstate and dlog_decay are None where not asked for."""
+    dq: torch.Tensor
+    dk: torch.Tensor
+    dv: torch.Tensor
+    dstate: Optional[torch.Tensor]
+    dlog_decay: Optional[torch.Tensor]
+
+
+def _on(dev):
+    """The device of the tensors made current: the library works on the current one."""
+    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _seq_dt(*ts) -> int:
+    for t in ts:
+        if t is not None and t.dtype != ts[0].dtype:
+            raise LaplexError(EINVAL, f"rows of {ts[0].dtype} and of {t.dtype}")
+    if ts[0].dtype not in _SEQ_DTYPES:
+        raise LaplexError(EINVAL, f"dtype {ts[0].dtype} is not float16, bfloat16, float32 or float64")
+    return _SEQ_DTYPES[ts[0].dtype]
+
+
+def _seq_dev(*ts):
+    dev = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise LaplexError(EINVAL, "tensors must be on a CUDA device")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise LaplexError(EINVAL, "tensors are on different devices")
+    return dev
+
+
+def _packed(name, x):
+    """[tokens, heads, dim] of x, which may also be [seqs, length, heads, dim]."""
+    if x.dim() == 4:
+        n, m = x.shape[:2]
+        if n > 1 and m > 1 and x.stride(0) != m * x.stride(1):
+            raise LaplexError(EINVAL, f"{name}: the sequences of a 4-d tensor must follow one another")
+        step = x.stride(1) if m > 1 else x.stride(0)
+        x = x.as_strided((n * m,) + tuple(x.shape[2:]), (step,) + x.stride()[2:])
+    if x.dim() != 3:
+        raise LaplexError(EINVAL, f"{name} must be [tokens, heads, dim] or [seqs, length, heads, dim]")
+    if x.numel() and x.stride(2) != 1 and x.shape[2] > 1:
+        raise LaplexError(EINVAL, f"{name}: the last dimension must be contiguous")
+    return x
+
+
+def _rows(x):
+    return None if x is None else ctypes.byref(_Rows(x.data_ptr(), x.stride(0), x.stride(1)))
+
+
+def _like(x):
+    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+
+
+def _state(name, x, shape, dtype):
+    if x is not None:
+        if tuple(x.shape) != tuple(shape) or x.dtype != dtype or not x.is_contiguous():
+            raise LaplexError(EINVAL, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return x
+
+
+def _shape(q3, k3, v3, seqs, cu, log_decay, scale, dt):
+    """The checked laplex_linattn_shape of packed q, k, v."""
+    t, hq, dk = q3.shape
+    hkv, dv = k3.shape[1], v3.shape[2]
+    if k3.shape != (t, hkv, dk) or v3.shape != (t, hkv, dv):
+        raise LaplexError(EINVAL, f"shapes of q {tuple(q3.shape)}, k {tuple(k3.shape)} and v {tuple(v3.shape)}")
+    acc = torch.float64 if dt == F64 else torch.float32
+    if tuple(log_decay.shape) != (hkv,) or log_decay.dtype != acc or not log_decay.is_contiguous():
+        raise LaplexError(EINVAL, f"log_decay must be a contiguous {acc} tensor of {hkv} heads")
+    s = _LinattnShape(t, seqs, None if cu is None else cu.data_ptr(), hq, hkv, dk, dv, log_decay.data_ptr(),
+                      float(dk ** -0.5 if scale is None else scale), dt)
+    return s, acc
+
+
+def _seqs(q, cu):
+    if cu is None:
+        return q.shape[0] if q.dim() == 4 else 1
+    if cu.dtype != torch.int32 or cu.dim() != 1 or cu.numel() < 1 or not cu.is_contiguous():
+        raise LaplexError(EINVAL, "cu_seqlens must be a contiguous int32 tensor [seqs + 1]")
+    return cu.numel() - 1
+
+
+def _seq_ws(dev, nbytes):
+    """Workspace of a sequence operator: the stream's, or while a graph is captured
+    one of the graph's own memory (the stream's may be replaced by a larger one
+    while the graph lives, and two graphs may run at the same time)."""
+    if not torch.cuda.is_current_stream_capturing():
+        buf = Workspace.get(dev, nbytes)
+    else:
+        buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        _check(lib().laplex_workspace_init(_ptr(buf), nbytes, _stream(dev)))
+    return buf, buf.numel()
+
+
+def _linattn_ws(s, call, dev):
+    out = ctypes.c_size_t(0)
+    _check(lib().laplex_linattn_workspace_size(ctypes.byref(s), call, ctypes.byref(out)))
+    return _seq_ws(dev, out.value)
+
+
+def linattn(q, k, v, log_decay, scale=None, cu_seqlens=None, state=None, return_state=False, out=None,
+            state_out=None):
+    """Decayed linear attention: S_t = e^lam S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
+
+    q [tokens, hq, dk], k [tokens, hkv, dk], v [tokens, hkv, dv] (float16,
+    bfloat16, float32 or float64; slices with a contiguous last dimension are
+    taken as they are), or 4-d [seqs, length, heads, dim].  log_decay [hkv]:
+    lam, float32 (float64 for float64 rows).  cu_seqlens: int32 [seqs + 1], the
+    bounds of packed sequences; rows behind the last bound are left as they are
+    (unset where this call made the output).  state [seqs, hkv, dk, dv]: the
+    states before the first tokens.  scale: dk ** -0.5 by default.
+
+    Returns o, or (o, states behind the last tokens) with return_state or
+    state_out (which may be `state` itself)."""
+    dev = _seq_dev(q, k, v, log_decay, cu_seqlens, state, out, state_out)
+    seqs = _seqs(q, cu_seqlens)
+    q3, k3, v3 = _packed("q", q), _packed("k", k), _packed("v", v)
+    s, acc = _shape(q3, k3, v3, seqs, cu_seqlens, log_decay, scale, _seq_dt(q, k, v, out))
+    shape = (seqs, s.hkv, s.dk, s.dv)
+    _state("state", state, shape, acc)
+    _state("state_out", state_out, shape, acc)
+    with _on(dev):
+        if out is None:
+            out = torch.empty(tuple(q.shape[:-1]) + (s.dv,), dtype=q.dtype, device=dev)
+        elif tuple(out.shape) != tuple(q.shape[:-1]) + (s.dv,):
+            raise LaplexError(EINVAL, f"out must have the shape {tuple(q.shape[:-1]) + (s.dv,)}")
+        if return_state and state_out is None:
+            state_out = torch.empty(shape, dtype=acc, device=dev)
+        ws, nb = _linattn_ws(s, LINATTN_FORWARD, dev)
+        _check(lib().laplex_linattn(ctypes.byref(s), _rows(q3), _rows(k3), _rows(v3), _ptr(state),
+                                    _rows(_packed("out", out)), _ptr(state_out), _ptr(ws), nb, _stream(dev)))
+    return out if state_out is None else (out, state_out)
+
+
+def linattn_backward(q, k, v, log_decay, dout, scale=None, cu_seqlens=None, state=None, dstate=None,
+                     return_dstate=None, return_dlog_decay=False, out=None):
+    """Gradients of <dout, o> + <dstate, states behind the last tokens> of linattn.
+
+    Arguments as in linattn; dout [tokens, hq, dv], dstate [seqs, hkv, dk, dv] or
+    None (zero).  Returns LinattnGrads(dq, dk, dv, dstate, dlog_decay): dstate,
+    the gradient of `state`, where return_dstate is set (by default where `state`
+    is given), dlog_decay [hkv] where return_dlog_decay is set.  out: (dq, dk,
+    dv) to write into."""
+    dev = _seq_dev(q, k, v, log_decay, dout, cu_seqlens, state, dstate, *(out or ()))
+    seqs = _seqs(q, cu_seqlens)
+    q3, k3, v3, do3 = _packed("q", q), _packed("k", k), _packed("v", v), _packed("dout", dout)
+    s, acc = _shape(q3, k3, v3, seqs, cu_seqlens, log_decay, scale, _seq_dt(q, k, v, dout, *(out or ())))
+    if tuple(do3.shape) != (s.tokens, s.hq, s.dv):
+        raise LaplexError(EINVAL, f"dout must have the shape {(s.tokens, s.hq, s.dv)}")
+    shape = (seqs, s.hkv, s.dk, s.dv)
+    _state("state", state, shape, acc)
+    _state("dstate", dstate, shape, acc)
+    with _on(dev):
+        if out is None:
+            out = (_like(q), _like(k), _like(v))
+        elif any(a.shape != b.shape for a, b in zip(out, (q, k, v))):
+            raise LaplexError(EINVAL, "out must have the shapes of q, k and v")
+        dq, dk, dv = out
+        ds = None
+        if return_dstate or (return_dstate is None and state is not None):
+            ds = torch.empty(shape, dtype=acc, device=dev)
+        dl = torch.empty(s.hkv, dtype=acc, device=dev) if return_dlog_decay else None
+        ws, nb = _linattn_ws(s, LINATTN_BACKWARD_DECAY if return_dlog_decay else LINATTN_BACKWARD, dev)
+        _check(lib().laplex_linattn_backward(
+            ctypes.byref(s), _rows(q3), _rows(k3), _rows(v3), _rows(do3), _ptr(state), _ptr(dstate),
+            _rows(_packed("dq", dq)), _rows(_packed("dk", dk)), _rows(_packed("dv", dv)), _ptr(ds), _ptr(dl),
+            _ptr(ws), nb, _stream(dev)))
+    return LinattnGrads(dq, dk, dv, ds, dl)
+
+
+def linattn_step(q, k, v, log_decay, states, slots=None, scale=None, out=None):
+    """One token per row of linattn against a cache of states, updated in place.
+
+    q [rows, hq, dk], k [rows, hkv, dk], v [rows, hkv, dv]; states [num_slots,
+    hkv, dk, dv] (float32; float64 for float64 rows).  slots: int32 [rows], the
+    state of each row (None: row n uses state n); a row whose slot is outside
+    the cache gets zeros, rows that name one slot are applied in row order.
+    Returns o [rows, hq, dv]."""
+    dev = _seq_dev(q, k, v, log_decay, states, slots, out)
+    if q.dim() != 3:
+        raise LaplexError(EINVAL, "q must be [rows, heads, dim]")
+    q3, k3, v3 = _packed("q", q), _packed("k", k), _packed("v", v)
+    s, acc = _shape(q3, k3, v3, 1, None, log_decay, scale, _seq_dt(q, k, v, out))
+    if states.dim() != 4:
+        raise LaplexError(EINVAL, "states must be [num_slots, hkv, dk, dv]")
+    _state("states", states, (states.shape[0], s.hkv, s.dk, s.dv), acc)
+    if slots is not None and (slots.dtype != torch.int32 or tuple(slots.shape) != (s.tokens,) or not slots.is_contiguous()):
+        raise LaplexError(EINVAL, "slots must be a contiguous int32 tensor [rows]")
+    with _on(dev):
+        if out is None:
+            out = torch.empty((s.tokens, s.hq, s.dv), dtype=q.dtype, device=dev)
+        elif tuple(out.shape) != (s.tokens, s.hq, s.dv):
+            raise LaplexError(EINVAL, f"out must have the shape {(s.tokens, s.hq, s.dv)}")
+        _check(lib().laplex_linattn_step(ctypes.byref(s), _rows(q3), _rows(k3), _rows(v3), _ptr(states),
+                                         states.shape[0], _ptr(slots), _rows(_packed("out", out)), _stream(dev)))
+    return out
+
+
+def _tokens(tokens):
+    if tokens.dtype not in (torch.int32, torch.int64) or not tokens.is_contiguous():
+        raise LaplexError(EINVAL, "tokens must be a contiguous int32 or int64 tensor")
+    return tokens.element_size()
+
+
+def _table(name, x, dim=None):
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1) or (dim is not None and x.shape[1] != dim):
+        raise LaplexError(EINVAL, f"{name} must be 2-d with contiguous rows" + ("" if dim is None else f" of {dim}"))
+    return x.stride(0)
+
+
+def embed(table, tokens, scale=1.0, out=None):
+    """scale * table[tokens]: [*tokens.shape, dim]; a row of zeros for a token
+    outside the table (padding).  table [rows, dim] of float16, bfloat16,
+    float32 or float64; tokens int32 or int64."""
+    dev = _seq_dev(table, tokens, out)
+    dt, tb, ld = _seq_dt(table, out), _tokens(tokens), _table("table", table)
+    shape = tuple(tokens.shape) + (table.shape[1],)
+    with _on(dev):
+        if out is None:
+            out = torch.empty(shape, dtype=table.dtype, device=dev)
+        elif tuple(out.shape) != shape or (out.dim() != 2 and not out.is_contiguous()):
+            raise LaplexError(EINVAL, f"out must have the shape {shape}")
+        o2 = out if out.dim() == 2 else out.view(-1, table.shape[1])
+        _check(lib().laplex_embed(_ptr(table), ld, table.shape[0], table.shape[1], _ptr(tokens), tb, tokens.numel(),
+                                  float(scale), _ptr(o2), _table("out", o2), dt, _stream(dev)))
+    return out
+
+
+def embed_backward(tokens, g, rows, scale=1.0, out=None, accumulate=False, dtype=None):
+    """Gradient of embed in the table: [rows, dim] with scale times the sum of the
+    rows of g (summed in fp32, in order of their positions) that name each row.
+
+    g [*tokens.shape, dim].  out: a [rows, dim] tensor of g's type or float32 to
+    write, or with accumulate to add into (rows that no token names are then
+    left as they are); dtype: the type of a fresh one (g's by default)."""
+    dev = _seq_dev(tokens, g, out)
+    dt, tb = _seq_dt(g), _tokens(tokens)
+    if g.shape[:-1] != tokens.shape:
+        raise LaplexError(EINVAL, f"g must have the shape {tuple(tokens.shape)} + (dim,)")
+    if g.dim() != 2:
+        if not g.is_contiguous():
+            raise LaplexError(EINVAL, "g of other than two dimensions must be contiguous")
+        g = g.view(-1, g.shape[-1])
+    dim, ld = g.shape[1], _table("g", g)
+    if accumulate and out is None:
+        raise LaplexError(EINVAL, "accumulate needs out")
+    with _on(dev):
+        if out is None:
+            out = torch.empty((rows, dim), dtype=dtype or g.dtype, device=dev)
+        if out.shape[0] != rows or out.dtype not in (g.dtype, torch.float32):
+            raise LaplexError(EINVAL, f"out must have {rows} rows of {g.dtype} or float32")
+        size = ctypes.c_size_t(0)
+        _check(lib().laplex_embed_backward_workspace_size(tokens.numel(), rows, dim, dt, ctypes.byref(size)))
+        ws, nb = _seq_ws(dev, size.value)
+        _check(lib().laplex_embed_backward(_ptr(tokens), tb, tokens.numel(), _ptr(g), ld, rows, dim, float(scale),
+                                           int(bool(accumulate)), _ptr(out), _table("out", out, dim), dt,
+                                           _SEQ_DTYPES[out.dtype], _ptr(ws), nb, _stream(dev)))
+    return out
 
 
 # ----------------------------------------------------------------------------- host buffers

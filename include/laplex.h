@@ -62,7 +62,9 @@ typedef enum {
     LAPLEX_ETIMEOUT = 5     /* a bounded inter-block wait expired (device)      */
 } laplex_status;
 
-typedef enum { LAPLEX_F32 = 0, LAPLEX_F64 = 1 } laplex_dtype;
+/* LAPLEX_F16 and LAPLEX_BF16 are taken by the sequence operators alone
+ * (laplex_linattn*, laplex_embed*); every other call refuses them. */
+typedef enum { LAPLEX_F32 = 0, LAPLEX_F64 = 1, LAPLEX_F16 = 2, LAPLEX_BF16 = 3 } laplex_dtype;
 
 typedef enum {
     LAPLEX_OP_SORT = 0,
@@ -383,6 +385,142 @@ laplex_status laplex_test_set_sort_wait(uint32_t polls, int force_expiry);
  */
 laplex_status laplex_matvec_sym_noalloc(const float* sorted, const int32_t* perm, int64_t n,
                                         const float* x, float* y, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Sequence operators: decayed linear attention and the embedding lookup.
+ *
+ * Decayed linear attention is the causal half of the library's kernel over a
+ * sequence's tokens.  With the anchors a_t = -lam t (lam <= 0: the head's log
+ * decay) exp(-|a_t - a_s|) = e^{lam (t - s)} for s <= t, and the rank-2 factor
+ * cos(phi_t - psi_s) of the phased kernel becomes the rank-dk inner product
+ * <q_t, k_s>:
+ *     o_t = scale sum_{s <= t} e^{lam (t - s)} <q_t, k_s> v_s,
+ * by the recurrence over the states (summary §2.2 with x_t = k_t v_t^T)
+ *     S_t = e^lam S_{t-1} + k_t v_t^T,     o_t = scale S_t^T q_t.
+ *
+ * Conventions of these calls, beyond the common ones:
+ *  - Rows are of `dtype` (any of the four).  States, log decays and their
+ *    gradients are float, double for LAPLEX_F64, contiguous; a state is [dk, dv].
+ *    16-bit rows: products of 16-bit values summed in fp32; inside a block of
+ *    tokens the weights e^{lam (t - s)} <q_t, k_s> and the state that q_t reads
+ *    are rounded once to the rows' type, the states are not.
+ *  - Tokens are packed: sequence n owns rows cu_seqlens[n] .. cu_seqlens[n+1]-1
+ *    (int32 on the device, ascending, cu_seqlens[0] = 0, at most `tokens`);
+ *    cu_seqlens NULL: `seqs` sequences of tokens / seqs rows each.  A sequence
+ *    may be empty.  Rows behind the last sequence are neither read nor written.
+ *    (Bounds that do not ascend give unspecified results, without an access
+ *    outside the tensors.)
+ *  - hq q-heads share hkv k/v-heads in groups of hq / hkv (at most 32); decay
+ *    and state belong to the k/v-head.  dk, dv: multiples of 8 up to 128.
+ *  - Strides are in elements and at least dim; rows start on 16 bytes.  Integer
+ *    arrays need only the alignment of their elements.
+ *  - A token never reaches an earlier output: NaN and Inf in row s of k or v
+ *    leave the rows t < s of o as they are.
+ *  - log_decay = -Inf keeps no past (S_t = k_t v_t^T).
+ * ------------------------------------------------------------------------ */
+
+/* Rows ptr + token * token_stride + head * head_stride (elements). */
+typedef struct {
+    void* ptr;
+    int64_t token_stride;
+    int64_t head_stride;
+} laplex_rows;
+
+typedef struct {
+    int64_t tokens;            /* packed tokens, < 2^31 */
+    int64_t seqs;              /* sequences, <= 65535 */
+    const int32_t* cu_seqlens; /* [seqs + 1] on the device, or NULL */
+    int32_t hq, hkv, dk, dv;
+    const void* log_decay;     /* [hkv] on the device */
+    double scale;
+    laplex_dtype dtype;
+} laplex_linattn_shape;
+
+typedef enum {
+    LAPLEX_LINATTN_FORWARD = 0,
+    LAPLEX_LINATTN_BACKWARD = 1,
+    LAPLEX_LINATTN_BACKWARD_DECAY = 2 /* laplex_linattn_backward with dlog_decay */
+} laplex_linattn_call;
+
+/* Workspace bytes of a call on this shape (host only; log_decay is not read,
+ * of cu_seqlens only whether it is NULL).  Includes the header. */
+laplex_status laplex_linattn_workspace_size(const laplex_linattn_shape* shape, laplex_linattn_call call,
+                                            size_t* bytes);
+
+/*
+ * A packed batch of sequences.
+ *   q [tokens, hq, dk], k [tokens, hkv, dk], v [tokens, hkv, dv]: in.
+ *   state_in  [seqs, hkv, dk, dv] | NULL: the states before the first tokens (NULL: 0).
+ *   o [tokens, hq, dv]: out.
+ *   state_out [seqs, hkv, dk, dv] | NULL: out, the states behind the last
+ *   tokens; it may be state_in itself.
+ */
+laplex_status laplex_linattn(const laplex_linattn_shape* shape, const laplex_rows* q, const laplex_rows* k,
+                             const laplex_rows* v, const void* state_in, const laplex_rows* o, void* state_out,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradients of L = <dout, o> + <dstate_out, state_out>:
+ *   dq_t = scale S_t dout_t,
+ *   dk_s = R_s v_s,   dv_s = R_s^T k_s,    R_s = sum_{t >= s} e^{lam (t - s)} scale q_t dout_t^T
+ *                                                + e^{lam (L - 1 - s)} dstate_out,
+ *   dstate_in = e^lam R_0,   dlog_decay = sum_t scale <dout_t, W_t^T q_t> + <dstate_out, W_last>,
+ *   W_t = e^lam (W_{t-1} + S_{t-1}) (summed over the sequences).
+ * k/v-heads shared by a group of q-heads receive the group's total.
+ *   state_in, dstate_out: NULL means 0.
+ *   dq, dk, dv, dstate_in, dlog_decay: out, each may be NULL (not computed).
+ * The gradient of the decay runs as a recurrence in fp32 (fp64) for every type.
+ */
+laplex_status laplex_linattn_backward(const laplex_linattn_shape* shape, const laplex_rows* q, const laplex_rows* k,
+                                      const laplex_rows* v, const laplex_rows* dout, const void* state_in,
+                                      const void* dstate_out, const laplex_rows* dq, const laplex_rows* dk,
+                                      const laplex_rows* dv, void* dstate_in, void* dlog_decay, void* ws,
+                                      size_t ws_bytes, void* stream);
+
+/*
+ * One token per row against a cache of states, updated in place (no workspace).
+ *   shape: tokens rows (seqs and cu_seqlens ignored).
+ *   states [num_slots, hkv, dk, dv]: in and out.
+ *   slots  [tokens] | NULL: int32, the state of each row (NULL: row n uses
+ *          state n, tokens <= num_slots).  A row whose slot is outside
+ *          [0, num_slots) gets zeros and touches no state.  Rows that name the
+ *          same slot are applied in row order.
+ *   o [tokens, hq, dv]: out.
+ */
+laplex_status laplex_linattn_step(const laplex_linattn_shape* shape, const laplex_rows* q, const laplex_rows* k,
+                                  const laplex_rows* v, void* states, int64_t num_slots, const int32_t* slots,
+                                  const laplex_rows* o, void* stream);
+
+/*
+ * Embedding lookup: the product with the routing [a_i == b_j], the kernel's
+ * limit of small temperature (summary §2.1), b the rows' numbers.
+ *   out_i = scale table[tokens_i] (computed in fp32, rounded once), a row of
+ *   zeros for a token outside [0, rows) (padding).
+ *   tokens [n]: int32 or int64 (token_bytes 4 or 8).  table [rows, ld], out [n, out_ld].
+ */
+laplex_status laplex_embed(const void* table, int64_t ld, int64_t rows, int64_t dim, const void* tokens,
+                           int token_bytes, int64_t n, double scale, void* out, int64_t out_ld, laplex_dtype dtype,
+                           void* stream);
+
+/* Workspace bytes of laplex_embed_backward (host only), header included. */
+laplex_status laplex_embed_backward_workspace_size(int64_t n, int64_t rows, int64_t dim, laplex_dtype dtype,
+                                                   size_t* bytes);
+
+/*
+ * Its gradient, by sorting the tokens (the stable digit passes of
+ * laplex_sort_anchors) and summing runs:
+ *   dtable_r = scale sum over {i : tokens_i = r} of g_i
+ * summed in fp32 (fp64) in a fixed order of ascending i: the result does not
+ * vary from run to run.  Every row of dtable is written (0 where no token
+ * names it); with accumulate != 0 the sums are added to dtable instead, and
+ * rows without a token are left as they are.
+ *   g [n, g_ld] of dtype; dtable [rows, ld] of out_dtype, dtype itself or LAPLEX_F32.
+ *   Workspace: laplex_embed_backward_workspace_size(n, rows, dim, dtype, ...).
+ */
+laplex_status laplex_embed_backward(const void* tokens, int token_bytes, int64_t n, const void* g, int64_t g_ld,
+                                    int64_t rows, int64_t dim, double scale, int accumulate, void* dtable,
+                                    int64_t ld, laplex_dtype dtype, laplex_dtype out_dtype, void* ws,
+                                    size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
