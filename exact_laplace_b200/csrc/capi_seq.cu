@@ -107,8 +107,12 @@ lx::LinSeqs make_seqs(const laplex_linattn_shape& s, int seg) {
     return S;
 }
 
-int segment(const laplex_linattn_shape& s, int dv) {
-    return lx::rec_segment(s.tokens, (int)s.seqs, s.hkv, dv, s.cu_seqlens == nullptr);
+bool tensor_cores(const laplex_linattn_shape& s) { return s.dtype == LAPLEX_F16 || s.dtype == LAPLEX_BF16; }
+
+int segment(const laplex_linattn_shape& s, bool backward) {
+    const bool equal = s.cu_seqlens == nullptr || s.seqs == 1;
+    if (tensor_cores(s)) return lx::tc_segment(s.tokens, (int)s.seqs, s.hkv, backward ? 3 : 1, equal);
+    return lx::rec_segment(s.tokens, (int)s.seqs, s.hkv, std::min(s.dk, s.dv), equal);
 }
 
 size_t states_bytes(const laplex_linattn_shape& s, int seg) {
@@ -117,7 +121,7 @@ size_t states_bytes(const laplex_linattn_shape& s, int seg) {
 }
 
 size_t linattn_body(const laplex_linattn_shape& s, laplex_linattn_call call) {
-    const int seg = segment(s, std::min(s.dk, s.dv));
+    const int seg = segment(s, call != LAPLEX_LINATTN_FORWARD);
     if (call == LAPLEX_LINATTN_FORWARD) return states_bytes(s, seg);
     size_t b = 2 * states_bytes(s, seg);
     if (call == LAPLEX_LINATTN_BACKWARD_DECAY)
@@ -152,26 +156,48 @@ lx::LinRole role(lx::LinRows q, lx::LinRows k, lx::LinRows v, int nq, int nk, in
     return R;
 }
 
-// The states before each segment of R's direction into `states` (by slot), and
-// behind the last one into `last` (or NULL).
-cudaError_t segment_states(const laplex_linattn_shape& s, lx::LinRole R, const lx::LinSeqs& S, const void* init,
-                           void* states, void* last, cudaStream_t st) {
-    R.state_in = nullptr;
-    R.state_out = states;
-    R.out_by_slot = 1;
-    R.o = nullptr;
-    cudaError_t e = lx::rec_run(s.dtype, R, S, s.hkv, s.log_decay, true, st);
-    if (e != cudaSuccess) return e;
-    lx::LinCarry C = {};
-    C.S = S;
-    C.H = s.hkv;
-    C.reverse = R.reverse;
-    C.len = (int64_t)s.dk * s.dv;
-    C.lam = s.log_decay;
-    C.init = init;
-    C.states = states;
-    C.last = last;
-    return lx::carry_run(s.dtype, C, st);
+// The products of roles[0 .. count), or the segments' own states alone.
+cudaError_t run(const laplex_linattn_shape& s, const lx::LinRole* roles, int count, const lx::LinSeqs& S,
+                bool state_only, uint32_t* status, cudaStream_t st) {
+    if (tensor_cores(s)) return lx::tc_run(s.dtype, roles, count, S, s.hkv, s.log_decay, state_only, status, st);
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < count && e == cudaSuccess; ++i)
+        e = lx::rec_run(s.dtype, roles[i], S, s.hkv, s.log_decay, state_only, st);
+    return e;
+}
+
+struct Direction {
+    lx::LinRole R;
+    const void* init;  // per sequence, or NULL
+    void* states;      // out, by slot: the states before each segment of R's direction
+    void* last;        // out, per sequence: behind the last segment, or NULL
+};
+
+cudaError_t segment_states(const laplex_linattn_shape& s, Direction* D, int count, const lx::LinSeqs& S,
+                           uint32_t* status, cudaStream_t st) {
+    lx::LinRole R[2];
+    for (int i = 0; i < count; ++i) {
+        R[i] = D[i].R;
+        R[i].state_in = nullptr;
+        R[i].state_out = D[i].states;
+        R[i].out_by_slot = 1;
+        R[i].skip_last = D[i].last == nullptr;
+        R[i].o = nullptr;
+    }
+    cudaError_t e = run(s, R, count, S, true, status, st);
+    for (int i = 0; i < count && e == cudaSuccess; ++i) {
+        lx::LinCarry C = {};
+        C.S = S;
+        C.H = s.hkv;
+        C.reverse = D[i].R.reverse;
+        C.len = (int64_t)s.dk * s.dv;
+        C.lam = s.log_decay;
+        C.init = D[i].init;
+        C.states = D[i].states;
+        C.last = D[i].last;
+        e = lx::carry_run(s.dtype, C, st);
+    }
+    return e;
 }
 
 }  // namespace
@@ -202,7 +228,8 @@ laplex_status laplex_linattn(const laplex_linattn_shape* shape, const laplex_row
     TRY(check_ws(ws, ws_bytes, linattn_body(s, LAPLEX_LINATTN_FORWARD)));
     if (s.seqs == 0) return done(cudaSuccess, "");
     cudaStream_t st = (cudaStream_t)stream;
-    const lx::LinSeqs S = make_seqs(s, segment(s, std::min(s.dk, s.dv)));
+    uint32_t* status = static_cast<uint32_t*>(ws);
+    const lx::LinSeqs S = make_seqs(s, segment(s, false));
     lx::LinRole R = role(rq, rk, rv, s.hq / s.hkv, 1, s.dk, s.dv, false, false, s.scale, 1.0);
     R.o = const_cast<void*>(ro.p);
     R.o_ts = ro.ts;
@@ -212,12 +239,13 @@ laplex_status laplex_linattn(const laplex_linattn_shape* shape, const laplex_row
     cudaError_t e = cudaSuccess;
     if (S.seg <= S.T) {
         void* states = static_cast<char*>(ws) + lx::HEADER_BYTES;
-        e = segment_states(s, R, S, state_in, states, state_out, st);
+        Direction D = {R, state_in, states, state_out};
+        e = segment_states(s, &D, 1, S, status, st);
         R.state_in = states;
         R.in_by_slot = 1;
         R.state_out = nullptr;
     }
-    if (e == cudaSuccess) e = lx::rec_run(s.dtype, R, S, s.hkv, s.log_decay, false, st);
+    if (e == cudaSuccess) e = run(s, &R, 1, S, false, status, st);
     return done(e, "laplex_linattn");
 }
 
@@ -239,12 +267,14 @@ laplex_status laplex_linattn_backward(const laplex_linattn_shape* shape, const l
     TRY(check_state("state_in", state_in, s.dtype));
     TRY(check_state("dstate_out", dstate_out, s.dtype));
     TRY(check_state("dstate_in", dstate_in, s.dtype));
+    REQ(dstate_in == nullptr || (dstate_in != dstate_out && dstate_in != state_in), "dstate_in overlaps an input");
     REQ(aligned(dlog_decay, lx::acc_bytes(s.dtype)), "dlog_decay is not aligned");
     TRY(check_ws(ws, ws_bytes, linattn_body(s, dlog_decay ? LAPLEX_LINATTN_BACKWARD_DECAY : LAPLEX_LINATTN_BACKWARD)));
     cudaStream_t st = (cudaStream_t)stream;
     char* body = static_cast<char*>(ws) + lx::HEADER_BYTES;
     const int G = s.hq / s.hkv;
-    const lx::LinSeqs S = make_seqs(s, segment(s, std::min(s.dk, s.dv)));
+    uint32_t* status = static_cast<uint32_t*>(ws);
+    const lx::LinSeqs S = make_seqs(s, segment(s, true));
     cudaError_t e = cudaSuccess;
     if (dlog_decay) {
         lx::LinRole R = role(rq, rk, rv, G, 1, s.dk, s.dv, false, false, s.scale, 1.0);
@@ -263,8 +293,11 @@ laplex_status laplex_linattn_backward(const laplex_linattn_shape* shape, const l
     if (cut) {
         void* fwd = body;
         void* bwd = body + states_bytes(s, S.seg);
-        if (dq) e = segment_states(s, role(rq, rk, rv, G, 1, s.dk, s.dv, false, false, s.scale, 1.0), S, state_in, fwd, nullptr, st);
-        if (e == cudaSuccess && rev) e = segment_states(s, Rv, S, dstate_out, bwd, dstate_in, st);
+        Direction D[2];
+        int count = 0;
+        if (dq) D[count++] = {role(rq, rk, rv, G, 1, s.dk, s.dv, false, false, s.scale, 1.0), state_in, fwd, nullptr};
+        if (rev) D[count++] = {Rv, dstate_out, bwd, dstate_in};
+        e = segment_states(s, D, count, S, status, st);
         if (e != cudaSuccess) return done(e, "laplex_linattn_backward");
         Rq.state_in = fwd;
         Rk.state_in = Rv.state_in = bwd;
@@ -275,19 +308,23 @@ laplex_status laplex_linattn_backward(const laplex_linattn_shape* shape, const l
         R->o_ts = to.ts;
         R->o_hs = to.hs;
     };
+    lx::LinRole roles[3];
+    int count = 0;
     if (dq) {
         out(&Rq, rdq);
-        e = lx::rec_run(s.dtype, Rq, S, s.hkv, s.log_decay, false, st);
+        roles[count++] = Rq;
     }
-    if (e == cudaSuccess && dk) {
+    if (dk) {
         out(&Rk, rdk);
-        e = lx::rec_run(s.dtype, Rk, S, s.hkv, s.log_decay, false, st);
+        roles[count++] = Rk;
     }
-    if (e == cudaSuccess && (dv || (dstate_in && !cut))) {
-        if (!cut) Rv.state_out = dstate_in;
-        if (dv) out(&Rv, rdv);
-        e = lx::rec_run(s.dtype, Rv, S, s.hkv, s.log_decay, !dv, st);
+    if (!cut) Rv.state_out = dstate_in;
+    if (dv) {
+        out(&Rv, rdv);
+        roles[count++] = Rv;
     }
+    e = run(s, roles, count, S, false, status, st);
+    if (e == cudaSuccess && !dv && dstate_in && !cut) e = run(s, &Rv, 1, S, true, status, st);
     return done(e, "laplex_linattn_backward");
 }
 

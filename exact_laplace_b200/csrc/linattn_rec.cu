@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
     if (READ == 2 && !used && threadIdx.x == 0)
         P.part[((int64_t)slot * P.H + h) * gridDim.z + blockIdx.z] = 0.0;
     if (!used) return;
+    if (READ == 0 && R.skip_last && (R.reverse ? t0 == P.S.at(seq) : t0 + len == P.S.at(seq + 1))) return;
     const A lam = clamp_lam(static_cast<const A*>(P.lam)[h]);
     const int heads = R.nq > R.nk ? R.nq : R.nk;
     int nb = REC_ROWS / heads;

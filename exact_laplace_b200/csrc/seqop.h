@@ -75,6 +75,7 @@ struct LinRole {
     int in_by_slot;
     void* state_out;       // per segment or per sequence, or NULL
     int out_by_slot;
+    int skip_last;         // state pass: the segment at the direction's end is not needed
     void* w_out;           // the states' derivatives in lam (state pass), by slot, or NULL
 };
 
@@ -98,6 +99,11 @@ cudaError_t carry_run(laplex_dtype dt, const LinCarry& C, cudaStream_t st);
 size_t dlam_ws_bytes(laplex_dtype dt, int64_t T, int N, int Hkv, int dk, int dv, bool equal);
 cudaError_t dlam_run(laplex_dtype dt, LinRole fwd, LinRows dout, LinSeqs S, int H, const void* lam,
                      const void* state, const void* dstate, void* dlam, void* ws, size_t ws_bytes, cudaStream_t st);
+
+// ---- 16-bit rows on the tensor cores (linattn_tc.cu): up to three products at a time
+int tc_segment(int64_t T, int N, int H, int roles, bool equal);
+cudaError_t tc_run(laplex_dtype dt, const LinRole* roles, int count, const LinSeqs& S, int H, const void* lam,
+                   bool state_only, uint32_t* status, cudaStream_t st);
 
 // ---- single tokens (linattn_step.cu)
 struct LinStep {

@@ -87,6 +87,9 @@ def test_states_and_workspaces(L):
     st = L.laplex_linattn_backward(ctypes.byref(s), rows(), rows(), rows(), rows(ptr=8), None, None, None, None, None,
                                    None, None, P(256), BIG, None)
     refused(L, st, "dout")
+    st = L.laplex_linattn_backward(ctypes.byref(s), rows(), rows(), rows(), rows(), None, P(256), rows(), rows(), rows(),
+                                   P(256), None, P(256), BIG, None)
+    refused(L, st, "dstate_in")
 
 
 def test_no_sequences_is_no_work(L):
