@@ -267,53 +267,72 @@ __global__ void __launch_bounds__(256) k_dlam_join(const double* __restrict__ pa
 }
 
 // States before each segment from the segments' own: per element a serial walk
-// over the segments of a sequence, four segments' loads in flight.
+// over the segments of a sequence.
 //     X_in(j + 1) = e^{lam len_j} X_in(j) + X_j            (reverse: towards smaller j)
 //     W_in(j + 1) = e^{lam len_j} (W_in(j) + len_j X_in(j)) + W_j
-// Bound by its traffic: each segment's state is read and written once.
+// Each segment's state is read and written once; a thread walks 16 bytes, the
+// loads of the next eight segments in flight while it writes these (one value a
+// thread and four loads at a time took 86 us for 37 segments x 16 heads of
+// 128 x 128, which move 78 MB).
 template <typename A, bool DER>
-__global__ void __launch_bounds__(256) k_carry(const __grid_constant__ LinCarry C) {
+__global__ void __launch_bounds__(128) k_carry(const __grid_constant__ LinCarry C) {
+    constexpr int VN = 16 / (int)sizeof(A), U = DER ? 4 : 8;
+    using V = Pack<A, VN>;
     const int seq = blockIdx.y, h = blockIdx.z;
-    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    const int64_t e = ((int64_t)blockIdx.x * 128 + threadIdx.x) * VN;
     if (e >= C.len) return;
     const A lam = clamp_lam(static_cast<const A*>(C.lam)[h]);
     const int64_t total = C.S.at(seq + 1) - C.S.at(seq);
-    int64_t count = total <= 0 ? 1 : (total + C.S.seg - 1) / C.S.seg;
+    int count = total <= 0 ? 1 : (int)((total + C.S.seg - 1) / C.S.seg);
     const int s0 = C.S.first_slot(seq);
-    if (count > C.S.slots - s0) count = C.S.slots - s0;  // (bounds that do not ascend)
+    count = min(count, C.S.slots - s0);  // (bounds that do not ascend)
     const int64_t by_seq = ((int64_t)seq * C.H + h) * C.len + e;
-    A x = C.init ? static_cast<const A*>(C.init)[by_seq] : (A)0, w = 0;
-    const A full = decay(lam, (A)C.S.seg), part = decay(lam, (A)(total - (count - 1) * C.S.seg));
-    A* st = static_cast<A*>(C.states);
-    A* wt = static_cast<A*>(C.w);
-    constexpr int U = 4;
-    for (int64_t i0 = 0; i0 < count; i0 += U) {
-        A own[U], wown[U];
+    V x, w;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t i = i0 + u;
-            const int64_t j = C.reverse ? count - 1 - i : i;
-            const int64_t at = ((int64_t)(s0 + j) * C.H + h) * C.len + e;
-            own[u] = i < count ? st[at] : (A)0;
-            wown[u] = DER && i < count ? wt[at] : (A)0;
-        }
+    for (int k = 0; k < VN; ++k) x.v[k] = w.v[k] = 0;
+    if (C.init) x = *reinterpret_cast<const V*>(static_cast<const A*>(C.init) + by_seq);
+    const int64_t tail = total - (int64_t)(count - 1) * C.S.seg;
+    const A full = decay(lam, (A)C.S.seg), part = decay(lam, (A)tail);
+    const int64_t step = (C.reverse ? -1 : 1) * (int64_t)C.H * C.len;
+    const int64_t at0 = ((int64_t)(s0 + (C.reverse ? count - 1 : 0)) * C.H + h) * C.len + e;
+    A* st = static_cast<A*>(C.states) + at0;
+    A* wt = DER ? static_cast<A*>(C.w) + at0 : nullptr;
+    V own[2][U], wown[2][DER ? U : 1];
+    const auto load = [&](int b, int i0) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t i = i0 + u;
-            if (i >= count) break;
-            const int64_t j = C.reverse ? count - 1 - i : i;
-            const int64_t at = ((int64_t)(s0 + j) * C.H + h) * C.len + e;
-            const A d = j == count - 1 ? part : full;
-            const A n = (A)(j == count - 1 ? total - (count - 1) * C.S.seg : (int64_t)C.S.seg);
-            st[at] = x;
-            if constexpr (DER) {
-                wt[at] = w;
-                w = dfma(d, dfma(n, x, w), wown[u]);
+        for (int u = 0; u < U; ++u)
+            if (i0 + u < count) {
+                own[b][u] = *reinterpret_cast<const V*>(st + (i0 + u) * step);
+                if constexpr (DER) wown[b][u] = *reinterpret_cast<const V*>(wt + (i0 + u) * step);
             }
-            x = dfma(d, x, own[u]);
+    };
+    const auto walk = [&](int b, int i0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u;
+            if (i < count) {
+                const bool end = C.reverse ? i == 0 : i == count - 1;  // the sequence's last segment
+                const A d = end ? part : full;
+                *reinterpret_cast<V*>(st + i * step) = x;
+                if constexpr (DER) {
+                    const A n = (A)(end ? tail : (int64_t)C.S.seg);
+                    *reinterpret_cast<V*>(wt + i * step) = w;
+#pragma unroll
+                    for (int k = 0; k < VN; ++k) w.v[k] = dfma(d, dfma(n, x.v[k], w.v[k]), wown[b][u].v[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < VN; ++k) x.v[k] = dfma(d, x.v[k], own[b][u].v[k]);
+            }
         }
+    };
+    load(0, 0);
+    for (int i0 = 0; i0 < count; i0 += 2 * U) {
+        load(1, i0 + U);
+        walk(0, i0);
+        load(0, i0 + 2 * U);
+        walk(1, i0 + U);
     }
-    if (C.last) static_cast<A*>(C.last)[by_seq] = x;
+    if (C.last) *reinterpret_cast<V*>(static_cast<A*>(C.last) + by_seq) = x;
 }
 
 // ---------------------------------------------------------------- host side
@@ -378,13 +397,14 @@ cudaError_t rec_run(laplex_dtype dt, const LinRole& R, const LinSeqs& S, int H, 
 cudaError_t carry_run(laplex_dtype dt, const LinCarry& C, cudaStream_t st) {
     if (C.S.N == 0 || C.H == 0) return cudaSuccess;
     // sequences ride in grid.y (at most 65535): the C boundary checks their number
-    const dim3 grid((unsigned)((C.len + 255) / 256), (unsigned)C.S.N, (unsigned)C.H);
+    const int64_t per = 128 * (16 / (int64_t)acc_bytes(dt));  // dk dv is a multiple of 64
+    const dim3 grid((unsigned)((C.len + per - 1) / per), (unsigned)C.S.N, (unsigned)C.H);
     if (dt == LAPLEX_F64) {
-        if (C.w) k_carry<double, true><<<grid, 256, 0, st>>>(C);
-        else k_carry<double, false><<<grid, 256, 0, st>>>(C);
+        if (C.w) k_carry<double, true><<<grid, 128, 0, st>>>(C);
+        else k_carry<double, false><<<grid, 128, 0, st>>>(C);
     } else {
-        if (C.w) k_carry<float, true><<<grid, 256, 0, st>>>(C);
-        else k_carry<float, false><<<grid, 256, 0, st>>>(C);
+        if (C.w) k_carry<float, true><<<grid, 128, 0, st>>>(C);
+        else k_carry<float, false><<<grid, 128, 0, st>>>(C);
     }
     return cudaGetLastError();
 }

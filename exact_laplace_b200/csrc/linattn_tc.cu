@@ -11,15 +11,25 @@
 // and the reversed products (the gradients dk and dv) are the same with the
 // mask s >= t, e^{lam (n - 1 - t)} before O2 and e^{lam s} inside U.
 //
-// A block of two warpgroups walks one segment of one head.  TMA boxes bring Q,
-// K, V into swizzled tiles (K and V two stages ahead); one thread issues the
-// products; all accumulators lie in tensor memory.  A thread owns a row: half of
-// the columns of P (weighted, rounded once to the rows' type, and put back into
-// tensor memory as the A operand of O1), of O1 and O2 (combined and stored), and
-// of the state, which stays in fp32 registers and reaches shared memory rounded
-// to the rows' type, for O2 alone.  K's weights are applied as a sum of two
-// 16-bit values (hi in place, lo beside it), so that U, and the states that
-// leave the call, carry 2^-17, not 2^-9.
+// A block walks one segment of one head.  TMA boxes bring Q, K, V into swizzled
+// tiles (K and V two chunks ahead); all accumulators lie in tensor memory.  Three
+// kinds of warps work at the same time and meet at mbarriers:
+//   issue (one warp):  the copies and the products, from one thread;
+//   state (8 warps):   V's scan, K's weights, the state.  The state is U's
+//                      accumulator in tensor memory (fp32): once a chunk each
+//                      thread reads half a row of it, writes it, rounded to the
+//                      rows' type, to shared memory (for O2 alone) and scales it
+//                      by the next chunk's e^{lam n}, on which the next U adds.
+//                      K is weighed as a sum of two 16-bit values (hi in place,
+//                      lo beside it), so that U carries 2^-17, not 2^-9; where
+//                      the state leaves the call, from fp32 products, and in
+//                      three parts for bf16;
+//   rows (8 warps):    P's weights, rounded once to the rows' type and put back
+//                      into tensor memory as the A operand of O1, and the outputs.
+// One group of 8 warps that did all of this in turn took 8.9 us a chunk of
+// dk = dv = 128 (issue slots 21 % busy, the rest latencies of the chain).  The
+// tiles leave hardly any L1: a spilled register is a trip to L2, so nothing is
+// kept in registers from chunk to chunk, and the loops over columns are not unrolled.
 //
 // fp16: weights, states and weighted K are scaled by powers of two (per row, per
 // state, per chunk) to 2^14..2^15 before they are rounded, so that nothing
@@ -27,8 +37,8 @@
 //
 // Causality: a masked weight is 0, and 0 times a NaN or Inf of a later row of V
 // would be NaN.  Each chunk's V is scanned (a few integer operations per 16
-// bytes, while P runs); non-finite values are replaced by 0 and their products
-// added by hand to the rows that they do reach.
+// bytes); non-finite values are replaced by 0 and their products added by hand to
+// the rows that they do reach.
 //
 // Bound by memory at full grids: a chunk of dk = dv = 128 moves 128 KB (2.8 us
 // of an SM's share of the measured bandwidth) against 2560 cycles of tensor work.
@@ -42,13 +52,14 @@
 
 namespace lx {
 
-constexpr int TC_NT = 256;
+constexpr int TC_GROUP = 256;  // threads of the state warps, and of the rows warps
 constexpr int TC_C = 128;  // tokens per chunk
 constexpr uint32_t TILE_BYTES = TC_C * 128;
 
 struct TcRole {
     int mq, mk, mv;  // maps of the operands
     int nq, nk, dk, dv, reverse, transposed, in_by_slot, out_by_slot, skip_last;
+    int exact;       // the state that leaves is a result, not only rounded for O2
     float sq, sk;
     const void* k;   // rows of k and v (for what a NaN or Inf reaches)
     int64_t k_ts, k_hs;
@@ -71,23 +82,39 @@ struct alignas(64) TcArgs {
 
 // shared memory behind the tiles
 struct TcShared {
-    uint64_t kv_full[2], q_full, p_done, o2_done, o_done, u_done;
+    uint64_t kv_full[2], q_full;             // copies
+    // A waiter names a phase by its parity, so no barrier may run two phases ahead of one of
+    // its waiters.  (p_done is waited for by the rows warps at every item; k_free says the same
+    // to the state warps where they weigh K; v_ready runs one load ahead, hence two of it.)
+    uint64_t p_done, k_free, o2_done, o_done, u_done;  // products
+    uint64_t v_ready[2], k_ready, s_ready;             // from the state warps
+    uint64_t p_ready, o_read;                          // from the rows warps
     uint32_t tmem;
-    uint32_t bad[2][4];  // rows of V with a NaN or Inf, by parity of the load
-    float wk[TC_C];      // weights of K's rows
-    float rmax[2][TC_C]; // fp16: largest weight of a row, by half
-    float red[2][8];     // fp16: block maxima
+    uint32_t dead;       // a wait ran out
+    uint32_t bad[8][4];  // rows of V with a NaN or Inf, by load
+    float wt[2 * TC_C];  // P's weights scale e^{lam |x|} at TC_C + x, x = row - column; 0 past the diagonal
+    union {
+        float dec[TC_C];   // K's weights g1 e^{lam d}, d >= 0 (exact)
+        uint2 dec2[TC_C];  // the same as sums of two 16-bit values, each twice
+    };
+    float s_inv[2];      // fp16: what the rounded state is to be multiplied by, by chunk
+    uint8_t rexp[2][TC_C];  // fp16: the exponent of a row's largest weight, by half
+    float red[2][8];     // fp16: maxima of the state warps
 };
 
 template <int DK, int DV, bool OUT> struct TcSize {
     static constexpr uint32_t KBY = DK / 64 * TILE_BYTES, VBY = DV / 64 * TILE_BYTES;
-    static constexpr uint32_t SBY = DK * 128 * (DV / 64);
-    static constexpr uint32_t K = 0, V = 2 * KBY, LO = V + 2 * VBY, S = LO + KBY, Q = S + (OUT ? SBY : 0);
+    // the rounded state, and in its place K's third part between O2 and the next state
+    static constexpr uint32_t SBY = OUT && DK * 128 * (DV / 64) > KBY ? DK * 128 * (DV / 64) : KBY;
+    static constexpr uint32_t K = 0, V = 2 * KBY, LO = V + 2 * VBY, S = LO + KBY, Q = S + SBY;
     static constexpr uint32_t TILES = Q + (OUT ? KBY : 0);
     static constexpr uint32_t BYTES = TILES + sizeof(TcShared);
-    // tensor memory columns: P (whose first half then holds the rounded weights), O1, O2, U
-    static constexpr uint32_t P = 0, O1 = 128, O2 = 128 + DV, U = !OUT ? 0 : DV == 64 ? 64 : 128 + 2 * DV;
-    static constexpr uint32_t COLS = !OUT ? DV : DV == 64 ? 256 : 512;
+    // tensor memory columns: P, O1, O2, U.  The rounded weights of P's columns 0-63
+    // take columns 0-31, those of 64-127 columns 64-95: each warp writes over what it alone read.
+    static constexpr uint32_t P = 0, O1 = 128, O2 = 256, U = OUT ? 384 : 0;
+    static constexpr uint32_t COLS = OUT ? 512 : DV;
+    // the issuing warp brings three idle ones: registers are moved between groups of four warps
+    static constexpr int NT = OUT ? 2 * TC_GROUP + 128 : TC_GROUP + 32;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -114,58 +141,64 @@ template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// the power of two that brings a largest magnitude m to [2^14, 2^15) (1 for 0, Inf and NaN)
+// the power of two that brings a largest magnitude m to [2^14, 2^15) (2^100 for less
+// than 2^-86; 1 for Inf and NaN)
+__device__ __forceinline__ float scale_of_exponent(int e) {
+    return __uint_as_float((uint32_t)(127 + 14 - max(e - 127, -86)) << 23);
+}
 __device__ __forceinline__ float scale_to_fp16(float m) {
-    if (!(m > 0.0f) || m > 3.0e38f) return 1.0f;
-    const int e = (int)(__float_as_uint(m) >> 23) - 127;
-    return __uint_as_float((uint32_t)(127 + 14 - max(e, -100)) << 23);
+    return m <= 3.0e38f ? scale_of_exponent((int)(__float_as_uint(m) >> 23)) : 1.0f;
 }
 
+// (a, b) * (c, d)
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    float2 r;
+    asm("{\n .reg .b64 a, b, c;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mul.rn.f32x2 c, a, b;\n"
+        " mov.b64 {%0, %1}, c;\n}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return r;
+}
+
+// 16-bit pairs: a b + c and a b, each rounded once
+template <typename T> struct Pair;
+template <> struct Pair<__nv_bfloat16> {
+    static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t r;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        return r;
+    }
+};
+template <> struct Pair<__half> {
+    static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
+        uint32_t r;
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+        return r;
+    }
+};
+
+template <int ID> __device__ __forceinline__ void group_sync() {
+    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(TC_GROUP) : "memory");
+}
+
+// What every warp of a block knows.
 template <typename T, int DK, int DV, bool OUT>
-__global__ void __launch_bounds__(TC_NT, 1) k_lin_tc(const __grid_constant__ TcArgs A) {
+struct TcBlock {
     using Z = TcSize<DK, DV, OUT>;
-    constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
-    constexpr int HV = DV / 2;  // state and output columns of a thread
-    extern __shared__ __align__(1024) unsigned char sm[];
-    TcShared& sh = *reinterpret_cast<TcShared*>(sm + Z::TILES);
-    const TcRole& R = A.role[blockIdx.x % A.nroles];
-    const int slot = blockIdx.x / A.nroles, h = blockIdx.y;
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
-    int seq, len;
+    static constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+    static constexpr int HV = DV / 2;  // columns of a thread of the state and of the outputs
+
+    const TcArgs& A;
+    const TcRole& R;
+    unsigned char* sm;
+    TcShared& sh;
+    uint32_t smb, tm;
+    int slot, h, seq, len, nch, nq, nk, G;
     int64_t t0;
-    if (!A.S.find(slot, &seq, &t0, &len)) return;
-    const bool rev = R.reverse;
-    if (!OUT && R.skip_last && (rev ? t0 == A.S.at(seq) : t0 + len == A.S.at(seq + 1))) return;
+    bool rev, exact;  // exact: K's weights from fp32, in three parts for bf16
+    float l2, g1, up1;  // K's largest weight (e^lam sk reversed, sk forward), times up1, a power of two (fp16)
 
-    if (smem_u32(sm) & 1023u) {  // the swizzle goes by address bits: the tiles must start on 1024 bytes
-        if (tid == 0) set_status(A.status, ST_TIMEOUT);
-        return;
-    }
-    if (tid == 0) {
-        mbar_init(&sh.kv_full[0], 1);
-        mbar_init(&sh.kv_full[1], 1);
-        mbar_init(&sh.q_full, 1);
-        mbar_init(&sh.p_done, 1);
-        mbar_init(&sh.o2_done, 1);
-        mbar_init(&sh.o_done, 1);
-        mbar_init(&sh.u_done, 1);
-        fence_proxy_async();
-    }
-    __syncwarp();
-    if (warp == 0) tmem_alloc(&sh.tmem, Z::COLS);
-    if (tid < 8) sh.bad[tid >> 2][tid & 3] = 0;
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tm = sh.tmem;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t smb = smem_u32(sm);
-
-    const int nch = (len + TC_C - 1) / TC_C;
-    const int nq = R.nq, nk = R.nk, G = max(nq, nk);
-    const int n_kv = nch * nk, n_q = OUT ? nch * nq : 0;
-    const auto chunk_at = [&](int c, int* n) -> int64_t {
+    __device__ __forceinline__ int64_t chunk_at(int c, int* n) const {
         if (!rev) {
             *n = min(TC_C, len - c * TC_C);
             return t0 + (int64_t)c * TC_C;
@@ -173,9 +206,26 @@ __global__ void __launch_bounds__(TC_NT, 1) k_lin_tc(const __grid_constant__ TcA
         const int end = len - c * TC_C, a = max(end - TC_C, 0);
         *n = end - a;
         return t0 + a;
-    };
-    const auto load_kv = [&](int i) {
-        if (i >= n_kv) return;
+    }
+    // bounded; false once any wait of the block has run out
+    __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
+        if (mbar_test(bar, parity & 1)) return true;
+        for (uint32_t it = 0; it < MBAR_POLLS; ++it) {
+            if (mbar_sleep(bar, parity & 1)) return true;
+            if ((it & 15) == 15 && *(volatile uint32_t*)&sh.dead) return false;
+        }
+        *(volatile uint32_t*)&sh.dead = 1;
+        return false;
+    }
+    // one arrival per warp, after its lanes' accesses
+    __device__ __forceinline__ void arrive(uint64_t* bar) const {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    }
+
+    // ---- copies and products, by one thread
+    __device__ __forceinline__ void load_kv(int i) const {
+        if (i >= nch * nk) return;
         int n;
         const int64_t a = chunk_at(i / nk, &n);
         const int head = h * nk + i % nk;
@@ -185,431 +235,673 @@ __global__ void __launch_bounds__(TC_NT, 1) k_lin_tc(const __grid_constant__ TcA
             tma_load3(sm + Z::K + (i & 1) * Z::KBY + b * TILE_BYTES, &A.map[R.mk], b * 64, head, (int)a, bar);
         for (int b = 0; b < DV / 64; ++b)
             tma_load3(sm + Z::V + (i & 1) * Z::VBY + b * TILE_BYTES, &A.map[R.mv], b * 64, head, (int)a, bar);
-    };
-    const auto load_q = [&](int i) {
-        if (i >= n_q) return;
+    }
+    __device__ __forceinline__ void load_q(int i) const {
+        if (i >= nch * nq) return;
         int n;
         const int64_t a = chunk_at(i / nq, &n);
         mbar_expect_tx(&sh.q_full, Z::KBY);
         for (int b = 0; b < DK / 64; ++b)
             tma_load3(sm + Z::Q + b * TILE_BYTES, &A.map[R.mq], b * 64, h * nq + i % nq, (int)a, &sh.q_full);
-    };
-    if (tid == 0) {
+    }
+    __device__ __forceinline__ void issue() const {
         load_kv(0);
         if (OUT) load_q(0);
         load_kv(1);
-    }
-
-    const float l2 = clamp_lam(A.lam[h]) * 1.44269504088896341f;
-    float pw[8];  // e^{lam j}, in the order of a row's columns
-#pragma unroll
-    for (int j = 0; j < 8; ++j) pw[j] = ex2(l2 * (float)(rev ? j : 7 - j));
-    const float ssk = R.sq * R.sk;
-    // reversed: K carries e^{lam s}, and U the e^lam that leads out of the chunk,
-    // so that the largest of K's weights is 1 (fp16: a fast decay would sink all)
-    const float u_out = rev ? exp2f(l2) : 1.0f;
-
-    float S[HV];  // the state: row `row` of dk, columns wg * HV ...
-#pragma unroll
-    for (int c = 0; c < HV; ++c) S[c] = 0.0f;
-    const int64_t by_slot = (int64_t)slot * A.H + h, by_seq = (int64_t)seq * A.H + h;
-    const int64_t ri = R.transposed ? 1 : R.dv, ci = R.transposed ? R.dk : 1;
-    bool has_state = R.state_in != nullptr;
-    if (has_state && row < R.dk) {
-        const float* p = R.state_in + (R.in_by_slot ? by_slot : by_seq) * R.dk * R.dv + row * ri;
-#pragma unroll
-        for (int c = 0; c < HV; ++c)
-            if (wg * HV + c < R.dv) S[c] = p[(wg * HV + c) * ci];
-    }
-    float s_inv = 1.0f;  // the rounded state is the state / s_inv
-    // the state, rounded, into shared memory as the B operand of O2 (by all threads)
-    const auto store_state = [&]() {
-        float up = 1.0f;
-        if constexpr (!BF) {
-            float m = 0.0f;
-#pragma unroll
-            for (int c = 0; c < HV; ++c) m = fmaxf(m, fabsf(S[c]));
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, s));
-            if (lane == 0) sh.red[1][warp] = m;
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < 8; ++w) m = fmaxf(m, sh.red[1][w]);
-            up = scale_to_fp16(m);
-            s_inv = 1.0f / up;
-        }
-        if (row < DK) {
-#pragma unroll
-            for (int u = 0; u < HV / 8; ++u) {
-                uint4 w;
-                uint32_t* q = &w.x;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) q[e] = pack2<T>(S[u * 8 + 2 * e] * up, S[u * 8 + 2 * e + 1] * up);
-                const int col = wg * HV + u * 8;
-                *reinterpret_cast<uint4*>(sm + Z::S + (col >> 6) * (DK * 128) + tile_at(row, (col & 63) >> 3)) = w;
-            }
-        }
-        fence_proxy_async();
-    };
-    if (OUT && has_state) store_state();
-
-    bool ok = true;
-    int wk_n = -1;       // tokens that the weights of K were made for
-    float k_inv = 1.0f;  // fp16: the weighted K is K / k_inv
-    float oacc[!BF && OUT ? HV : 1];
-    bool stop = false;
-    uint32_t item = 0, u_count = 0;
-    for (int c = 0; c < nch && !stop; ++c) {
-        int n;
-        const int64_t a = chunk_at(c, &n);
-        const float wq = R.sq * exp2f(l2 * (float)(rev ? n - 1 - row : row + 1));
-        const float whole = exp2f(l2 * (float)n);
-        for (int i = 0; i < G; ++i, ++item) {
-            const int kv = c * nk + (nk > 1 ? i : 0), qi = c * nq + (nq > 1 ? i : 0);
-            const bool new_kv = i == 0 || nk > 1, new_q = i == 0 || nq > 1;
-            const bool last = i == G - 1;
-            const bool conv = nk > 1 || last;        // K is needed no more: weigh it
-            const bool emit = nq > 1 || last;        // O1 is whole
-            unsigned char* Ks = sm + Z::K + (kv & 1) * Z::KBY;
-            unsigned char* Vs = sm + Z::V + (kv & 1) * Z::VBY;
-            const uint32_t Ka = smb + Z::K + (kv & 1) * Z::KBY, Va = smb + Z::V + (kv & 1) * Z::VBY;
-            if (new_kv) ok &= mbar_wait(&sh.kv_full[kv & 1], (uint32_t)(kv >> 1) & 1);
-            if (OUT && new_q) ok &= mbar_wait(&sh.q_full, (uint32_t)qi & 1);
-            tc_fence_before();
-            if (__syncthreads_or(!ok)) {
-                stop = true;
-                break;
-            }
-            if (OUT && tid == 0) {
-                tc_fence_after();
-                constexpr uint32_t id = mma_desc(BF, false, false, 128, 128);
-#pragma unroll
-                for (int s = 0; s < DK / 16; ++s) {
-                    const uint32_t off = (s >> 2) * TILE_BYTES + (s & 3) * 32;
-                    mma_ss(tm + Z::P, tile_desc(smb + Z::Q + off, 16, 1024), tile_desc(Ka + off, 16, 1024), id, s > 0);
-                }
-                mma_commit(&sh.p_done);
-                if (new_q) {
-                    if (has_state) {
-                        constexpr uint32_t id2 = mma_desc(BF, false, true, 128, DV);
-#pragma unroll
-                        for (int s = 0; s < DK / 16; ++s) {
-                            const uint32_t off = (s >> 2) * TILE_BYTES + (s & 3) * 32;
-                            mma_ss(tm + Z::O2, tile_desc(smb + Z::Q + off, 16, 1024),
-                                   tile_desc(smb + Z::S + s * 2048, DK * 128, 1024), id2, s > 0);
-                        }
-                    }
-                    mma_commit(&sh.o2_done);
-                }
-            }
-            if (wk_n != n) {  // (the last chunk's are read no more: all threads have passed the barrier above)
-                wk_n = n;
-                if (tid < TC_C) sh.wk[tid] = tid < n ? R.sk * exp2f(l2 * (float)(rev ? tid : n - 1 - tid)) : 0.0f;
-            }
-            if (new_kv) {
-                // V: rows past the chunk's tokens become 0, and so do NaN and Inf
-                if (tid < 4) sh.bad[(kv + 1) & 1][tid] = 0;
-                constexpr uint32_t ONE = BF ? 0x00800080u : 0x04000400u;
-#pragma unroll
-                for (int x = 0; x < DV / 64 * 4; ++x) {
-                    const int u = x * TC_NT + tid, r = (u >> 3) & 127, b = u >> 10;
-                    uint4* p = reinterpret_cast<uint4*>(Vs + b * TILE_BYTES + tile_at(r, u & 7));
-                    if (r >= n) {
-                        *p = make_uint4(0, 0, 0, 0);
-                        continue;
-                    }
-                    uint4 w = *p;
-                    const uint32_t any = ((w.x & 0x7fff7fffu) + ONE) | ((w.y & 0x7fff7fffu) + ONE) |
-                                         ((w.z & 0x7fff7fffu) + ONE) | ((w.w & 0x7fff7fffu) + ONE);
-                    if (OUT && (any & 0x80008000u)) {
-                        atomicOr(&sh.bad[kv & 1][r >> 5], 1u << (r & 31));
-                        uint32_t* q = &w.x;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const uint32_t t = (q[e] & 0x7fff7fffu) + ONE;
-                            q[e] &= (t & 0x8000u ? 0u : 0xffffu) | (t & 0x80000000u ? 0u : 0xffff0000u);
-                        }
-                        *p = w;
-                    }
-                }
-                if constexpr (!BF) {
-                    uint32_t m = 0;
-#pragma unroll
-                    for (int x = 0; x < DK / 64 * 4; ++x) {
-                        const int u = x * TC_NT + tid, r = (u >> 3) & 127, b = u >> 10;
-                        if (r >= n) continue;
-                        const uint4 w = *reinterpret_cast<const uint4*>(Ks + b * TILE_BYTES + tile_at(r, u & 7));
-                        m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
-                                                 __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
-                    }
-                    m = max(m & 0xffffu, m >> 16);
-#pragma unroll
-                    for (int s = 16; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(FULL, m, s));
-                    if (lane == 0) sh.red[0][warp] = __half2float(__ushort_as_half((unsigned short)m));
-                }
-            }
-            uint32_t pk[32];       // the weights, rounded, two a word
-            float pf[BF ? 1 : 64];  // fp16: before they are rounded
-            float p_inv = 1.0f;
-            if constexpr (OUT) {
-                ok &= mbar_wait(&sh.p_done, item & 1);
-                tc_fence_after();
-                const int tw = (warp & 3) * 32;
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t r[32];
-                    const int base = wg * 64 + half * 32;
-                    tmem_ld32(tm + lanes + Z::P + base, r);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                        const int s0 = base + b * 8;
-                        float w[8];
-                        const bool none = rev ? s0 + 7 < tw || s0 >= n : s0 > tw + 31;
-                        const bool all = rev ? s0 >= tw + 31 && s0 + 8 <= n : s0 + 7 <= tw;
-                        if (none) {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) w[j] = 0.0f;
-                        } else if (all) {
-                            const float f = ssk * ex2(l2 * (float)(rev ? s0 - row : row - s0 - 7));
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) w[j] = __uint_as_float(r[b * 8 + j]) * (f * pw[j]);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const int s = s0 + j, d = rev ? s - row : row - s;
-                                w[j] = d >= 0 && s < n ? __uint_as_float(r[b * 8 + j]) * (ssk * ex2(l2 * (float)d)) : 0.0f;
-                            }
-                        }
-                        if constexpr (BF) {
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) pk[half * 16 + b * 4 + j] = pack2<T>(w[2 * j], w[2 * j + 1]);
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) pf[half * 32 + b * 8 + j] = w[j];
-                        }
-                    }
-                }
-                if constexpr (!BF) {
-                    float m = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) m = fmaxf(m, fabsf(pf[j]));
-                    sh.rmax[wg][row] = m;
-                }
-                tc_fence_before();
-            }
-            __syncthreads();  // all of P is read (its columns take the rounded weights), block maxima are there
-            if constexpr (OUT) {
-                if constexpr (!BF) {
-                    const float up = scale_to_fp16(fmaxf(sh.rmax[0][row], sh.rmax[1][row]));
-                    p_inv = 1.0f / up;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) pk[j] = pack2<T>(pf[2 * j] * up, pf[2 * j + 1] * up);
-                }
-                tc_fence_after();
-                tmem_st32(tm + lanes + Z::P + wg * 32, pk);
-                tmem_wait_st();
-            }
-            if (conv) {
-                float k_up = 1.0f;
-                if constexpr (!BF) {
-                    float m = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < 8; ++w) m = fmaxf(m, sh.red[0][w]);
-                    k_up = scale_to_fp16(m * fabsf(R.sk));
-                    k_inv = 1.0f / k_up;
-                }
-#pragma unroll
-                for (int x = 0; x < DK / 64 * 4; ++x) {
-                    const int u = x * TC_NT + tid, r = (u >> 3) & 127, b = u >> 10;
-                    const uint32_t at = b * TILE_BYTES + tile_at(r, u & 7);
-                    uint4 w = *reinterpret_cast<const uint4*>(Ks + at), hi, lo;
-                    const float f = sh.wk[r] * k_up;
-                    const uint32_t* q = &w.x;
-                    uint32_t *qh = &hi.x, *ql = &lo.x;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float2 v = unpack2<T>(q[e]);
-                        v.x *= f;
-                        v.y *= f;
-                        qh[e] = pack2<T>(v.x, v.y);
-                        const float2 g = unpack2<T>(qh[e]);
-                        float2 d = make_float2(v.x - g.x, v.y - g.y);
-                        d.x = d.x == d.x ? d.x : 0.0f;  // Inf - Inf: the upper part says it
-                        d.y = d.y == d.y ? d.y : 0.0f;
-                        ql[e] = pack2<T>(d.x, d.y);
-                    }
-                    if (r >= n) hi = lo = make_uint4(0, 0, 0, 0);  // not 0 * NaN
-                    *reinterpret_cast<uint4*>(Ks + at) = hi;
-                    *reinterpret_cast<uint4*>(sm + Z::LO + at) = lo;
-                }
-            }
-            fence_proxy_async();  // V, K and its lower part are read by the products
-            tc_fence_before();
-            __syncthreads();
-            if (tid == 0) {
-                tc_fence_after();
+        bool has_state = R.state_in != nullptr;
+        int item = 0, us = 0, refill = -1;
+        for (int c = 0; c < nch; ++c) {
+            for (int i = 0; i < G; ++i, ++item) {
+                const int kv = c * nk + (nk > 1 ? i : 0), qi = c * nq + (nq > 1 ? i : 0);
+                const bool new_kv = i == 0 || nk > 1, new_q = i == 0 || nq > 1, last = i == G - 1;
+                const bool conv = nk > 1 || last, emit = nq > 1 || last;
+                const uint32_t Ka = smb + Z::K + (kv & 1) * Z::KBY, Va = smb + Z::V + (kv & 1) * Z::VBY;
+                if (new_kv && !wait(&sh.kv_full[kv & 1], kv >> 1)) return;
                 if constexpr (OUT) {
+                    if (new_q && !wait(&sh.q_full, qi)) return;
+                    if (item > 0 && !wait(&sh.o_done, item - 1)) return;  // O1 has read the weights in P's place
+                    tc_fence_after();
+                    constexpr uint32_t id = mma_desc(BF, false, false, 128, 128);
+                    const uint64_t dq = tile_desc(smb + Z::Q, 16, 1024), dk = tile_desc(Ka, 16, 1024);
+#pragma unroll 1
+                    for (int s = 0; s < DK / 16; ++s) {
+                        const uint32_t off = ((s >> 2) * TILE_BYTES + (s & 3) * 32) >> 4;
+                        mma_ss(tm + Z::P, dq + off, dk + off, id, s > 0);
+                    }
+                    mma_commit(&sh.p_done);
+                    if (conv && !(BF && exact)) mma_commit(&sh.k_free);
+                }
+                if (refill >= 0) {  // the last products have read their K and V
+                    if (!wait(&sh.u_done, us - 1)) return;
+                    load_kv(refill);
+                    refill = -1;
+                }
+                if constexpr (OUT) {
+                    if (item > 0 && !wait(&sh.o_read, item - 1)) return;
+                    if (new_q) {
+                        if (has_state) {
+                            if (i == 0 && !wait(&sh.s_ready, R.state_in ? c : c - 1)) return;
+                            tc_fence_after();
+                            constexpr uint32_t id = mma_desc(BF, false, true, 128, DV);
+                            const uint64_t dq = tile_desc(smb + Z::Q, 16, 1024), ds = tile_desc(smb + Z::S, DK * 128, 1024);
+#pragma unroll 1
+                            for (int s = 0; s < DK / 16; ++s)
+                                mma_ss(tm + Z::O2, dq + (((s >> 2) * TILE_BYTES + (s & 3) * 32) >> 4), ds + s * (2048 >> 4),
+                                       id, s > 0);
+                        }
+                        mma_commit(&sh.o2_done);
+                    }
+                    if (conv && BF && exact) mma_commit(&sh.k_free);  // K's third part takes the state's place
+                    if (emit && new_q) {  // P and O2 have read Q
+                        if (!wait(&sh.o2_done, qi)) return;
+                        load_q(qi + 1);
+                    }
+                    if (!wait(&sh.p_ready, item)) return;
+                    if (emit && !new_q) load_q(qi + 1);  // (O2 was before the last P)
+                    if (new_kv && !wait(&sh.v_ready[kv & 1], kv >> 1)) return;
+                    tc_fence_after();
                     constexpr uint32_t id = mma_desc(BF, false, true, 128, DV);
-                    const bool more = BF && nk > 1 && i > 0;
-#pragma unroll
+                    const bool more = nk > 1 && i > 0;
+                    const uint64_t dv = tile_desc(Va, TILE_BYTES, 1024);
+#pragma unroll 1
                     for (int s = 0; s < 8; ++s)
-                        mma_ts(tm + Z::O1, tm + Z::P + s * 8, tile_desc(Va + s * 2048, TILE_BYTES, 1024), id, more || s > 0);
+                        mma_ts(tm + Z::O1, tm + Z::P + (s >> 2) * 64 + (s & 3) * 8, dv + s * (2048 >> 4), id, more || s > 0);
                     mma_commit(&sh.o_done);
                 }
                 if (conv) {
+                    if (!wait(&sh.k_ready, us)) return;  // and the state is scaled
+                    tc_fence_after();
                     // dk = 64: M stays 128, the second half repeats the first (leading offset 0) and is not read
                     constexpr uint32_t id = mma_desc(BF, true, true, 128, DV), lead = DK == 64 ? 0 : TILE_BYTES;
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        mma_ss(tm + Z::U, tile_desc(Ka + s * 2048, lead, 1024), tile_desc(Va + s * 2048, TILE_BYTES, 1024),
-                               id, s > 0);
-#pragma unroll
-                    for (int s = 0; s < 8; ++s)
-                        mma_ss(tm + Z::U, tile_desc(smb + Z::LO + s * 2048, lead, 1024),
-                               tile_desc(Va + s * 2048, TILE_BYTES, 1024), id, true);
+                    const int parts = BF && exact ? 3 : 2;
+                    const uint64_t dv = tile_desc(Va, TILE_BYTES, 1024);
+#pragma unroll 1
+                    for (int x = 0; x < parts; ++x) {
+                        const uint64_t dk = tile_desc(x == 0 ? Ka : smb + (x == 1 ? Z::LO : Z::S), lead, 1024);
+#pragma unroll 1
+                        for (int s = 0; s < 8; ++s)
+                            mma_ss(tm + Z::U, dk + s * (2048 >> 4), dv + s * (2048 >> 4), id,
+                                   us > 0 || R.state_in || x > 0 || s > 0);
+                    }
                     mma_commit(&sh.u_done);
+                    ++us;
+                    refill = kv + 2;
                 }
             }
-            const bool patch = OUT && (sh.bad[kv & 1][0] | sh.bad[kv & 1][1] | sh.bad[kv & 1][2] | sh.bad[kv & 1][3]);
-            if constexpr (OUT) {
-                ok &= mbar_wait(&sh.o_done, item & 1);
-                if (new_q) ok &= mbar_wait(&sh.o2_done, (uint32_t)qi & 1);
-                tc_fence_after();
-                if (emit && tid == 0) load_q(qi + 1);  // P and O2 have read Q
-                T* out = static_cast<T*>(R.o) + (a + row) * R.o_ts + (int64_t)(h * nq + (nq > 1 ? i : 0)) * R.o_hs;
-#pragma unroll
-                for (int cb = 0; cb < HV; cb += 32) {
-                    if (BF && !emit && !patch) continue;  // the sum goes on in tensor memory
-                    uint32_t r1[32];
-                    __syncwarp();
-                    tmem_ld32(tm + lanes + Z::O1 + wg * HV + cb, r1);
-                    tmem_wait_ld();
-                    if constexpr (!BF) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const float v = __uint_as_float(r1[j]) * p_inv;
-                            oacc[cb + j] = nk > 1 && i > 0 ? oacc[cb + j] + v : v;
-                            r1[j] = __float_as_uint(oacc[cb + j]);
-                        }
-                    }
-                    if (patch) {
-                        // + weight (t, s) v_s where v_s is not finite and s reaches t; weights as O1 took them
+            has_state = true;
+        }
+    }
+
+    // ---- V's scan, K's weights, the state
+    // V of load kv: rows past the chunk's n tokens become 0, and so do NaN and Inf.  fp16: the largest |k|.
+    // (Thread tid has unit tid % 8 of the rows tid / 8 + 32 y of each tile: one offset, 4096 bytes apart.)
+    __device__ __forceinline__ float scan(int kv, int n, int tid) const {
+        unsigned char* Vs = sm + Z::V + (kv & 1) * Z::VBY + tile_at(tid >> 3, tid & 7);
+        const int r0 = tid >> 3;
+        if (OUT && tid < 4) sh.bad[(kv + 2) & 7][tid] = 0;
+        constexpr uint32_t INF = BF ? 0x7f80u : 0x7c00u;
+        if (OUT) {
+            uint4 w[4];
 #pragma unroll 1
-                        for (int s = 0; s < n; ++s) {
-                            if (!(sh.bad[kv & 1][s >> 5] >> (s & 31) & 1)) continue;
-                            __syncwarp();
-                            const uint32_t w2 = tmem_ld1(tm + lanes + Z::P + (s >> 1));
-                            tmem_wait_ld();
-                            const float2 wp = unpack2<T>(w2);
-                            const float w = (s & 1 ? wp.y : wp.x) * p_inv;
-                            if (rev ? s < row : s > row) continue;
-                            const T* vr = static_cast<const T*>(R.v) + (a + s) * R.v_ts +
-                                          (int64_t)(h * nk + (nk > 1 ? i : 0)) * R.v_hs + wg * HV + cb;
+            for (int b = 0; b < DV / 64; ++b, Vs += TILE_BYTES) {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                if (wg * HV + cb + j >= R.dv) break;
-                                const float v = to_acc<float, T>(vr[j]);
-                                if (!(fabsf(v) <= 3.0e38f)) r1[j] = __float_as_uint(__uint_as_float(r1[j]) + w * v);
-                            }
-                        }
-                        if constexpr (!BF) {
+                for (int y = 0; y < 4; ++y) w[y] = *reinterpret_cast<const uint4*>(Vs + y * 4096);
 #pragma unroll
-                            for (int j = 0; j < 32; ++j) oacc[cb + j] = __uint_as_float(r1[j]);
-                        } else if (!emit) {
-                            __syncwarp();
-                            tmem_st32(tm + lanes + Z::O1 + wg * HV + cb, r1);
-                            tmem_wait_st();
-                        }
-                    }
-                    if (emit) {
-                        uint32_t r2[32];
-                        if (has_state) {
-                            __syncwarp();
-                            tmem_ld32(tm + lanes + Z::O2 + wg * HV + cb, r2);
-                            tmem_wait_ld();
-                        }
-                        if (row < n) {
-                            const float w2 = wq * s_inv;
+                for (int y = 0; y < 4; ++y) {
+                    const uint32_t m = __vmaxu2(__vmaxu2(w[y].x & 0x7fff7fffu, w[y].y & 0x7fff7fffu),
+                                                __vmaxu2(w[y].z & 0x7fff7fffu, w[y].w & 0x7fff7fffu));
+                    if (max(m & 0xffffu, m >> 16) >= INF && r0 + 32 * y < n) {
+                        const int r = r0 + 32 * y;
+                        atomicOr(&sh.bad[kv & 7][r >> 5], 1u << (r & 31));
+                        uint32_t q[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                if (wg * HV + cb + u * 8 >= R.dv) break;
-                                uint4 w;
-                                uint32_t* q = &w.x;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const int j = u * 8 + 2 * e;
-                                    float x = __uint_as_float(r1[j]), y = __uint_as_float(r1[j + 1]);
-                                    if (has_state) {
-                                        x = fmaf(w2, __uint_as_float(r2[j]), x);
-                                        y = fmaf(w2, __uint_as_float(r2[j + 1]), y);
-                                    }
-                                    q[e] = pack2<T>(x, y);
-                                }
-                                *reinterpret_cast<uint4*>(out + wg * HV + cb + u * 8) = w;
-                            }
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            q[e] &= ((q[e] & 0x7fffu) >= INF ? 0u : 0xffffu) |
+                                    ((q[e] >> 16 & 0x7fffu) >= INF ? 0u : 0xffff0000u);
+                        *reinterpret_cast<uint4*>(Vs + y * 4096) = make_uint4(q[0], q[1], q[2], q[3]);
                     }
                 }
             }
-            if (conv) {
-                ok &= mbar_wait(&sh.u_done, u_count & 1);
-                ++u_count;
-                tc_fence_after();
-                if (tid == 0) load_kv(kv + 2);  // O1 and U have read K and V
-                const float d = nk > 1 && i > 0 ? 1.0f : whole, us = BF ? u_out : u_out * k_inv;
+        }
+        if (n < TC_C) {
+            Vs = sm + Z::V + (kv & 1) * Z::VBY + tile_at(tid >> 3, tid & 7);
+            for (int b = 0; b < DV / 64; ++b)
+                for (int y = 0; y < 4; ++y)
+                    if (r0 + 32 * y >= n) *reinterpret_cast<uint4*>(Vs + b * TILE_BYTES + y * 4096) = make_uint4(0, 0, 0, 0);
+        }
+        float km = 0.0f;
+        if constexpr (!BF) {
+            const unsigned char* Ks = sm + Z::K + (kv & 1) * Z::KBY + tile_at(tid >> 3, tid & 7);
+            uint32_t m = 0;
 #pragma unroll
-                for (int cb = 0; cb < HV; cb += 32) {
-                    uint32_t r[32];
-                    __syncwarp();
-                    tmem_ld32(tm + lanes + Z::U + wg * HV + cb, r);
-                    tmem_wait_ld();
+            for (int x = 0; x < DK / 64 * 4; ++x) {
+                if (r0 + 32 * (x & 3) >= n) continue;
+                const uint4 w = *reinterpret_cast<const uint4*>(Ks + (x >> 2) * TILE_BYTES + (x & 3) * 4096);
+                m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
+                                         __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+            }
+            m = max(m & 0xffffu, m >> 16);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        S[cb + j] = fmaf(d, S[cb + j], us * __uint_as_float(r[j]));
-                    }
-                }
-                if (patch && row < R.dk) {
+            for (int s = 16; s > 0; s >>= 1) m = max(m, __shfl_xor_sync(FULL, m, s));
+            km = __half2float(__ushort_as_half((unsigned short)m));  // of the warp
+        }
+        fence_proxy_async();
+        if (OUT) arrive(&sh.v_ready[kv & 1]);
+        return km;
+    }
+
+    // K of load kv, times g1 e^{lam d} (and k_up, fp16), as a sum of 16-bit parts
+    __device__ __forceinline__ void weigh(int kv, int n, float k_up, int tid) const {
+        const uint32_t at0 = tile_at(tid >> 3, tid & 7);
+        unsigned char* Ks = sm + Z::K + (kv & 1) * Z::KBY + at0;
+        unsigned char* Ls = sm + Z::LO + at0;
+        const int r0 = tid >> 3, d0 = rev ? r0 : n - 1 - r0, dd = rev ? 32 : -32;
+        if (exact) {
 #pragma unroll 1
-                    for (int s = 0; s < n; ++s) {
-                        if (!(sh.bad[kv & 1][s >> 5] >> (s & 31) & 1)) continue;
-                        const int64_t head = h * nk + (nk > 1 ? i : 0);
-                        const float kw = u_out * sh.wk[s] * to_acc<float, T>(static_cast<const T*>(R.k)[(a + s) * R.k_ts + head * R.k_hs + row]);
-                        const T* vr = static_cast<const T*>(R.v) + (a + s) * R.v_ts + head * R.v_hs + wg * HV;
+            for (int x = 0; x < DK / 64 * 4; ++x) {
+                const uint32_t at = (x >> 2) * TILE_BYTES + (x & 3) * 4096;
+                const uint4 w = *reinterpret_cast<const uint4*>(Ks + at);
+                uint4 p0, p1, p2;
+                const float f = sh.dec[(d0 + (x & 3) * dd) & 127] * k_up;
+                const uint32_t* q = &w.x;
+                uint32_t *a0 = &p0.x, *a1 = &p1.x, *a2 = &p2.x;
 #pragma unroll
-                        for (int j = 0; j < HV; ++j) {
-                            if (wg * HV + j >= R.dv) break;
-                            const float v = to_acc<float, T>(vr[j]);
-                            if (!(fabsf(v) <= 3.0e38f)) S[j] = fmaf(kw, v, S[j]);
-                        }
+                for (int e = 0; e < 4; ++e) {
+                    float2 v = unpack2<T>(q[e]);
+                    v = make_float2(v.x * f, v.y * f);
+                    a0[e] = pack2<T>(v.x, v.y);
+                    float2 g = unpack2<T>(a0[e]);
+                    // (Inf - Inf: the first part says it)
+                    v = make_float2(fabsf(g.x) <= 3.3e38f ? v.x - g.x : 0.0f, fabsf(g.y) <= 3.3e38f ? v.y - g.y : 0.0f);
+                    a1[e] = pack2<T>(v.x, v.y);
+                    if constexpr (BF) {
+                        g = unpack2<T>(a1[e]);
+                        a2[e] = pack2<T>(v.x - g.x, v.y - g.y);
                     }
                 }
-                if (last) {
-                    has_state = true;
-                    if (OUT && c + 1 < nch) store_state();
+                if (r0 + 32 * (x & 3) >= n) p0 = p1 = p2 = make_uint4(0, 0, 0, 0);  // not 0 * NaN
+                *reinterpret_cast<uint4*>(Ks + at) = p0;
+                *reinterpret_cast<uint4*>(Ls + at) = p1;
+                if constexpr (BF) *reinterpret_cast<uint4*>(sm + Z::S + at0 + at) = p2;
+            }
+        } else {
+            const uint32_t up = BF ? 0u : pack2<T>(k_up, k_up), zero = 0x80008000u;  // x y + -0 = x y
+            constexpr uint32_t INF = BF ? 0x7f80u : 0x7c00u;
+#pragma unroll 1
+            for (int b = 0; b < DK / 64; ++b, Ks += TILE_BYTES, Ls += TILE_BYTES) {
+                uint4 w[4];
+                uint2 f[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    w[y] = *reinterpret_cast<const uint4*>(Ks + y * 4096);
+                    f[y] = sh.dec2[(d0 + y * dd) & 127];
                 }
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    uint4 hi, lo;
+                    uint32_t *q = &w[y].x, *qh = &hi.x, *ql = &lo.x, any = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if constexpr (!BF) q[e] = Pair<T>::fma(q[e], up, zero);  // exact
+                        // k (f1 + f2): hi = rn(k f1), k f1 - hi exactly, + k f2
+                        qh[e] = Pair<T>::fma(q[e], f[y].x, zero);
+                        ql[e] = Pair<T>::fma(q[e], f[y].y, Pair<T>::fma(q[e], f[y].x, qh[e] ^ 0x80008000u));
+                        any = __vmaxu2(any, qh[e] & 0x7fff7fffu);
+                    }
+                    if (max(any & 0xffffu, any >> 16) >= INF) {  // (Inf - Inf: the first part says it)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            ql[e] &= ((qh[e] & 0x7fffu) >= INF ? 0u : 0xffffu) |
+                                     ((qh[e] >> 16 & 0x7fffu) >= INF ? 0u : 0xffff0000u);
+                    }
+                    if (r0 + 32 * y >= n) hi = lo = make_uint4(0, 0, 0, 0);  // not 0 * NaN
+                    *reinterpret_cast<uint4*>(Ks + y * 4096) = hi;
+                    *reinterpret_cast<uint4*>(Ls + y * 4096) = lo;
+                }
+            }
+        }
+        fence_proxy_async();
+    }
+
+    // Where V of load kv has a NaN or Inf (and 0 in shared memory): adds weight(s) v_s, to this
+    // warp's rows that s reaches, in the HV columns of tensor memory at D.  (Rare: a column at a time.)
+    template <typename Weight, typename Reach>
+    __device__ __forceinline__ void mend(uint32_t D, int kv, int64_t a, int n, Weight weight, Reach reach) const {
+        const int wg = (threadIdx.x / 128) & 1;
+        const uint32_t* rows = sh.bad[kv & 7];
+#pragma unroll 1
+        for (int s = 0; s < n; ++s) {
+            if (!(rows[s >> 5] >> (s & 31) & 1)) continue;
+            __syncwarp();
+            const float w = weight(s);
+            const bool hit = reach(s);
+            const T* v = static_cast<const T*>(R.v) + (a + s) * R.v_ts + (int64_t)(h * nk + kv % nk) * R.v_hs + wg * HV;
+#pragma unroll 1
+            for (int j = 0; j < HV && wg * HV + j < R.dv; ++j) {
+                const float x = to_acc<float, T>(v[j]);
+                if (fabsf(x) <= 3.0e38f) continue;  // (one value for the warp)
+                __syncwarp();
+                const uint32_t d = tmem_ld1(D + j);
+                tmem_wait_ld();
+                tmem_st1(D + j, hit ? __float_as_uint(fmaf(w, x, __uint_as_float(d))) : d);
+                tmem_wait_st();
             }
         }
     }
-    if (!ok || stop) {
-        // a copy or a product did not come: report it, and let the copies in flight land
-        if (tid == 0) {
-            set_status(A.status, ST_TIMEOUT);
-            mbar_wait(&sh.kv_full[0], 0);
-            mbar_wait(&sh.kv_full[1], 0);
-            mbar_wait(&sh.q_full, 0);
+
+    // The state, in tensor memory in units of 1 / up, with what a NaN or Inf of V of load kv
+    // reaches: rounded into shared memory as the B operand of O2 (which: its number);
+    // scaled for the next U; or out into memory.
+    __device__ __forceinline__ void pass(int tid, bool bad, int kv, int64_t a, int n, float up, bool round, int which,
+                                         bool scale, float factor, float* out) const {
+        const int warp = tid >> 5, lane = tid & 31, wg = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t St = tm + ((uint32_t)((warp & 3) * 32) << 16) + Z::U + wg * HV;
+        if (bad) {
+            const float f = g1 * up / up1;
+            mend(St, kv, a, n, [&](int s) {
+                return row < R.dk ? f * exp2f(l2 * (float)(rev ? s : n - 1 - s)) *
+                                        to_acc<float, T>(static_cast<const T*>(
+                                            R.k)[(a + s) * R.k_ts + (int64_t)(h * nk + kv % nk) * R.k_hs + row])
+                                  : 0.0f;
+            }, [](int) { return true; });
         }
-    } else if (R.state_out && row < R.dk) {
-        float* p = R.state_out + (R.out_by_slot ? by_slot : by_seq) * R.dk * R.dv + row * ri;
+        float s_up = 1.0f / up;
+        if (!BF && round) {
+            float m = 0.0f;
+#pragma unroll 1
+            for (int cb = 0; cb < HV; cb += 32) {
+                uint32_t r[32];
+                __syncwarp();
+                tmem_ld32(St + cb, r);
+                tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < HV; ++c)
-            if (wg * HV + c < R.dv) p[(wg * HV + c) * ci] = S[c];
+                for (int j = 0; j < 32; ++j) {
+                    const float v = fabsf(__uint_as_float(r[j]));
+                    m = v <= 3.0e38f ? fmaxf(m, v) : m;  // (NaN and Inf stay what they are at any scale)
+                }
+            }
+            if (row >= R.dk) m = 0.0f;  // (dk < 128: rows that repeat others or hold nothing)
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, s));
+            if (lane == 0) sh.red[1][warp] = m;
+            group_sync<1>();
+#pragma unroll
+            for (int w = 0; w < 8; ++w) m = fmaxf(m, sh.red[1][w]);
+            s_up = scale_to_fp16(m);
+            if (tid == 0) sh.s_inv[which & 1] = 1.0f / (s_up * up);
+        }
+#pragma unroll 1
+        for (int cb = 0; cb < HV; cb += 32) {
+            uint32_t r[32];
+            __syncwarp();
+            tmem_ld32(St + cb, r);
+            tmem_wait_ld();
+            if (round && row < DK) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint4 w;
+                    uint32_t* q = &w.x;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = __uint_as_float(r[u * 8 + 2 * e]), y = __uint_as_float(r[u * 8 + 2 * e + 1]);
+                        q[e] = BF ? pack2<T>(x, y) : pack2<T>(x * s_up, y * s_up);
+                    }
+                    const int at = wg * HV + cb + u * 8;
+                    *reinterpret_cast<uint4*>(sm + Z::S + (at >> 6) * (DK * 128) + tile_at(row, (at & 63) >> 3)) = w;
+                }
+            }
+            if (scale) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * factor);
+                __syncwarp();
+                tmem_st32(St + cb, r);
+            }
+            if (out && row < R.dk) {
+                const float inv = 1.0f / up;
+                const int64_t ri = R.transposed ? 1 : R.dv, ci = R.transposed ? R.dk : 1;
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int col = wg * HV + cb + j;
+                    if (col < R.dv) out[row * ri + col * ci] = __uint_as_float(r[j]) * inv;
+                }
+            }
+        }
+        if (round) {
+            fence_proxy_async();
+            arrive(&sh.s_ready);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+    }
+
+    // fp16: the power of two for K, from the warps' maxima
+    __device__ __forceinline__ float k_scale(float km, int tid) const {
+        if constexpr (BF) return 1.0f;
+        group_sync<1>();
+        if ((tid & 31) == 0) sh.red[0][tid >> 5] = km;
+        group_sync<1>();
+        float m = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) m = fmaxf(m, sh.red[0][w]);
+        return fminf(scale_to_fp16(m), 32768.0f);
+    }
+
+    __device__ __forceinline__ void states(int tid) const {
+        const int warp = tid >> 5, lane = tid & 31, wg = warp >> 2, row = (warp & 3) * 32 + lane;
+        const int64_t by_slot = (int64_t)slot * A.H + h, by_seq = (int64_t)seq * A.H + h;
+        const int64_t ri = R.transposed ? 1 : R.dv, ci = R.transposed ? R.dk : 1;
+        const float* in = R.state_in ? R.state_in + (R.in_by_slot ? by_slot : by_seq) * R.dk * R.dv + row * ri : nullptr;
+        float* out = R.state_out ? R.state_out + (R.out_by_slot ? by_slot : by_seq) * R.dk * R.dv : nullptr;
+        if (nch == 0) {
+            if (out && row < R.dk)
+                for (int c = wg * HV; c < min(R.dv, wg * HV + HV); ++c) out[row * ri + c * ci] = in ? in[c * ci] : 0.0f;
+            return;
+        }
+        int n;
+        int64_t a = chunk_at(0, &n);
+        if (in) {
+            const uint32_t St = tm + ((uint32_t)((warp & 3) * 32) << 16) + Z::U + wg * HV;
+#pragma unroll 1
+            for (int cb = 0; cb < HV; cb += 32) {
+                uint32_t r[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    const int col = wg * HV + cb + j;
+                    r[j] = row < R.dk && col < R.dv ? __float_as_uint(in[col * ci]) : 0u;
+                }
+                __syncwarp();
+                tmem_st32(St + cb, r);
+            }
+            tmem_wait_st();
+        }
+        if (!wait(&sh.kv_full[0], 0)) return;
+        float k_up = k_scale(scan(0, n, tid), tid);
+        if (in) pass(tid, false, 0, 0, 0, 1.0f, OUT, 0, true, exp2f(l2 * (float)n) * (k_up * up1), nullptr);
+        const int n_kv = nch * nk;
+        for (int kv = 0, us = 0; kv < n_kv; ++kv) {  // (a chunk's q-heads share one load)
+            const int c = kv / nk;
+            a = chunk_at(c, &n);
+            // P has read K (and O2 the state, in whose place the third part goes)
+            if (OUT && !wait(&sh.k_free, us)) return;
+            weigh(kv, n, k_up, tid);
+            arrive(&sh.k_ready);
+            const float up = k_up * up1;
+            const bool more = kv + 1 < n_kv;
+            const int c2 = (kv + 1) / nk;
+            int n2 = 0;
+            if (more) {  // the next load's scan, while U runs
+                chunk_at(c2, &n2);
+                if (!wait(&sh.kv_full[(kv + 1) & 1], (kv + 1) >> 1)) return;
+                k_up = k_scale(scan(kv + 1, n2, tid), tid);
+            }
+            if (!wait(&sh.u_done, us)) return;
+            ++us;
+            tc_fence_after();
+            const uint32_t* rows = sh.bad[kv & 7];
+            const bool bad = OUT && (rows[0] | rows[1] | rows[2] | rows[3]);
+            if (more) {
+                const float factor = (c2 != c ? exp2f(l2 * (float)n2) : 1.0f) * (k_up * up1 / up);
+                if (!BF || c2 != c || bad)
+                    pass(tid, bad, kv, a, n, up, OUT && c2 != c, R.state_in ? c2 : c2 - 1, true, factor, nullptr);
+            } else if (out)
+                pass(tid, bad, kv, a, n, up, false, 0, false, 1.0f, out);
+        }
+    }
+
+    // ---- P's weights and the outputs
+    // 16 columns base .. of row `row` of P, weighted; tw: the warp's first row
+    __device__ __forceinline__ void weights(uint32_t (&r)[16], int base, int row, int tw, int n) const {
+        if (rev ? base + 15 < tw || base >= n : base > tw + 31) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[j] = 0;
+            return;
+        }
+        const float* w = sh.wt + TC_C + row - base;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float f = w[-j], p = __uint_as_float(r[j]) * f;
+            r[j] = f != 0.0f ? __float_as_uint(p) : 0u;  // not 0 * NaN
+        }
+        if (n < TC_C) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (base + j >= n) r[j] = 0;
+        }
+    }
+
+    __device__ __forceinline__ void rows(int tid) const {
+        const int warp = tid >> 5, lane = tid & 31, wg = warp >> 2, row = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int tw = (warp & 3) * 32;
+        const uint32_t Pc = tm + lanes + Z::P + wg * 64;  // this warp's columns of P, and of the rounded weights
+        const uint32_t O1 = tm + lanes + Z::O1 + wg * HV, O2 = tm + lanes + Z::O2 + wg * HV;
+        float up = 1.0f;  // fp16: the scale of this row's weights and of O1
+        int item = 0;
+        for (int c = 0; c < nch; ++c) {
+            int n;
+            const int64_t a = chunk_at(c, &n);
+            const bool has_state = c > 0 || R.state_in;
+            const float wq = R.sq * exp2f(l2 * (float)(rev ? n - 1 - row : row + 1));
+            for (int i = 0; i < G; ++i, ++item) {
+                const int kv = c * nk + (nk > 1 ? i : 0), qi = c * nq + (nq > 1 ? i : 0);
+                const bool emit = nq > 1 || i == G - 1;
+                if (!wait(&sh.p_done, item)) return;
+                tc_fence_after();
+                // 16 columns at a time, the next ones on their way
+                const float before = up;
+                uint32_t r[2][16], pk[8];
+                float m = 0.0f;
+                __syncwarp();
+                tmem_ld16(Pc, r[0]);
+                tmem_wait_ld();
+#pragma unroll 1
+                for (int x = 0; x < 64; x += 32) {
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        __syncwarp();
+                        if (y == 0 || x == 0) tmem_ld16(Pc + x + y * 16 + 16, r[y ^ 1]);
+                        weights(r[y], wg * 64 + x + y * 16, row, tw, n);
+                        __syncwarp();
+                        if constexpr (BF) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                pk[j] = pack2<T>(__uint_as_float(r[y][2 * j]), __uint_as_float(r[y][2 * j + 1]));
+                            tmem_st8(Pc + (x + y * 16) / 2, pk);  // over columns that have been read
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float v = fabsf(__uint_as_float(r[y][j]));
+                                m = v <= 3.0e38f ? fmaxf(m, v) : m;  // (NaN and Inf stay what they are at any scale)
+                            }
+                            tmem_st16(Pc + x + y * 16, r[y]);
+                        }
+                        tmem_wait_ld();
+                    }
+                }
+                if constexpr (!BF) {
+                    const int e = (int)(__float_as_uint(m) >> 23);  // (m is finite)
+                    sh.rexp[wg][row] = (uint8_t)e;
+                    group_sync<2>();
+                    const float fresh = scale_of_exponent(max(e, (int)sh.rexp[wg ^ 1][row]));
+                    group_sync<2>();
+                    // heads that sum into one O1 share a scale that only falls
+                    const bool sum = nk > 1 && i > 0;
+                    up = sum ? fminf(before, fresh) : fresh;
+                    tmem_wait_st();
+#pragma unroll 1
+                    for (int x = 0; x < 64; x += 16) {
+                        __syncwarp();
+                        tmem_ld16(Pc + x, r[0]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            pk[j] = pack2<T>(__uint_as_float(r[0][2 * j]) * up, __uint_as_float(r[0][2 * j + 1]) * up);
+                        tmem_st8(Pc + x / 2, pk);
+                    }
+                    if (sum) {
+                        const float f = up / before;
+#pragma unroll 1
+                        for (int cb = 0; cb < HV; cb += 16) {
+                            __syncwarp();
+                            tmem_ld16(O1 + cb, r[0]);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) r[0][j] = __float_as_uint(__uint_as_float(r[0][j]) * f);
+                            tmem_st16(O1 + cb, r[0]);
+                        }
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(&sh.p_ready);
+                if (!wait(&sh.v_ready[kv & 1], kv >> 1)) return;  // (the rows with NaN or Inf are known)
+                if (!wait(&sh.o_done, item)) return;
+                if (emit && !wait(&sh.o2_done, qi)) return;
+                tc_fence_after();
+                const uint32_t* bad = sh.bad[kv & 7];
+                const bool patch = bad[0] | bad[1] | bad[2] | bad[3];
+                const float w1 = BF ? 1.0f : 1.0f / up;
+                const float w2 = BF ? wq : wq * (has_state ? sh.s_inv[(R.state_in ? c : c - 1) & 1] : 1.0f);
+                T* out = static_cast<T*>(R.o) + (a + row) * R.o_ts + (int64_t)(h * nq + (nq > 1 ? i : 0)) * R.o_hs + wg * HV;
+                if (patch)  // weights as O1 took them
+                    mend(O1, kv, a, n, [&](int s) {
+                        const uint32_t w = tmem_ld1(tm + lanes + Z::P + (s >> 6) * 64 + ((s & 63) >> 1));
+                        tmem_wait_ld();
+                        const float2 x = unpack2<T>(w);
+                        return s & 1 ? x.y : x.x;
+                    }, [&](int s) { return rev ? s >= row : s <= row; });
+                if (emit) {
+                    uint32_t q[2][16];
+                    __syncwarp();
+                    tmem_ld16(O1, r[0]);
+                    if (has_state) tmem_ld16(O2, q[0]);
+                    tmem_wait_ld();
+#pragma unroll 1
+                    for (int cb = 0; cb < HV; cb += 32) {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            __syncwarp();
+                            if (y == 0 || cb + 32 < HV) {
+                                tmem_ld16(O1 + cb + y * 16 + 16, r[y ^ 1]);
+                                if (has_state) tmem_ld16(O2 + cb + y * 16 + 16, q[y ^ 1]);
+                            }
+                            if (row < n) {
+#pragma unroll
+                                for (int u = 0; u < 2; ++u) {
+                                    const int at = cb + y * 16 + u * 8;
+                                    if (wg * HV + at >= R.dv) break;
+                                    uint32_t w[4];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        const int j = u * 8 + 2 * e;
+                                        float p = __uint_as_float(r[y][j]), s = __uint_as_float(r[y][j + 1]);
+                                        if constexpr (!BF) {
+                                            p *= w1;
+                                            s *= w1;
+                                        }
+                                        if (has_state) {
+                                            p = fmaf(w2, __uint_as_float(q[y][j]), p);
+                                            s = fmaf(w2, __uint_as_float(q[y][j + 1]), s);
+                                        }
+                                        w[e] = pack2<T>(p, s);
+                                    }
+                                    *reinterpret_cast<uint4*>(out + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                                }
+                            }
+                            tmem_wait_ld();
+                        }
+                    }
+                }
+                tc_fence_before();
+                arrive(&sh.o_read);
+            }
+        }
+    }
+};
+
+template <typename T, int DK, int DV, bool OUT>
+__global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT, 1) k_lin_tc(const __grid_constant__ TcArgs A) {
+    using Z = TcSize<DK, DV, OUT>;
+    extern __shared__ __align__(1024) unsigned char sm[];
+    TcShared& sh = *reinterpret_cast<TcShared*>(sm + Z::TILES);
+    const TcRole& R = A.role[blockIdx.x % A.nroles];
+    const int slot = blockIdx.x / A.nroles, h = blockIdx.y, tid = threadIdx.x;
+    int seq, len;
+    int64_t t0;
+    if (!A.S.find(slot, &seq, &t0, &len)) return;
+    const bool rev = R.reverse;
+    if (!OUT && R.skip_last && (rev ? t0 == A.S.at(seq) : t0 + len == A.S.at(seq + 1))) return;
+    if (smem_u32(sm) & 1023u) {  // the swizzle goes by address bits: the tiles must start on 1024 bytes
+        if (tid == 0) set_status(A.status, ST_TIMEOUT);
+        return;
+    }
+    constexpr int ISSUE = (OUT ? 2 : 1) * TC_GROUP / 32;  // the issuing warp
+    if (tid == 0) {
+        for (uint64_t* b : {&sh.kv_full[0], &sh.kv_full[1], &sh.q_full, &sh.p_done, &sh.k_free, &sh.o2_done, &sh.o_done, &sh.u_done})
+            mbar_init(b, 1);
+        for (uint64_t* b : {&sh.v_ready[0], &sh.v_ready[1], &sh.k_ready, &sh.s_ready, &sh.p_ready, &sh.o_read})
+            mbar_init(b, TC_GROUP / 32);
+        sh.dead = 0;
+        fence_proxy_async();
+    }
+    __syncwarp();
+    if (tid / 32 == ISSUE) tmem_alloc(&sh.tmem, Z::COLS);
+    const float l2 = clamp_lam(A.lam[h]) * 1.44269504088896341f;
+    if (tid < 32) sh.bad[tid >> 2][tid & 3] = 0;
+    const bool exact = R.state_out && R.exact;
+    // K's weights are g1 e^{lam d}, d >= 0.  fp16: a fast decay (reversed) or a small scale
+    // would sink all of them, so a power of two goes from g1 into the state's unit.
+    float g1 = R.sk * (rev ? exp2f(l2) : 1.0f), up1 = 1.0f;
+    if (std::is_same<T, __half>::value) {
+        const int e = (int)(__float_as_uint(g1) >> 23 & 255) - 127;
+        up1 = __uint_as_float((uint32_t)(127 - min(max(e, -40), 40)) << 23);
+        g1 *= up1;
+    }
+    if (tid < TC_C) {
+        const float e = exp2f(l2 * (float)tid), d = g1 * e;
+        sh.wt[TC_C + (rev ? -tid : tid)] = R.sq * R.sk * e;
+        sh.wt[(rev ? TC_C + 1 + tid : tid) % (2 * TC_C)] = 0.0f;
+        if (exact) sh.dec[tid] = d;
+        else {
+            const uint32_t hi = pack2<T>(d, d), lo = pack2<T>(d - unpack2<T>(hi).x, d - unpack2<T>(hi).x);
+            sh.dec2[tid] = make_uint2(hi, lo);
+        }
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    tc_fence_after();
+    const int nch = (len + TC_C - 1) / TC_C;
+    const TcBlock<T, DK, DV, OUT> B{A,   R,   sm,  sh,   smem_u32(sm), sh.tmem, slot, h,   seq, len, nch,
+                                    R.nq, R.nk, max(R.nq, R.nk), t0, rev, exact, l2, g1, up1};
+    if constexpr (OUT) {
+        // registers: 640 threads x 96 (61440) >= 512 x 104 + 128 x 56 (60416)
+        if (tid < TC_GROUP) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+            B.states(tid);
+        } else if (tid < 2 * TC_GROUP) {
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+            B.rows(tid - TC_GROUP);
+        } else {
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+            if (tid == 2 * TC_GROUP) B.issue();
+        }
+    } else {
+        if (tid < TC_GROUP) B.states(tid);
+        else if (tid == TC_GROUP) B.issue();
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (sh.dead && tid == 0) {
+        // a copy or a product did not come: report it, and let the copies in flight land
+        set_status(A.status, ST_TIMEOUT);
+        mbar_wait(&sh.kv_full[0], 0);
+        mbar_wait(&sh.kv_full[1], 0);
+        mbar_wait(&sh.q_full, 0);
+    }
+    if (tid / 32 == ISSUE) {
         tc_fence_after();
-        tmem_free(tm, Z::COLS);
+        tmem_free(sh.tmem, Z::COLS);
     }
 }
 
@@ -686,13 +978,15 @@ static cudaError_t tc_launch(const TcArgs& A, cudaStream_t st) {
     constexpr size_t smem = TcSize<DK, DV, OUT>::BYTES;
     int dev = 0, sms = 0, per = 0;
     cudaError_t e = current_device_sms(&dev, &sms);
-    if (e == cudaSuccess) e = blocks_per_sm<kern>(dev, TC_NT, smem, &per);
+    if (e == cudaSuccess) e = blocks_per_sm<kern>(dev, TcSize<DK, DV, OUT>::NT, smem, &per);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(A.S.slots * A.nroles), (unsigned)A.H);
     if (grid.x == 0) return cudaSuccess;
-    kern<<<grid, TC_NT, smem, st>>>(A);
+    kern<<<grid, TcSize<DK, DV, OUT>::NT, smem, st>>>(A);
     return cudaGetLastError();
 }
+
+static_assert(TcSize<128, 128, true>::BYTES <= 232448, "shared memory of a block");
 
 template <typename T, bool OUT>
 static cudaError_t tc_dims(const TcArgs& A, int dk, int dv, cudaStream_t st) {
@@ -741,6 +1035,7 @@ cudaError_t tc_run(laplex_dtype dt, const LinRole* roles, int count, const LinSe
             R.in_by_slot = L.in_by_slot;
             R.out_by_slot = L.out_by_slot;
             R.skip_last = L.skip_last;
+            R.exact = !state_only || !L.skip_last;
             R.sq = (float)L.sq;
             R.sk = (float)L.sk;
             R.k = L.k.p;

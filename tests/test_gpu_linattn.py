@@ -284,12 +284,16 @@ def test_same_bits_on_every_run():
         assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
-def test_gradients_that_are_not_asked_for():
-    """The C call leaves out what is NULL; the rest is the same."""
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_gradients_that_are_not_asked_for(dt):
+    """The C call leaves out what is NULL and computes the rest.  (16-bit rows: not
+    to the last bit as beside the others, since K's weights take a third part only
+    where a state leaves the call; the bounds against the definition are the same.)"""
     import ctypes
-    c = Case("bf16", [300, 20], 4, 2, 64, 64)
+    c = Case(dt, [300, 20], 4, 2, 64, 64)
     g = c.run_backward()
-    s, _ = X._shape(c.q, c.k, c.v, 2, c.cu, c.lam, c.scale, X.BF16)
+    s, _ = X._shape(c.q, c.k, c.v, 2, c.cu, c.lam, c.scale, X._seq_dt(c.q))
+    r, n = c.backward_ref()
     for keep in ("dq", "dk", "dv", "dstate"):
         new = {n: torch.empty_like(getattr(g, n)) if n == keep else None for n in ("dq", "dk", "dv", "dstate")}
         ws, nb = X._linattn_ws(s, X.LINATTN_BACKWARD, c.q.device)
@@ -297,7 +301,9 @@ def test_gradients_that_are_not_asked_for():
             ctypes.byref(s), X._rows(c.q), X._rows(c.k), X._rows(c.v), X._rows(c.do), X._ptr(c.s0), X._ptr(c.ds),
             X._rows(new["dq"]), X._rows(new["dk"]), X._rows(new["dv"]), X._ptr(new["dstate"]), None, X._ptr(ws), nb,
             X._stream(c.q.device)))
-        assert torch.equal(new[keep], getattr(g, keep)), keep
+        check(new[keep], r[keep], n[keep], tol_acc(dt) if keep == "dstate" else tol_rows(dt), keep)
+        if dt == "fp32":
+            assert torch.equal(new[keep], getattr(g, keep)), keep
 
 
 # ----------------------------------------------------------------------------- single tokens
