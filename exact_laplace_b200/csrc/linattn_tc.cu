@@ -177,6 +177,19 @@ template <> struct Pair<__half> {
     }
 };
 
+// 32 bytes at a 32-byte boundary
+__device__ __forceinline__ void st32(void* p, const uint32_t* a, const uint32_t* b) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]),
+                 "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3])
+                 : "memory");
+}
+__device__ __forceinline__ void ld32(const float* p, uint32_t* r) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(p)
+                 : "memory");
+}
+
 template <int ID> __device__ __forceinline__ void group_sync() {
     asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(TC_GROUP) : "memory");
 }
@@ -223,26 +236,37 @@ struct TcBlock {
         if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
     }
 
-    // ---- copies and products, by one thread
+    // ---- copies and products: by one warp, all lanes of which walk through them together (the
+    // operands of a product are uniform registers), and one of which acts
     __device__ __forceinline__ void load_kv(int i) const {
         if (i >= nch * nk) return;
         int n;
         const int64_t a = chunk_at(i / nk, &n);
         const int head = h * nk + i % nk;
         uint64_t* bar = &sh.kv_full[i & 1];
-        mbar_expect_tx(bar, Z::KBY + Z::VBY);
-        for (int b = 0; b < DK / 64; ++b)
-            tma_load3(sm + Z::K + (i & 1) * Z::KBY + b * TILE_BYTES, &A.map[R.mk], b * 64, head, (int)a, bar);
-        for (int b = 0; b < DV / 64; ++b)
-            tma_load3(sm + Z::V + (i & 1) * Z::VBY + b * TILE_BYTES, &A.map[R.mv], b * 64, head, (int)a, bar);
+        if (elect()) {
+            mbar_expect_tx(bar, Z::KBY + Z::VBY);
+            for (int b = 0; b < DK / 64; ++b)
+                tma_load3(sm + Z::K + (i & 1) * Z::KBY + b * TILE_BYTES, &A.map[R.mk], b * 64, head, (int)a, bar);
+            for (int b = 0; b < DV / 64; ++b)
+                tma_load3(sm + Z::V + (i & 1) * Z::VBY + b * TILE_BYTES, &A.map[R.mv], b * 64, head, (int)a, bar);
+        }
+        __syncwarp();
     }
     __device__ __forceinline__ void load_q(int i) const {
         if (i >= nch * nq) return;
         int n;
         const int64_t a = chunk_at(i / nq, &n);
-        mbar_expect_tx(&sh.q_full, Z::KBY);
-        for (int b = 0; b < DK / 64; ++b)
-            tma_load3(sm + Z::Q + b * TILE_BYTES, &A.map[R.mq], b * 64, h * nq + i % nq, (int)a, &sh.q_full);
+        if (elect()) {
+            mbar_expect_tx(&sh.q_full, Z::KBY);
+            for (int b = 0; b < DK / 64; ++b)
+                tma_load3(sm + Z::Q + b * TILE_BYTES, &A.map[R.mq], b * 64, h * nq + i % nq, (int)a, &sh.q_full);
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ void commit(uint64_t* bar) const {
+        if (elect()) mma_commit(bar);
+        __syncwarp();
     }
     __device__ __forceinline__ void issue() const {
         load_kv(0);
@@ -263,13 +287,16 @@ struct TcBlock {
                     tc_fence_after();
                     constexpr uint32_t id = mma_desc(BF, false, false, 128, 128);
                     const uint64_t dq = tile_desc(smb + Z::Q, 16, 1024), dk = tile_desc(Ka, 16, 1024);
-#pragma unroll 1
-                    for (int s = 0; s < DK / 16; ++s) {
-                        const uint32_t off = ((s >> 2) * TILE_BYTES + (s & 3) * 32) >> 4;
-                        mma_ss(tm + Z::P, dq + off, dk + off, id, s > 0);
+                    if (elect()) {
+#pragma unroll
+                        for (int s = 0; s < DK / 16; ++s) {
+                            const uint32_t off = ((s >> 2) * TILE_BYTES + (s & 3) * 32) >> 4;
+                            mma_ss(tm + Z::P, dq + off, dk + off, id, s > 0);
+                        }
+                        mma_commit(&sh.p_done);
+                        if (conv && !(BF && exact)) mma_commit(&sh.k_free);
                     }
-                    mma_commit(&sh.p_done);
-                    if (conv && !(BF && exact)) mma_commit(&sh.k_free);
+                    __syncwarp();
                 }
                 if (refill >= 0) {  // the last products have read their K and V
                     if (!wait(&sh.u_done, us - 1)) return;
@@ -284,15 +311,18 @@ struct TcBlock {
                             tc_fence_after();
                             constexpr uint32_t id = mma_desc(BF, false, true, 128, DV);
                             const uint64_t dq = tile_desc(smb + Z::Q, 16, 1024), ds = tile_desc(smb + Z::S, DK * 128, 1024);
-#pragma unroll 1
-                            for (int s = 0; s < DK / 16; ++s)
-                                mma_ss(tm + Z::O2, dq + (((s >> 2) * TILE_BYTES + (s & 3) * 32) >> 4), ds + s * (2048 >> 4),
-                                       id, s > 0);
+                            if (elect()) {
+#pragma unroll
+                                for (int s = 0; s < DK / 16; ++s)
+                                    mma_ss(tm + Z::O2, dq + (((s >> 2) * TILE_BYTES + (s & 3) * 32) >> 4),
+                                           ds + s * (2048 >> 4), id, s > 0);
+                            }
+                            __syncwarp();
                         }
-                        mma_commit(&sh.o2_done);
+                        commit(&sh.o2_done);
                     }
-                    if (conv && BF && exact) mma_commit(&sh.k_free);  // K's third part takes the state's place
-                    if (emit && new_q) {  // P and O2 have read Q
+                    if (conv && BF && exact) commit(&sh.k_free);  // K's third part takes the state's place
+                    if (emit && new_q) {                          // P and O2 have read Q
                         if (!wait(&sh.o2_done, qi)) return;
                         load_q(qi + 1);
                     }
@@ -303,27 +333,35 @@ struct TcBlock {
                     constexpr uint32_t id = mma_desc(BF, false, true, 128, DV);
                     const bool more = nk > 1 && i > 0;
                     const uint64_t dv = tile_desc(Va, TILE_BYTES, 1024);
-#pragma unroll 1
-                    for (int s = 0; s < 8; ++s)
-                        mma_ts(tm + Z::O1, tm + Z::P + (s >> 2) * 64 + (s & 3) * 8, dv + s * (2048 >> 4), id, more || s > 0);
-                    mma_commit(&sh.o_done);
+                    if (elect()) {
+#pragma unroll
+                        for (int s = 0; s < 8; ++s)
+                            mma_ts(tm + Z::O1, tm + Z::P + (s >> 2) * 64 + (s & 3) * 8, dv + s * (2048 >> 4), id, more || s > 0);
+                        mma_commit(&sh.o_done);
+                    }
+                    __syncwarp();
                 }
                 if (conv) {
                     if (!wait(&sh.k_ready, us)) return;  // and the state is scaled
                     tc_fence_after();
                     // dk = 64: M stays 128, the second half repeats the first (leading offset 0) and is not read
                     constexpr uint32_t id = mma_desc(BF, true, true, 128, DV), lead = DK == 64 ? 0 : TILE_BYTES;
-                    const int parts = BF && exact ? 3 : 2;
-                    const uint64_t dv = tile_desc(Va, TILE_BYTES, 1024);
-#pragma unroll 1
-                    for (int x = 0; x < parts; ++x) {
-                        const uint64_t dk = tile_desc(x == 0 ? Ka : smb + (x == 1 ? Z::LO : Z::S), lead, 1024);
-#pragma unroll 1
+                    const uint64_t dv = tile_desc(Va, TILE_BYTES, 1024), d0 = tile_desc(Ka, lead, 1024),
+                                   d1 = tile_desc(smb + Z::LO, lead, 1024), d2 = tile_desc(smb + Z::S, lead, 1024);
+                    const bool add = us > 0 || R.state_in;
+                    if (elect()) {
+#pragma unroll
                         for (int s = 0; s < 8; ++s)
-                            mma_ss(tm + Z::U, dk + s * (2048 >> 4), dv + s * (2048 >> 4), id,
-                                   us > 0 || R.state_in || x > 0 || s > 0);
+                            mma_ss(tm + Z::U, d0 + s * (2048 >> 4), dv + s * (2048 >> 4), id, add || s > 0);
+#pragma unroll
+                        for (int s = 0; s < 8; ++s) mma_ss(tm + Z::U, d1 + s * (2048 >> 4), dv + s * (2048 >> 4), id, true);
+                        if (BF && exact) {
+#pragma unroll
+                            for (int s = 0; s < 8; ++s) mma_ss(tm + Z::U, d2 + s * (2048 >> 4), dv + s * (2048 >> 4), id, true);
+                        }
+                        mma_commit(&sh.u_done);
                     }
-                    mma_commit(&sh.u_done);
+                    __syncwarp();
                     ++us;
                     refill = kv + 2;
                 }
@@ -559,10 +597,26 @@ struct TcBlock {
             if (out && row < R.dk) {
                 const float inv = 1.0f / up;
                 const int64_t ri = R.transposed ? 1 : R.dv, ci = R.transposed ? R.dk : 1;
+                if (ci == 1) {
+                    const bool whole = (reinterpret_cast<uintptr_t>(out + row * ri) & 31) == 0;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int col = wg * HV + cb + j;
-                    if (col < R.dv) out[row * ri + col * ci] = __uint_as_float(r[j]) * inv;
+                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * inv);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 8) {
+                        float* p = out + row * ri + wg * HV + cb + j;
+                        if (wg * HV + cb + j >= R.dv) break;
+                        if (whole) st32(p, r + j, r + j + 4);
+                        else {
+                            *reinterpret_cast<uint4*>(p) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+                            *reinterpret_cast<uint4*>(p + 4) = make_uint4(r[j + 4], r[j + 5], r[j + 6], r[j + 7]);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int col = wg * HV + cb + j;
+                        if (col < R.dv) out[row * ri + col * ci] = __uint_as_float(r[j]) * inv;
+                    }
                 }
             }
         }
@@ -604,10 +658,28 @@ struct TcBlock {
 #pragma unroll 1
             for (int cb = 0; cb < HV; cb += 32) {
                 uint32_t r[32];
+                if (ci == 1) {  // (a row is dv values, a multiple of 8)
+                    const bool whole = (reinterpret_cast<uintptr_t>(in) & 31) == 0;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const int col = wg * HV + cb + j;
-                    r[j] = row < R.dk && col < R.dv ? __float_as_uint(in[col * ci]) : 0u;
+                    for (int j = 0; j < 32; j += 8) {
+                        const int col = wg * HV + cb + j;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) r[j + e] = 0;
+                        if (row < R.dk && col < R.dv) {
+                            if (whole) ld32(in + col, r + j);
+                            else {
+                                const uint4 x = *reinterpret_cast<const uint4*>(in + col), y = *reinterpret_cast<const uint4*>(in + col + 4);
+                                r[j] = x.x, r[j + 1] = x.y, r[j + 2] = x.z, r[j + 3] = x.w;
+                                r[j + 4] = y.x, r[j + 5] = y.y, r[j + 6] = y.z, r[j + 7] = y.w;
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        const int col = wg * HV + cb + j;
+                        r[j] = row < R.dk && col < R.dv ? __float_as_uint(in[col * ci]) : 0u;
+                    }
                 }
                 __syncwarp();
                 tmem_st32(St + cb, r);
@@ -634,13 +706,14 @@ struct TcBlock {
                 if (!wait(&sh.kv_full[(kv + 1) & 1], (kv + 1) >> 1)) return;
                 k_up = k_scale(scan(kv + 1, n2, tid), tid);
             }
+            float factor = 1.0f;
+            if (more) factor = (c2 != c ? exp2f(l2 * (float)n2) : 1.0f) * (BF ? 1.0f : k_up * up1 / up);
             if (!wait(&sh.u_done, us)) return;
             ++us;
             tc_fence_after();
             const uint32_t* rows = sh.bad[kv & 7];
             const bool bad = OUT && (rows[0] | rows[1] | rows[2] | rows[3]);
             if (more) {
-                const float factor = (c2 != c ? exp2f(l2 * (float)n2) : 1.0f) * (k_up * up1 / up);
                 if (!BF || c2 != c || bad)
                     pass(tid, bad, kv, a, n, up, OUT && c2 != c, R.state_in ? c2 : c2 - 1, true, factor, nullptr);
             } else if (out)
@@ -657,10 +730,15 @@ struct TcBlock {
             return;
         }
         const float* w = sh.wt + TC_C + row - base;
+        if (rev ? base > tw + 31 : base + 15 < tw) {  // nothing masked
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            const float f = w[-j], p = __uint_as_float(r[j]) * f;
-            r[j] = f != 0.0f ? __float_as_uint(p) : 0u;  // not 0 * NaN
+            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * w[-j]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const float f = w[-j], p = __uint_as_float(r[j]) * f;
+                r[j] = f != 0.0f ? __float_as_uint(p) : 0u;  // not 0 * NaN
+            }
         }
         if (n < TC_C) {
 #pragma unroll
@@ -675,6 +753,8 @@ struct TcBlock {
         const int tw = (warp & 3) * 32;
         const uint32_t Pc = tm + lanes + Z::P + wg * 64;  // this warp's columns of P, and of the rounded weights
         const uint32_t O1 = tm + lanes + Z::O1 + wg * HV, O2 = tm + lanes + Z::O2 + wg * HV;
+        // outputs in whole 32-byte sectors where they start on one
+        const bool wide = ((reinterpret_cast<uintptr_t>(R.o) | (uintptr_t)(R.o_ts * 2) | (uintptr_t)(R.o_hs * 2)) & 31) == 0;
         float up = 1.0f;  // fp16: the scale of this row's weights and of O1
         int item = 0;
         for (int c = 0; c < nch; ++c) {
@@ -805,7 +885,15 @@ struct TcBlock {
                                         }
                                         w[e] = pack2<T>(p, s);
                                     }
-                                    *reinterpret_cast<uint4*>(out + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                                    if (u == 0) {
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e) pk[e] = w[e];
+                                        if (!wide || wg * HV + at + 8 >= R.dv)
+                                            *reinterpret_cast<uint4*>(out + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                                    } else if (wide) {
+                                        st32(out + at - 8, pk, w);
+                                    } else
+                                        *reinterpret_cast<uint4*>(out + at) = make_uint4(w[0], w[1], w[2], w[3]);
                                 }
                             }
                             tmem_wait_ld();
@@ -874,7 +962,7 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT, 1) k_lin_tc(const __g
     const TcBlock<T, DK, DV, OUT> B{A,   R,   sm,  sh,   smem_u32(sm), sh.tmem, slot, h,   seq, len, nch,
                                     R.nq, R.nk, max(R.nq, R.nk), t0, rev, exact, l2, g1, up1};
     if constexpr (OUT) {
-        // registers: 640 threads x 96 (61440) >= 512 x 104 + 128 x 56 (60416)
+        // registers: 640 threads x 96 = 512 x 104 + 128 x 64
         if (tid < TC_GROUP) {
             asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
             B.states(tid);
@@ -882,12 +970,12 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT, 1) k_lin_tc(const __g
             asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
             B.rows(tid - TC_GROUP);
         } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
-            if (tid == 2 * TC_GROUP) B.issue();
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+            if (tid < 2 * TC_GROUP + 32) B.issue();
         }
     } else {
         if (tid < TC_GROUP) B.states(tid);
-        else if (tid == TC_GROUP) B.issue();
+        else B.issue();
     }
     __syncwarp();
     tc_fence_before();

@@ -39,6 +39,13 @@ constexpr uint32_t mma_desc(bool bf16, bool a_mn, bool b_mn, int M, int N) {
            ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(N / 8) << 17) | ((uint32_t)(M / 16) << 24);
 }
 
+// true in one lane of a converged warp
+__device__ __forceinline__ bool elect() {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+    return ok != 0u;
+}
+
 // D (+)= A B, A and B in shared memory; by one thread
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
