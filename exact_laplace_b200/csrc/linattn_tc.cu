@@ -92,10 +92,13 @@ struct TcShared {
     uint32_t tmem;
     uint32_t dead;       // a wait ran out
     uint32_t bad[8][4];  // rows of V with a NaN or Inf, by load
-    float wt[2 * TC_C];  // P's weights scale e^{lam |x|} at TC_C + x, x = row - column; 0 past the diagonal
+    alignas(16) float grow[16];  // e^{lam j}, 16 columns of P towards the row's end
+    float wt[TC_C + 32]; // P's weights scale e^{lam |x|} at 32 + x (reversed: 127 + x), x = row - column; 0 up to 31 past the diagonal
+    // K's weights g1 e^{lam d}, d >= 0, as sums of 16-bit values, each twice
+    uint2 dec2[TC_C];
     union {
-        float dec[TC_C];   // K's weights g1 e^{lam d}, d >= 0 (exact)
-        uint2 dec2[TC_C];  // the same as sums of two 16-bit values, each twice
+        uint32_t dec3[TC_C];  // bf16, exact: the third
+        float dec[TC_C];      // fp16, exact: in fp32
     };
     float s_inv[2];      // fp16: what the rounded state is to be multiplied by, by chunk
     uint8_t rexp[2][TC_C];  // fp16: the exponent of a row's largest weight, by half
@@ -160,22 +163,46 @@ __device__ __forceinline__ float2 mul2(float2 x, float2 y) {
     return r;
 }
 
-// 16-bit pairs: a b + c and a b, each rounded once
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 r;
+    asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+        " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return r;
+}
+__device__ __forceinline__ float2 pair(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
+
+// 16-bit pairs: a b + c, a b, a b - c, each rounded once
 template <typename T> struct Pair;
-template <> struct Pair<__nv_bfloat16> {
-    static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
-        uint32_t r;
-        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-        return r;
-    }
-};
-template <> struct Pair<__half> {
-    static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {
-        uint32_t r;
-        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
-        return r;
-    }
-};
+#define LX_PAIR(T, S)                                                                                      \
+    template <> struct Pair<T> {                                                                           \
+        static __device__ __forceinline__ uint32_t fma(uint32_t a, uint32_t b, uint32_t c) {               \
+            uint32_t r;                                                                                    \
+            asm("fma.rn." S " %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));                         \
+            return r;                                                                                      \
+        }                                                                                                  \
+        static __device__ __forceinline__ uint32_t mul(uint32_t a, uint32_t b) {                           \
+            uint32_t r;                                                                                    \
+            asm("mul.rn." S " %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));                                     \
+            return r;                                                                                      \
+        }                                                                                                  \
+        static __device__ __forceinline__ uint32_t fms(uint32_t a, uint32_t b, uint32_t c) {               \
+            uint32_t r;                                                                                    \
+            asm("{\n .reg .b32 n;\n neg." S " n, %3;\n fma.rn." S " %0, %1, %2, n;\n}\n"                    \
+                : "=r"(r)                                                                                  \
+                : "r"(a), "r"(b), "r"(c));                                                                 \
+            return r;                                                                                      \
+        }                                                                                                  \
+        static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {                           \
+            uint32_t r;                                                                                    \
+            asm("sub.rn." S " %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));                                     \
+            return r;                                                                                      \
+        }                                                                                                  \
+    };
+LX_PAIR(__nv_bfloat16, "bf16x2")
+LX_PAIR(__half, "f16x2")
+#undef LX_PAIR
 
 // 32 bytes at a 32-byte boundary
 __device__ __forceinline__ void st32(void* p, const uint32_t* a, const uint32_t* b) {
@@ -379,25 +406,32 @@ struct TcBlock {
         if (OUT && tid < 4) sh.bad[(kv + 2) & 7][tid] = 0;
         constexpr uint32_t INF = BF ? 0x7f80u : 0x7c00u;
         if (OUT) {
-            uint4 w[4];
+            uint32_t acc[4] = {0, 0, 0, 0};  // sums of x * 0: NaN where an x is NaN or Inf
+#pragma unroll
+            for (int x = 0; x < DV / 64 * 4; ++x) {
+                const uint4 w = *reinterpret_cast<const uint4*>(Vs + (x >> 2) * TILE_BYTES + (x & 3) * 4096);
+                acc[0] = Pair<T>::fma(w.x, 0u, acc[0]);
+                acc[1] = Pair<T>::fma(w.y, 0u, acc[1]);
+                acc[2] = Pair<T>::fma(w.z, 0u, acc[2]);
+                acc[3] = Pair<T>::fma(w.w, 0u, acc[3]);
+            }
+            if ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) {
 #pragma unroll 1
-            for (int b = 0; b < DV / 64; ++b, Vs += TILE_BYTES) {
+                for (int x = 0; x < DV / 64 * 4; ++x) {
+                    const int r = r0 + 32 * (x & 3);
+                    if (r >= n) continue;
+                    uint4* p = reinterpret_cast<uint4*>(Vs + (x >> 2) * TILE_BYTES + (x & 3) * 4096);
+                    uint4 w = *p;
+                    uint32_t q[4] = {w.x, w.y, w.z, w.w}, any = 0;
 #pragma unroll
-                for (int y = 0; y < 4; ++y) w[y] = *reinterpret_cast<const uint4*>(Vs + y * 4096);
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const uint32_t m = __vmaxu2(__vmaxu2(w[y].x & 0x7fff7fffu, w[y].y & 0x7fff7fffu),
-                                                __vmaxu2(w[y].z & 0x7fff7fffu, w[y].w & 0x7fff7fffu));
-                    if (max(m & 0xffffu, m >> 16) >= INF && r0 + 32 * y < n) {
-                        const int r = r0 + 32 * y;
-                        atomicOr(&sh.bad[kv & 7][r >> 5], 1u << (r & 31));
-                        uint32_t q[4] = {w[y].x, w[y].y, w[y].z, w[y].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            q[e] &= ((q[e] & 0x7fffu) >= INF ? 0u : 0xffffu) |
-                                    ((q[e] >> 16 & 0x7fffu) >= INF ? 0u : 0xffff0000u);
-                        *reinterpret_cast<uint4*>(Vs + y * 4096) = make_uint4(q[0], q[1], q[2], q[3]);
+                    for (int e = 0; e < 4; ++e) {
+                        const uint32_t m = ((q[e] & 0x7fffu) >= INF ? 0u : 0xffffu) | ((q[e] >> 16 & 0x7fffu) >= INF ? 0u : 0xffff0000u);
+                        any |= ~m;
+                        q[e] &= m;
                     }
+                    if (!any) continue;
+                    atomicOr(&sh.bad[kv & 7][r >> 5], 1u << (r & 31));
+                    *p = make_uint4(q[0], q[1], q[2], q[3]);
                 }
             }
         }
@@ -433,70 +467,48 @@ struct TcBlock {
         const uint32_t at0 = tile_at(tid >> 3, tid & 7);
         unsigned char* Ks = sm + Z::K + (kv & 1) * Z::KBY + at0;
         unsigned char* Ls = sm + Z::LO + at0;
+        unsigned char* Ms = sm + Z::S + at0;
         const int r0 = tid >> 3, d0 = rev ? r0 : n - 1 - r0, dd = rev ? 32 : -32;
-        if (exact) {
-#pragma unroll 1
-            for (int x = 0; x < DK / 64 * 4; ++x) {
-                const uint32_t at = (x >> 2) * TILE_BYTES + (x & 3) * 4096;
-                const uint4 w = *reinterpret_cast<const uint4*>(Ks + at);
-                uint4 p0, p1, p2;
-                const float f = sh.dec[(d0 + (x & 3) * dd) & 127] * k_up;
-                const uint32_t* q = &w.x;
-                uint32_t *a0 = &p0.x, *a1 = &p1.x, *a2 = &p2.x;
+        using H = Pair<T>;
+#pragma unroll 2
+        for (int x = 0; x < DK / 64 * 4; ++x) {
+            const uint32_t at = (x >> 2) * TILE_BYTES + (x & 3) * 4096;
+            const uint4 w = *reinterpret_cast<const uint4*>(Ks + at);
+            const int d = (d0 + (x & 3) * dd) & 127;
+            const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+            uint32_t a0[4], a1[4], a2[4];
+            if (!BF && exact) {
+                // from fp32 products: weights below fp16's smallest still count
+                const float f = sh.dec[d] * k_up;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float2 v = unpack2<T>(q[e]);
                     v = make_float2(v.x * f, v.y * f);
                     a0[e] = pack2<T>(v.x, v.y);
-                    float2 g = unpack2<T>(a0[e]);
-                    // (Inf - Inf: the first part says it)
-                    v = make_float2(fabsf(g.x) <= 3.3e38f ? v.x - g.x : 0.0f, fabsf(g.y) <= 3.3e38f ? v.y - g.y : 0.0f);
-                    a1[e] = pack2<T>(v.x, v.y);
-                    if constexpr (BF) {
-                        g = unpack2<T>(a1[e]);
-                        a2[e] = pack2<T>(v.x - g.x, v.y - g.y);
-                    }
+                    const float2 g = unpack2<T>(a0[e]);
+                    a1[e] = pack2<T>(v.x - g.x, v.y - g.y);
                 }
-                if (r0 + 32 * (x & 3) >= n) p0 = p1 = p2 = make_uint4(0, 0, 0, 0);  // not 0 * NaN
-                *reinterpret_cast<uint4*>(Ks + at) = p0;
-                *reinterpret_cast<uint4*>(Ls + at) = p1;
-                if constexpr (BF) *reinterpret_cast<uint4*>(sm + Z::S + at0 + at) = p2;
-            }
-        } else {
-            const uint32_t up = BF ? 0u : pack2<T>(k_up, k_up), zero = 0x80008000u;  // x y + -0 = x y
-            constexpr uint32_t INF = BF ? 0x7f80u : 0x7c00u;
-#pragma unroll 1
-            for (int b = 0; b < DK / 64; ++b, Ks += TILE_BYTES, Ls += TILE_BYTES) {
-                uint4 w[4];
-                uint2 f[4];
+            } else {
+                // k (f1 + f2 (+ f3)): the first part rn(k f1); k f1 less it is exact, and with k f2 gives
+                // the second; what that rounds off, with k f3, the third
+                const uint2 f = sh.dec2[d];
+                const uint32_t f3 = BF && exact ? sh.dec3[d] : 0u, up = BF ? 0u : pack2<T>(k_up, k_up);
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    w[y] = *reinterpret_cast<const uint4*>(Ks + y * 4096);
-                    f[y] = sh.dec2[(d0 + y * dd) & 127];
-                }
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    uint4 hi, lo;
-                    uint32_t *q = &w[y].x, *qh = &hi.x, *ql = &lo.x, any = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if constexpr (!BF) q[e] = Pair<T>::fma(q[e], up, zero);  // exact
-                        // k (f1 + f2): hi = rn(k f1), k f1 - hi exactly, + k f2
-                        qh[e] = Pair<T>::fma(q[e], f[y].x, zero);
-                        ql[e] = Pair<T>::fma(q[e], f[y].y, Pair<T>::fma(q[e], f[y].x, qh[e] ^ 0x80008000u));
-                        any = __vmaxu2(any, qh[e] & 0x7fff7fffu);
-                    }
-                    if (max(any & 0xffffu, any >> 16) >= INF) {  // (Inf - Inf: the first part says it)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            ql[e] &= ((qh[e] & 0x7fffu) >= INF ? 0u : 0xffffu) |
-                                     ((qh[e] >> 16 & 0x7fffu) >= INF ? 0u : 0xffff0000u);
-                    }
-                    if (r0 + 32 * y >= n) hi = lo = make_uint4(0, 0, 0, 0);  // not 0 * NaN
-                    *reinterpret_cast<uint4*>(Ks + y * 4096) = hi;
-                    *reinterpret_cast<uint4*>(Ls + y * 4096) = lo;
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t k = BF ? q[e] : H::mul(q[e], up);  // (exact)
+                    a0[e] = H::mul(k, f.x);
+                    const uint32_t left = H::fms(k, f.x, a0[e]);
+                    a1[e] = H::fma(k, f.y, left);
+                    if (BF && exact) a2[e] = H::fma(k, f3, H::fma(k, f.y, H::sub(left, a1[e])));
                 }
             }
+            if (n < TC_C && r0 + 32 * (x & 3) >= n) {  // not 0 * NaN
+#pragma unroll
+                for (int e = 0; e < 4; ++e) a0[e] = a1[e] = a2[e] = 0;
+            }
+            *reinterpret_cast<uint4*>(Ks + at) = make_uint4(a0[0], a0[1], a0[2], a0[3]);
+            *reinterpret_cast<uint4*>(Ls + at) = make_uint4(a1[0], a1[1], a1[2], a1[3]);
+            if (BF && exact) *reinterpret_cast<uint4*>(Ms + at) = make_uint4(a2[0], a2[1], a2[2], a2[3]);
         }
         fence_proxy_async();
     }
@@ -590,7 +602,11 @@ struct TcBlock {
             }
             if (scale) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * factor);
+                for (int j = 0; j < 32; j += 2) {
+                    const float2 x = mul2(pair(r[j], r[j + 1]), make_float2(factor, factor));
+                    r[j] = __float_as_uint(x.x);
+                    r[j + 1] = __float_as_uint(x.y);
+                }
                 __syncwarp();
                 tmem_st32(St + cb, r);
             }
@@ -729,10 +745,21 @@ struct TcBlock {
             for (int j = 0; j < 16; ++j) r[j] = 0;
             return;
         }
-        const float* w = sh.wt + TC_C + row - base;
-        if (rev ? base > tw + 31 : base + 15 < tw) {  // nothing masked
+        const float* w = sh.wt + (rev ? TC_C - 1 : 32) + row - base;
+        if (rev ? base > tw + 31 : base + 15 < tw) {
+            // nothing masked: e^{lam (row - edge)} e^{lam (edge - s)}, edge the nearest column; both at most 1
+            const float f = rev ? w[0] : w[-15];
+            const float4* g = reinterpret_cast<const float4*>(sh.grow);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * w[-j]);
+            for (int j = 0; j < 4; ++j) {
+                const float4 x = g[j];
+                const float2 a = mul2(pair(r[4 * j], r[4 * j + 1]), mul2(make_float2(f, f), make_float2(x.x, x.y)));
+                const float2 b = mul2(pair(r[4 * j + 2], r[4 * j + 3]), mul2(make_float2(f, f), make_float2(x.z, x.w)));
+                r[4 * j] = __float_as_uint(a.x);
+                r[4 * j + 1] = __float_as_uint(a.y);
+                r[4 * j + 2] = __float_as_uint(b.x);
+                r[4 * j + 3] = __float_as_uint(b.y);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
@@ -852,10 +879,14 @@ struct TcBlock {
                     }, [&](int s) { return rev ? s >= row : s <= row; });
                 if (emit) {
                     uint32_t q[2][16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) q[0][j] = q[1][j] = 0;  // (without a state)
                     __syncwarp();
                     tmem_ld16(O1, r[0]);
                     if (has_state) tmem_ld16(O2, q[0]);
                     tmem_wait_ld();
+                    const bool in = row < n;
+                    const int cols = R.dv - wg * HV;
 #pragma unroll 1
                     for (int cb = 0; cb < HV; cb += 32) {
 #pragma unroll
@@ -865,37 +896,21 @@ struct TcBlock {
                                 tmem_ld16(O1 + cb + y * 16 + 16, r[y ^ 1]);
                                 if (has_state) tmem_ld16(O2 + cb + y * 16 + 16, q[y ^ 1]);
                             }
-                            if (row < n) {
 #pragma unroll
-                                for (int u = 0; u < 2; ++u) {
-                                    const int at = cb + y * 16 + u * 8;
-                                    if (wg * HV + at >= R.dv) break;
-                                    uint32_t w[4];
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e) {
-                                        const int j = u * 8 + 2 * e;
-                                        float p = __uint_as_float(r[y][j]), s = __uint_as_float(r[y][j + 1]);
-                                        if constexpr (!BF) {
-                                            p *= w1;
-                                            s *= w1;
-                                        }
-                                        if (has_state) {
-                                            p = fmaf(w2, __uint_as_float(q[y][j]), p);
-                                            s = fmaf(w2, __uint_as_float(q[y][j + 1]), s);
-                                        }
-                                        w[e] = pack2<T>(p, s);
-                                    }
-                                    if (u == 0) {
-#pragma unroll
-                                        for (int e = 0; e < 4; ++e) pk[e] = w[e];
-                                        if (!wide || wg * HV + at + 8 >= R.dv)
-                                            *reinterpret_cast<uint4*>(out + at) = make_uint4(w[0], w[1], w[2], w[3]);
-                                    } else if (wide) {
-                                        st32(out + at - 8, pk, w);
-                                    } else
-                                        *reinterpret_cast<uint4*>(out + at) = make_uint4(w[0], w[1], w[2], w[3]);
-                                }
+                            for (int j = 0; j < 8; ++j) {
+                                float2 p = pair(r[y][2 * j], r[y][2 * j + 1]);
+                                if constexpr (!BF) p = mul2(p, make_float2(w1, w1));
+                                p = fma2(make_float2(w2, w2), pair(q[y][2 * j], q[y][2 * j + 1]), p);
+                                pk[j] = pack2<T>(p.x, p.y);
                             }
+                            const int at = cb + y * 16;
+                            if (in && wide && at + 16 <= cols) {
+                                st32(out + at, pk, pk + 4);
+                            } else if (in) {
+                                if (at < cols) *reinterpret_cast<uint4*>(out + at) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+                                if (at + 8 < cols) *reinterpret_cast<uint4*>(out + at + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+                            }
+                            __syncwarp();
                             tmem_wait_ld();
                         }
                     }
@@ -947,12 +962,17 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT, 1) k_lin_tc(const __g
     }
     if (tid < TC_C) {
         const float e = exp2f(l2 * (float)tid), d = g1 * e;
-        sh.wt[TC_C + (rev ? -tid : tid)] = R.sq * R.sk * e;
-        sh.wt[(rev ? TC_C + 1 + tid : tid) % (2 * TC_C)] = 0.0f;
-        if (exact) sh.dec[tid] = d;
+        if (tid < 16) sh.grow[rev ? tid : 15 - tid] = e;
+        sh.wt[rev ? TC_C - 1 - tid : 32 + tid] = R.sq * R.sk * e;
+        if (tid < 32) sh.wt[rev ? TC_C + tid : tid] = 0.0f;
+        const uint32_t hi = pack2<T>(d, d);
+        float left = d - unpack2<T>(hi).x;
+        const uint32_t lo = pack2<T>(left, left);
+        sh.dec2[tid] = make_uint2(hi, lo);
+        if (std::is_same<T, __half>::value) sh.dec[tid] = d;
         else {
-            const uint32_t hi = pack2<T>(d, d), lo = pack2<T>(d - unpack2<T>(hi).x, d - unpack2<T>(hi).x);
-            sh.dec2[tid] = make_uint2(hi, lo);
+            left -= unpack2<T>(lo).x;
+            sh.dec3[tid] = pack2<T>(left, left);
         }
     }
     tc_fence_before();
