@@ -36,12 +36,15 @@
 // overflows and small ones do not sink below the type's normal range.
 //
 // Causality: a masked weight is 0, and 0 times a NaN or Inf of a later row of V
-// would be NaN.  Each chunk's V is scanned (a few integer operations per 16
-// bytes); non-finite values are replaced by 0 and their products added by hand to
-// the rows that they do reach.
+// is NaN in O1.  A warp that finds an output not finite although its O2 is takes
+// that output from the definition (repair).  The state may keep the NaN: V's
+// token is in it.  (A scan of V before its use cost a read of the tile from
+// shared memory, whose bandwidth the products need.)
 //
-// Bound by memory at full grids: a chunk of dk = dv = 128 moves 128 KB (2.8 us
-// of an SM's share of the measured bandwidth) against 2560 cycles of tensor work.
+// Bounds of a chunk of dk = dv = 128: 128 KB of device memory (2.8 us of an SM's
+// share of the measured bandwidth), 2560 cycles of tensor work, about 5000 cycles
+// of shared memory (operands of the products 2300, copies 770, K's parts 770, the
+// state 256, outputs, tables).
 #include <algorithm>
 #include <atomic>
 
@@ -54,14 +57,15 @@ namespace lx {
 
 constexpr int TC_GROUP = 256;  // threads of the state warps, and of the rows warps
 constexpr int TC_C = 128;  // tokens per chunk
-constexpr uint32_t TILE_BYTES = TC_C * 128;
 
 struct TcRole {
     int mq, mk, mv;  // maps of the operands
     int nq, nk, dk, dv, reverse, transposed, in_by_slot, out_by_slot, skip_last;
     int exact;       // the state that leaves is a result, not only rounded for O2
     float sq, sk;
-    const void* k;   // rows of k and v (for what a NaN or Inf reaches)
+    const void* q;   // rows of q, k and v (for repair)
+    int64_t q_ts, q_hs;
+    const void* k;
     int64_t k_ts, k_hs;
     const void* v;
     int64_t v_ts, v_hs;
@@ -82,34 +86,38 @@ struct alignas(64) TcArgs {
 
 // shared memory behind the tiles
 struct TcShared {
-    uint64_t kv_full[2], q_full;             // copies
+    uint64_t kv_full[4], q_full;             // copies
     // A waiter names a phase by its parity, so no barrier may run two phases ahead of one of
     // its waiters.  (p_done is waited for by the rows warps at every item; k_free says the same
-    // to the state warps where they weigh K; v_ready runs one load ahead, hence two of it.)
-    uint64_t p_done, k_free, o2_done, o_done, u_done;  // products
-    uint64_t v_ready[2], k_ready, s_ready;             // from the state warps
+    // to the state warps where they weigh K; v_ready, k_ready and u_done run one load ahead: two of each.)
+    uint64_t p_done, k_free, o2_done, o_done, u_done[2];  // products
+    uint64_t v_ready[2], k_ready[2], s_ready;          // from the state warps
     uint64_t p_ready, o_read;                          // from the rows warps
     uint32_t tmem;
     uint32_t dead;       // a wait ran out
-    uint32_t bad[8][4];  // rows of V with a NaN or Inf, by load
     alignas(16) float grow[16];  // e^{lam j}, 16 columns of P towards the row's end
     float wt[TC_C + 32]; // P's weights scale e^{lam |x|} at 32 + x (reversed: 127 + x), x = row - column; 0 up to 31 past the diagonal
     // K's weights g1 e^{lam d}, d >= 0, as sums of 16-bit values, each twice
     uint2 dec2[TC_C];
     union {
-        uint32_t dec3[TC_C];  // bf16, exact: the third
-        float dec[TC_C];      // fp16, exact: in fp32
+        uint32_t dec3[TC_C];  // bf16, products: the third
+        float dec[TC_C];      // fp16, and the state pass: in fp32
     };
     float s_inv[2];      // fp16: what the rounded state is to be multiplied by, by chunk
     uint8_t rexp[2][TC_C];  // fp16: the exponent of a row's largest weight, by half
     float red[2][8];     // fp16: maxima of the state warps
 };
 
-template <int DK, int DV, bool OUT> struct TcSize {
-    static constexpr uint32_t KBY = DK / 64 * TILE_BYTES, VBY = DV / 64 * TILE_BYTES;
-    // the rounded state, and in its place K's third part between O2 and the next state
-    static constexpr uint32_t SBY = OUT && DK * 128 * (DV / 64) > KBY ? DK * 128 * (DV / 64) : KBY;
-    static constexpr uint32_t K = 0, V = 2 * KBY, LO = V + 2 * VBY, S = LO + KBY, Q = S + SBY;
+// CH tokens at a time.  The state pass of bf16 takes 64, in four stages: it only streams K and
+// V, and two stages of 128 left the copies' latency (about 3500 cycles under load) in the open.
+template <int DK, int DV, bool OUT, bool BF> struct TcSize {
+    static constexpr int CH = OUT || !BF ? 128 : 64, STAGES = CH == 64 ? 4 : 2;
+    static constexpr uint32_t TB = CH * 128;  // bytes of a tile of 64 columns
+    static constexpr uint32_t KBY = DK / 64 * TB, VBY = DV / 64 * TB;
+    // K's lower parts.  Products: the second in LO, the third (bf16) in the place of the rounded
+    // state between O2 and the next state.  State pass of bf16: two buffers of both.
+    static constexpr uint32_t SBY = OUT && DK * 128 * (DV / 64) > KBY ? DK * 128 * (DV / 64) : OUT ? KBY : BF ? 3 * KBY : 0;
+    static constexpr uint32_t K = 0, V = STAGES * KBY, LO = V + STAGES * VBY, S = LO + KBY, Q = S + SBY;
     static constexpr uint32_t TILES = Q + (OUT ? KBY : 0);
     static constexpr uint32_t BYTES = TILES + sizeof(TcShared);
     // tensor memory columns: P, O1, O2, U.  The rounded weights of P's columns 0-63
@@ -224,8 +232,10 @@ template <int ID> __device__ __forceinline__ void group_sync() {
 // What every warp of a block knows.
 template <typename T, int DK, int DV, bool OUT>
 struct TcBlock {
-    using Z = TcSize<DK, DV, OUT>;
     static constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
+    using Z = TcSize<DK, DV, OUT, BF>;
+    static constexpr int CH = Z::CH, NS = Z::STAGES;
+    static constexpr uint32_t TB = Z::TB;
     static constexpr int HV = DV / 2;  // columns of a thread of the state and of the outputs
 
     const TcArgs& A;
@@ -240,10 +250,10 @@ struct TcBlock {
 
     __device__ __forceinline__ int64_t chunk_at(int c, int* n) const {
         if (!rev) {
-            *n = min(TC_C, len - c * TC_C);
-            return t0 + (int64_t)c * TC_C;
+            *n = min(CH, len - c * CH);
+            return t0 + (int64_t)c * CH;
         }
-        const int end = len - c * TC_C, a = max(end - TC_C, 0);
+        const int end = len - c * CH, a = max(end - CH, 0);
         *n = end - a;
         return t0 + a;
     }
@@ -270,13 +280,13 @@ struct TcBlock {
         int n;
         const int64_t a = chunk_at(i / nk, &n);
         const int head = h * nk + i % nk;
-        uint64_t* bar = &sh.kv_full[i & 1];
+        uint64_t* bar = &sh.kv_full[i % NS];
         if (elect()) {
             mbar_expect_tx(bar, Z::KBY + Z::VBY);
             for (int b = 0; b < DK / 64; ++b)
-                tma_load3(sm + Z::K + (i & 1) * Z::KBY + b * TILE_BYTES, &A.map[R.mk], b * 64, head, (int)a, bar);
+                tma_load3(sm + Z::K + (i % NS) * Z::KBY + b * TB, &A.map[R.mk], b * 64, head, (int)a, bar);
             for (int b = 0; b < DV / 64; ++b)
-                tma_load3(sm + Z::V + (i & 1) * Z::VBY + b * TILE_BYTES, &A.map[R.mv], b * 64, head, (int)a, bar);
+                tma_load3(sm + Z::V + (i % NS) * Z::VBY + b * TB, &A.map[R.mv], b * 64, head, (int)a, bar);
         }
         __syncwarp();
     }
@@ -287,9 +297,14 @@ struct TcBlock {
         if (elect()) {
             mbar_expect_tx(&sh.q_full, Z::KBY);
             for (int b = 0; b < DK / 64; ++b)
-                tma_load3(sm + Z::Q + b * TILE_BYTES, &A.map[R.mq], b * 64, h * nq + i % nq, (int)a, &sh.q_full);
+                tma_load3(sm + Z::Q + b * TB, &A.map[R.mq], b * 64, h * nq + i % nq, (int)a, &sh.q_full);
         }
         __syncwarp();
+    }
+    // where the second (1) and third (2) part of K go for the us-th U
+    __device__ __forceinline__ uint32_t part(int x, int us) const {
+        if (OUT || !BF) return x == 1 ? Z::LO : Z::S;
+        return Z::LO + (2 * (us & 1) + x - 1) * Z::KBY;
     }
     __device__ __forceinline__ void commit(uint64_t* bar) const {
         if (elect()) mma_commit(bar);
@@ -298,7 +313,7 @@ struct TcBlock {
     __device__ __forceinline__ void issue() const {
         load_kv(0);
         if (OUT) load_q(0);
-        load_kv(1);
+        for (int i = 1; i < NS; ++i) load_kv(i);
         bool has_state = R.state_in != nullptr;
         int item = 0, us = 0, refill = -1;
         for (int c = 0; c < nch; ++c) {
@@ -306,8 +321,8 @@ struct TcBlock {
                 const int kv = c * nk + (nk > 1 ? i : 0), qi = c * nq + (nq > 1 ? i : 0);
                 const bool new_kv = i == 0 || nk > 1, new_q = i == 0 || nq > 1, last = i == G - 1;
                 const bool conv = nk > 1 || last, emit = nq > 1 || last;
-                const uint32_t Ka = smb + Z::K + (kv & 1) * Z::KBY, Va = smb + Z::V + (kv & 1) * Z::VBY;
-                if (new_kv && !wait(&sh.kv_full[kv & 1], kv >> 1)) return;
+                const uint32_t Ka = smb + Z::K + (kv % NS) * Z::KBY, Va = smb + Z::V + (kv % NS) * Z::VBY;
+                if (new_kv && !wait(&sh.kv_full[kv % NS], kv / NS)) return;
                 if constexpr (OUT) {
                     if (new_q && !wait(&sh.q_full, qi)) return;
                     if (item > 0 && !wait(&sh.o_done, item - 1)) return;  // O1 has read the weights in P's place
@@ -317,7 +332,7 @@ struct TcBlock {
                     if (elect()) {
 #pragma unroll
                         for (int s = 0; s < DK / 16; ++s) {
-                            const uint32_t off = ((s >> 2) * TILE_BYTES + (s & 3) * 32) >> 4;
+                            const uint32_t off = ((s >> 2) * TB + (s & 3) * 32) >> 4;
                             mma_ss(tm + Z::P, dq + off, dk + off, id, s > 0);
                         }
                         mma_commit(&sh.p_done);
@@ -326,7 +341,7 @@ struct TcBlock {
                     __syncwarp();
                 }
                 if (refill >= 0) {  // the last products have read their K and V
-                    if (!wait(&sh.u_done, us - 1)) return;
+                    if (!wait(&sh.u_done[(us - 1) & 1], (us - 1) >> 1)) return;
                     load_kv(refill);
                     refill = -1;
                 }
@@ -341,7 +356,7 @@ struct TcBlock {
                             if (elect()) {
 #pragma unroll
                                 for (int s = 0; s < DK / 16; ++s)
-                                    mma_ss(tm + Z::O2, dq + (((s >> 2) * TILE_BYTES + (s & 3) * 32) >> 4),
+                                    mma_ss(tm + Z::O2, dq + (((s >> 2) * TB + (s & 3) * 32) >> 4),
                                            ds + s * (2048 >> 4), id, s > 0);
                             }
                             __syncwarp();
@@ -359,7 +374,7 @@ struct TcBlock {
                     tc_fence_after();
                     constexpr uint32_t id = mma_desc(BF, false, true, 128, DV);
                     const bool more = nk > 1 && i > 0;
-                    const uint64_t dv = tile_desc(Va, TILE_BYTES, 1024);
+                    const uint64_t dv = tile_desc(Va, TB, 1024);
                     if (elect()) {
 #pragma unroll
                         for (int s = 0; s < 8; ++s)
@@ -369,86 +384,53 @@ struct TcBlock {
                     __syncwarp();
                 }
                 if (conv) {
-                    if (!wait(&sh.k_ready, us)) return;  // and the state is scaled
+                    if (!wait(&sh.k_ready[us & 1], us >> 1)) return;  // and the state is scaled
                     tc_fence_after();
                     // dk = 64: M stays 128, the second half repeats the first (leading offset 0) and is not read
-                    constexpr uint32_t id = mma_desc(BF, true, true, 128, DV), lead = DK == 64 ? 0 : TILE_BYTES;
-                    const uint64_t dv = tile_desc(Va, TILE_BYTES, 1024), d0 = tile_desc(Ka, lead, 1024),
-                                   d1 = tile_desc(smb + Z::LO, lead, 1024), d2 = tile_desc(smb + Z::S, lead, 1024);
+                    constexpr uint32_t id = mma_desc(BF, true, true, 128, DV), lead = DK == 64 ? 0 : TB;
+                    const uint64_t dv = tile_desc(Va, TB, 1024), d0 = tile_desc(Ka, lead, 1024),
+                                   d1 = tile_desc(smb + part(1, us), lead, 1024), d2 = tile_desc(smb + part(2, us), lead, 1024);
                     const bool add = us > 0 || R.state_in;
                     if (elect()) {
 #pragma unroll
-                        for (int s = 0; s < 8; ++s)
+                        for (int s = 0; s < CH / 16; ++s)
                             mma_ss(tm + Z::U, d0 + s * (2048 >> 4), dv + s * (2048 >> 4), id, add || s > 0);
 #pragma unroll
-                        for (int s = 0; s < 8; ++s) mma_ss(tm + Z::U, d1 + s * (2048 >> 4), dv + s * (2048 >> 4), id, true);
+                        for (int s = 0; s < CH / 16; ++s) mma_ss(tm + Z::U, d1 + s * (2048 >> 4), dv + s * (2048 >> 4), id, true);
                         if (BF && exact) {
 #pragma unroll
-                            for (int s = 0; s < 8; ++s) mma_ss(tm + Z::U, d2 + s * (2048 >> 4), dv + s * (2048 >> 4), id, true);
+                            for (int s = 0; s < CH / 16; ++s) mma_ss(tm + Z::U, d2 + s * (2048 >> 4), dv + s * (2048 >> 4), id, true);
                         }
-                        mma_commit(&sh.u_done);
+                        mma_commit(&sh.u_done[us & 1]);
                     }
                     __syncwarp();
                     ++us;
-                    refill = kv + 2;
+                    refill = kv + NS;
                 }
             }
             has_state = true;
         }
     }
 
-    // ---- V's scan, K's weights, the state
-    // V of load kv: rows past the chunk's n tokens become 0, and so do NaN and Inf.  fp16: the largest |k|.
+    // ---- K's weights, the state
+    // V of load kv: rows past the chunk's n tokens become 0 (theirs are of other sequences).  fp16: the largest |k|.
     // (Thread tid has unit tid % 8 of the rows tid / 8 + 32 y of each tile: one offset, 4096 bytes apart.)
     __device__ __forceinline__ float scan(int kv, int n, int tid) const {
-        unsigned char* Vs = sm + Z::V + (kv & 1) * Z::VBY + tile_at(tid >> 3, tid & 7);
         const int r0 = tid >> 3;
-        if (OUT && tid < 4) sh.bad[(kv + 2) & 7][tid] = 0;
-        constexpr uint32_t INF = BF ? 0x7f80u : 0x7c00u;
-        if (OUT) {
-            uint32_t acc[4] = {0, 0, 0, 0};  // sums of x * 0: NaN where an x is NaN or Inf
-#pragma unroll
-            for (int x = 0; x < DV / 64 * 4; ++x) {
-                const uint4 w = *reinterpret_cast<const uint4*>(Vs + (x >> 2) * TILE_BYTES + (x & 3) * 4096);
-                acc[0] = Pair<T>::fma(w.x, 0u, acc[0]);
-                acc[1] = Pair<T>::fma(w.y, 0u, acc[1]);
-                acc[2] = Pair<T>::fma(w.z, 0u, acc[2]);
-                acc[3] = Pair<T>::fma(w.w, 0u, acc[3]);
-            }
-            if ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7fff7fffu) {
-#pragma unroll 1
-                for (int x = 0; x < DV / 64 * 4; ++x) {
-                    const int r = r0 + 32 * (x & 3);
-                    if (r >= n) continue;
-                    uint4* p = reinterpret_cast<uint4*>(Vs + (x >> 2) * TILE_BYTES + (x & 3) * 4096);
-                    uint4 w = *p;
-                    uint32_t q[4] = {w.x, w.y, w.z, w.w}, any = 0;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const uint32_t m = ((q[e] & 0x7fffu) >= INF ? 0u : 0xffffu) | ((q[e] >> 16 & 0x7fffu) >= INF ? 0u : 0xffff0000u);
-                        any |= ~m;
-                        q[e] &= m;
-                    }
-                    if (!any) continue;
-                    atomicOr(&sh.bad[kv & 7][r >> 5], 1u << (r & 31));
-                    *p = make_uint4(q[0], q[1], q[2], q[3]);
-                }
-            }
-        }
-        if (n < TC_C) {
-            Vs = sm + Z::V + (kv & 1) * Z::VBY + tile_at(tid >> 3, tid & 7);
+        if (n < CH) {
+            unsigned char* Vs = sm + Z::V + (kv % NS) * Z::VBY + tile_at(tid >> 3, tid & 7);
             for (int b = 0; b < DV / 64; ++b)
-                for (int y = 0; y < 4; ++y)
-                    if (r0 + 32 * y >= n) *reinterpret_cast<uint4*>(Vs + b * TILE_BYTES + y * 4096) = make_uint4(0, 0, 0, 0);
+                for (int y = 0; y < CH / 32; ++y)
+                    if (r0 + 32 * y >= n) *reinterpret_cast<uint4*>(Vs + b * TB + y * 4096) = make_uint4(0, 0, 0, 0);
         }
         float km = 0.0f;
         if constexpr (!BF) {
-            const unsigned char* Ks = sm + Z::K + (kv & 1) * Z::KBY + tile_at(tid >> 3, tid & 7);
+            const unsigned char* Ks = sm + Z::K + (kv % NS) * Z::KBY + tile_at(tid >> 3, tid & 7);
             uint32_t m = 0;
 #pragma unroll
-            for (int x = 0; x < DK / 64 * 4; ++x) {
-                if (r0 + 32 * (x & 3) >= n) continue;
-                const uint4 w = *reinterpret_cast<const uint4*>(Ks + (x >> 2) * TILE_BYTES + (x & 3) * 4096);
+            for (int x = 0; x < DK / 64 * (CH / 32); ++x) {
+                if (r0 + 32 * (x % (CH / 32)) >= n) continue;
+                const uint4 w = *reinterpret_cast<const uint4*>(Ks + (x / (CH / 32)) * TB + (x % (CH / 32)) * 4096);
                 m = __vmaxu2(m, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu),
                                          __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
             }
@@ -463,18 +445,19 @@ struct TcBlock {
     }
 
     // K of load kv, times g1 e^{lam d} (and k_up, fp16), as a sum of 16-bit parts
-    __device__ __forceinline__ void weigh(int kv, int n, float k_up, int tid) const {
+    // The state pass of bf16: times `far` as well (us: the number of this U).
+    __device__ __forceinline__ void weigh(int kv, int n, float k_up, int tid, float far, int us) const {
         const uint32_t at0 = tile_at(tid >> 3, tid & 7);
-        unsigned char* Ks = sm + Z::K + (kv & 1) * Z::KBY + at0;
-        unsigned char* Ls = sm + Z::LO + at0;
-        unsigned char* Ms = sm + Z::S + at0;
+        unsigned char* Ks = sm + Z::K + (kv % NS) * Z::KBY + at0;
+        unsigned char* Ls = sm + part(1, us) + at0;
+        unsigned char* Ms = sm + part(2, us) + at0;
         const int r0 = tid >> 3, d0 = rev ? r0 : n - 1 - r0, dd = rev ? 32 : -32;
         using H = Pair<T>;
 #pragma unroll 2
-        for (int x = 0; x < DK / 64 * 4; ++x) {
-            const uint32_t at = (x >> 2) * TILE_BYTES + (x & 3) * 4096;
+        for (int x = 0; x < DK / 64 * (CH / 32); ++x) {
+            const uint32_t at = (x / (CH / 32)) * TB + (x % (CH / 32)) * 4096;
             const uint4 w = *reinterpret_cast<const uint4*>(Ks + at);
-            const int d = (d0 + (x & 3) * dd) & 127;
+            const int d = (d0 + (x % (CH / 32)) * dd) & 127;
             const uint32_t q[4] = {w.x, w.y, w.z, w.w};
             uint32_t a0[4], a1[4], a2[4];
             if (!BF && exact) {
@@ -491,8 +474,22 @@ struct TcBlock {
             } else {
                 // k (f1 + f2 (+ f3)): the first part rn(k f1); k f1 less it is exact, and with k f2 gives
                 // the second; what that rounds off, with k f3, the third
-                const uint2 f = sh.dec2[d];
-                const uint32_t f3 = BF && exact ? sh.dec3[d] : 0u, up = BF ? 0u : pack2<T>(k_up, k_up);
+                uint2 f;
+                uint32_t f3 = 0;
+                if (BF && !OUT) {
+                    float y = sh.dec[d] * far;
+                    f.x = pack2<T>(y, y);
+                    y -= unpack2<T>(f.x).x;
+                    f.y = pack2<T>(y, y);
+                    if (exact) {
+                        y -= unpack2<T>(f.y).x;
+                        f3 = pack2<T>(y, y);
+                    }
+                } else {
+                    f = sh.dec2[d];
+                    if (BF && exact) f3 = sh.dec3[d];
+                }
+                const uint32_t up = BF ? 0u : pack2<T>(k_up, k_up);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t k = BF ? q[e] : H::mul(q[e], up);  // (exact)
@@ -502,7 +499,7 @@ struct TcBlock {
                     if (BF && exact) a2[e] = H::fma(k, f3, H::fma(k, f.y, H::sub(left, a1[e])));
                 }
             }
-            if (n < TC_C && r0 + 32 * (x & 3) >= n) {  // not 0 * NaN
+            if (n < CH && r0 + 32 * (x % (CH / 32)) >= n) {  // not 0 * NaN
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a0[e] = a1[e] = a2[e] = 0;
             }
@@ -513,48 +510,11 @@ struct TcBlock {
         fence_proxy_async();
     }
 
-    // Where V of load kv has a NaN or Inf (and 0 in shared memory): adds weight(s) v_s, to this
-    // warp's rows that s reaches, in the HV columns of tensor memory at D.  (Rare: a column at a time.)
-    template <typename Weight, typename Reach>
-    __device__ __forceinline__ void mend(uint32_t D, int kv, int64_t a, int n, Weight weight, Reach reach) const {
-        const int wg = (threadIdx.x / 128) & 1;
-        const uint32_t* rows = sh.bad[kv & 7];
-#pragma unroll 1
-        for (int s = 0; s < n; ++s) {
-            if (!(rows[s >> 5] >> (s & 31) & 1)) continue;
-            __syncwarp();
-            const float w = weight(s);
-            const bool hit = reach(s);
-            const T* v = static_cast<const T*>(R.v) + (a + s) * R.v_ts + (int64_t)(h * nk + kv % nk) * R.v_hs + wg * HV;
-#pragma unroll 1
-            for (int j = 0; j < HV && wg * HV + j < R.dv; ++j) {
-                const float x = to_acc<float, T>(v[j]);
-                if (fabsf(x) <= 3.0e38f) continue;  // (one value for the warp)
-                __syncwarp();
-                const uint32_t d = tmem_ld1(D + j);
-                tmem_wait_ld();
-                tmem_st1(D + j, hit ? __float_as_uint(fmaf(w, x, __uint_as_float(d))) : d);
-                tmem_wait_st();
-            }
-        }
-    }
-
-    // The state, in tensor memory in units of 1 / up, with what a NaN or Inf of V of load kv
-    // reaches: rounded into shared memory as the B operand of O2 (which: its number);
+    // The state, in tensor memory in units of 1 / up: rounded into shared memory as the B operand of O2 (which: its number);
     // scaled for the next U; or out into memory.
-    __device__ __forceinline__ void pass(int tid, bool bad, int kv, int64_t a, int n, float up, bool round, int which,
-                                         bool scale, float factor, float* out) const {
+    __device__ __forceinline__ void pass(int tid, float up, bool round, int which, bool scale, float factor, float* out) const {
         const int warp = tid >> 5, lane = tid & 31, wg = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t St = tm + ((uint32_t)((warp & 3) * 32) << 16) + Z::U + wg * HV;
-        if (bad) {
-            const float f = g1 * up / up1;
-            mend(St, kv, a, n, [&](int s) {
-                return row < R.dk ? f * exp2f(l2 * (float)(rev ? s : n - 1 - s)) *
-                                        to_acc<float, T>(static_cast<const T*>(
-                                            R.k)[(a + s) * R.k_ts + (int64_t)(h * nk + kv % nk) * R.k_hs + row])
-                                  : 0.0f;
-            }, [](int) { return true; });
-        }
         float s_up = 1.0f / up;
         if (!BF && round) {
             float m = 0.0f;
@@ -703,37 +663,54 @@ struct TcBlock {
             tmem_wait_st();
         }
         if (!wait(&sh.kv_full[0], 0)) return;
+        if constexpr (BF && !OUT) {
+            // The state pass of bf16: K's weights reach to the segment's end, U adds up over all
+            // chunks, and the state is read once.  K's lower parts have two buffers: a chunk is
+            // weighed while the last one is multiplied.
+            if (in) pass(tid, 1.0f, false, 0, true, exp2f(l2 * (float)len), nullptr);
+            const int n_kv = nch * nk;
+            for (int kv = 0; kv < n_kv; ++kv) {
+                a = chunk_at(kv / nk, &n);
+                if (kv > 0 && !wait(&sh.kv_full[kv % NS], kv / NS)) return;
+                if (kv > 1 && !wait(&sh.u_done[kv & 1], (kv - 2) >> 1)) return;  // the parts' buffer is free
+                const int64_t far = rev ? a - t0 : t0 + len - a - n;
+                scan(kv, n, tid);
+                weigh(kv, n, 1.0f, tid, exp2f(l2 * (float)far), kv);
+                arrive(&sh.k_ready[kv & 1]);
+            }
+            if (!wait(&sh.u_done[(n_kv - 1) & 1], (n_kv - 1) >> 1)) return;  // (and with it all before)
+            tc_fence_after();
+            pass(tid, 1.0f, false, 0, false, 1.0f, out);
+            return;
+        }
         float k_up = k_scale(scan(0, n, tid), tid);
-        if (in) pass(tid, false, 0, 0, 0, 1.0f, OUT, 0, true, exp2f(l2 * (float)n) * (k_up * up1), nullptr);
+        if (in) pass(tid, 1.0f, OUT, 0, true, exp2f(l2 * (float)n) * (k_up * up1), nullptr);
         const int n_kv = nch * nk;
         for (int kv = 0, us = 0; kv < n_kv; ++kv) {  // (a chunk's q-heads share one load)
             const int c = kv / nk;
             a = chunk_at(c, &n);
             // P has read K (and O2 the state, in whose place the third part goes)
             if (OUT && !wait(&sh.k_free, us)) return;
-            weigh(kv, n, k_up, tid);
-            arrive(&sh.k_ready);
+            weigh(kv, n, k_up, tid, 1.0f, us);
+            arrive(&sh.k_ready[us & 1]);
             const float up = k_up * up1;
             const bool more = kv + 1 < n_kv;
             const int c2 = (kv + 1) / nk;
             int n2 = 0;
             if (more) {  // the next load's scan, while U runs
                 chunk_at(c2, &n2);
-                if (!wait(&sh.kv_full[(kv + 1) & 1], (kv + 1) >> 1)) return;
+                if (!wait(&sh.kv_full[(kv + 1) % NS], (kv + 1) / NS)) return;
                 k_up = k_scale(scan(kv + 1, n2, tid), tid);
             }
             float factor = 1.0f;
             if (more) factor = (c2 != c ? exp2f(l2 * (float)n2) : 1.0f) * (BF ? 1.0f : k_up * up1 / up);
-            if (!wait(&sh.u_done, us)) return;
+            if (!wait(&sh.u_done[us & 1], us >> 1)) return;
             ++us;
             tc_fence_after();
-            const uint32_t* rows = sh.bad[kv & 7];
-            const bool bad = OUT && (rows[0] | rows[1] | rows[2] | rows[3]);
             if (more) {
-                if (!BF || c2 != c || bad)
-                    pass(tid, bad, kv, a, n, up, OUT && c2 != c, R.state_in ? c2 : c2 - 1, true, factor, nullptr);
+                if (!BF || c2 != c) pass(tid, up, OUT && c2 != c, R.state_in ? c2 : c2 - 1, true, factor, nullptr);
             } else if (out)
-                pass(tid, bad, kv, a, n, up, false, 0, false, 1.0f, out);
+                pass(tid, up, false, 0, false, 1.0f, out);
         }
     }
 
@@ -767,10 +744,57 @@ struct TcBlock {
                 r[j] = f != 0.0f ? __float_as_uint(p) : 0u;  // not 0 * NaN
             }
         }
-        if (n < TC_C) {
+        if (n < CH) {
 #pragma unroll
             for (int j = 0; j < 16; ++j)
                 if (base + j >= n) r[j] = 0;
+        }
+    }
+
+    // Outputs whose O1 is not finite while their O2 is: a NaN or Inf of V that their row
+    // may not see, times a weight of 0.  They come from the definition, over the rows s that
+    // reach them; 8 columns at a time.  (In the chunk of the first such token: afterwards it is
+    // in the state.)
+    __device__ __forceinline__ void repair(uint32_t O1, uint32_t O2, T* out, int64_t a, int n, int row, int wg, int head,
+                                           bool has_state, float w1, float w2) const {
+        const T* qr = static_cast<const T*>(R.q) + (a + row) * R.q_ts + (int64_t)(h * nq + head) * R.q_hs;
+#pragma unroll 1
+        for (int cb = 0; cb < HV && wg * HV + cb < R.dv; cb += 8) {
+            float sum[8];
+            uint32_t want = 0;
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+                __syncwarp();
+                const float x = __uint_as_float(tmem_ld1(O1 + cb + j));
+                const float y = has_state ? __uint_as_float(tmem_ld1(O2 + cb + j)) : 0.0f;
+                tmem_wait_ld();
+                if (row < n && !(fabsf(x) <= 3.3e38f) && fabsf(w2 * y) <= 3.3e38f) want |= 1u << j;
+            }
+            if (!__any_sync(FULL, want != 0)) continue;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum[j] = 0.0f;
+            if (want) {
+#pragma unroll 1
+                for (int g = 0; g < nk; ++g)
+#pragma unroll 1
+                    for (int s = rev ? row : 0; rev ? s < n : s <= row; ++s) {
+                        const T* kr = static_cast<const T*>(R.k) + (a + s) * R.k_ts + (int64_t)(h * nk + g) * R.k_hs;
+                        const T* vr = static_cast<const T*>(R.v) + (a + s) * R.v_ts + (int64_t)(h * nk + g) * R.v_hs + wg * HV + cb;
+                        float dot = 0.0f;
+#pragma unroll 1
+                        for (int e = 0; e < R.dk; ++e) dot = fmaf(to_acc<float, T>(qr[e]), to_acc<float, T>(kr[e]), dot);
+                        dot *= R.sq * R.sk * exp2f(l2 * (float)(rev ? s - row : row - s));
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) sum[j] = fmaf(dot, to_acc<float, T>(vr[j]), sum[j]);
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                __syncwarp();
+                const float y = has_state ? __uint_as_float(tmem_ld1(O2 + cb + j)) : 0.0f;
+                tmem_wait_ld();
+                if (want >> j & 1) out[cb + j] = from_acc<T, float>(fmaf(w2, y, sum[j]));
+            }
         }
     }
 
@@ -782,15 +806,20 @@ struct TcBlock {
         const uint32_t O1 = tm + lanes + Z::O1 + wg * HV, O2 = tm + lanes + Z::O2 + wg * HV;
         // outputs in whole 32-byte sectors where they start on one
         const bool wide = ((reinterpret_cast<uintptr_t>(R.o) | (uintptr_t)(R.o_ts * 2) | (uintptr_t)(R.o_hs * 2)) & 31) == 0;
+        int wq_n = -1;
+        float wq = 0.0f;
         float up = 1.0f;  // fp16: the scale of this row's weights and of O1
         int item = 0;
         for (int c = 0; c < nch; ++c) {
             int n;
             const int64_t a = chunk_at(c, &n);
             const bool has_state = c > 0 || R.state_in;
-            const float wq = R.sq * exp2f(l2 * (float)(rev ? n - 1 - row : row + 1));
+            if (n != wq_n) {
+                wq_n = n;
+                wq = R.sq * exp2f(l2 * (float)(rev ? n - 1 - row : row + 1));
+            }
             for (int i = 0; i < G; ++i, ++item) {
-                const int kv = c * nk + (nk > 1 ? i : 0), qi = c * nq + (nq > 1 ? i : 0);
+                const int qi = c * nq + (nq > 1 ? i : 0);
                 const bool emit = nq > 1 || i == G - 1;
                 if (!wait(&sh.p_done, item)) return;
                 tc_fence_after();
@@ -861,22 +890,12 @@ struct TcBlock {
                 tmem_wait_st();
                 tc_fence_before();
                 arrive(&sh.p_ready);
-                if (!wait(&sh.v_ready[kv & 1], kv >> 1)) return;  // (the rows with NaN or Inf are known)
                 if (!wait(&sh.o_done, item)) return;
                 if (emit && !wait(&sh.o2_done, qi)) return;
                 tc_fence_after();
-                const uint32_t* bad = sh.bad[kv & 7];
-                const bool patch = bad[0] | bad[1] | bad[2] | bad[3];
                 const float w1 = BF ? 1.0f : 1.0f / up;
                 const float w2 = BF ? wq : wq * (has_state ? sh.s_inv[(R.state_in ? c : c - 1) & 1] : 1.0f);
                 T* out = static_cast<T*>(R.o) + (a + row) * R.o_ts + (int64_t)(h * nq + (nq > 1 ? i : 0)) * R.o_hs + wg * HV;
-                if (patch)  // weights as O1 took them
-                    mend(O1, kv, a, n, [&](int s) {
-                        const uint32_t w = tmem_ld1(tm + lanes + Z::P + (s >> 6) * 64 + ((s & 63) >> 1));
-                        tmem_wait_ld();
-                        const float2 x = unpack2<T>(w);
-                        return s & 1 ? x.y : x.x;
-                    }, [&](int s) { return rev ? s >= row : s <= row; });
                 if (emit) {
                     uint32_t q[2][16];
 #pragma unroll
@@ -887,6 +906,7 @@ struct TcBlock {
                     tmem_wait_ld();
                     const bool in = row < n;
                     const int cols = R.dv - wg * HV;
+                    uint32_t odd = 0;  // the sum of the outputs times 0: NaN if one is not finite
 #pragma unroll 1
                     for (int cb = 0; cb < HV; cb += 32) {
 #pragma unroll
@@ -902,6 +922,7 @@ struct TcBlock {
                                 if constexpr (!BF) p = mul2(p, make_float2(w1, w1));
                                 p = fma2(make_float2(w2, w2), pair(q[y][2 * j], q[y][2 * j + 1]), p);
                                 pk[j] = pack2<T>(p.x, p.y);
+                                odd = Pair<T>::fma(pk[j], 0u, odd);
                             }
                             const int at = cb + y * 16;
                             if (in && wide && at + 16 <= cols) {
@@ -914,6 +935,8 @@ struct TcBlock {
                             tmem_wait_ld();
                         }
                     }
+                    if (__any_sync(FULL, in && (odd & 0x7fff7fffu) != 0))
+                        repair(O1, O2, out, a, n, row, wg, nq > 1 ? i : 0, has_state, w1, w2);
                 }
                 tc_fence_before();
                 arrive(&sh.o_read);
@@ -923,8 +946,8 @@ struct TcBlock {
 };
 
 template <typename T, int DK, int DV, bool OUT>
-__global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT, 1) k_lin_tc(const __grid_constant__ TcArgs A) {
-    using Z = TcSize<DK, DV, OUT>;
+__global__ void __launch_bounds__(TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloat16>::value>::NT, 1) k_lin_tc(const __grid_constant__ TcArgs A) {
+    using Z = TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloat16>::value>;
     extern __shared__ __align__(1024) unsigned char sm[];
     TcShared& sh = *reinterpret_cast<TcShared*>(sm + Z::TILES);
     const TcRole& R = A.role[blockIdx.x % A.nroles];
@@ -940,9 +963,9 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT, 1) k_lin_tc(const __g
     }
     constexpr int ISSUE = (OUT ? 2 : 1) * TC_GROUP / 32;  // the issuing warp
     if (tid == 0) {
-        for (uint64_t* b : {&sh.kv_full[0], &sh.kv_full[1], &sh.q_full, &sh.p_done, &sh.k_free, &sh.o2_done, &sh.o_done, &sh.u_done})
+        for (uint64_t* b : {&sh.kv_full[0], &sh.kv_full[1], &sh.kv_full[2], &sh.kv_full[3], &sh.q_full, &sh.p_done, &sh.k_free, &sh.o2_done, &sh.o_done, &sh.u_done[0], &sh.u_done[1]})
             mbar_init(b, 1);
-        for (uint64_t* b : {&sh.v_ready[0], &sh.v_ready[1], &sh.k_ready, &sh.s_ready, &sh.p_ready, &sh.o_read})
+        for (uint64_t* b : {&sh.v_ready[0], &sh.v_ready[1], &sh.k_ready[0], &sh.k_ready[1], &sh.s_ready, &sh.p_ready, &sh.o_read})
             mbar_init(b, TC_GROUP / 32);
         sh.dead = 0;
         fence_proxy_async();
@@ -950,7 +973,6 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT, 1) k_lin_tc(const __g
     __syncwarp();
     if (tid / 32 == ISSUE) tmem_alloc(&sh.tmem, Z::COLS);
     const float l2 = clamp_lam(A.lam[h]) * 1.44269504088896341f;
-    if (tid < 32) sh.bad[tid >> 2][tid & 3] = 0;
     const bool exact = R.state_out && R.exact;
     // K's weights are g1 e^{lam d}, d >= 0.  fp16: a fast decay (reversed) or a small scale
     // would sink all of them, so a power of two goes from g1 into the state's unit.
@@ -969,7 +991,7 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT, 1) k_lin_tc(const __g
         float left = d - unpack2<T>(hi).x;
         const uint32_t lo = pack2<T>(left, left);
         sh.dec2[tid] = make_uint2(hi, lo);
-        if (std::is_same<T, __half>::value) sh.dec[tid] = d;
+        if (std::is_same<T, __half>::value || !OUT) sh.dec[tid] = d;
         else {
             left -= unpack2<T>(lo).x;
             sh.dec3[tid] = pack2<T>(left, left);
@@ -978,7 +1000,7 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT, 1) k_lin_tc(const __g
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const int nch = (len + TC_C - 1) / TC_C;
+    const int nch = (len + Z::CH - 1) / Z::CH;
     const TcBlock<T, DK, DV, OUT> B{A,   R,   sm,  sh,   smem_u32(sm), sh.tmem, slot, h,   seq, len, nch,
                                     R.nq, R.nk, max(R.nq, R.nk), t0, rev, exact, l2, g1, up1};
     if constexpr (OUT) {
@@ -1003,8 +1025,7 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT, 1) k_lin_tc(const __g
     if (sh.dead && tid == 0) {
         // a copy or a product did not come: report it, and let the copies in flight land
         set_status(A.status, ST_TIMEOUT);
-        mbar_wait(&sh.kv_full[0], 0);
-        mbar_wait(&sh.kv_full[1], 0);
+        for (uint64_t& b : sh.kv_full) mbar_wait(&b, 0);
         mbar_wait(&sh.q_full, 0);
     }
     if (tid / 32 == ISSUE) {
@@ -1032,13 +1053,13 @@ static EncodeTiled encode_fn() {
     return reinterpret_cast<EncodeTiled>(f);
 }
 
-// boxes of [128 tokens][one head][64 values]; values past dim and tokens past T read as 0
-static cudaError_t encode(CUtensorMap* m, laplex_dtype dt, const LinRows& x, int dim, int heads, int64_t T) {
+// boxes of [tokens][one head][64 values]; values past dim and tokens past T read as 0
+static cudaError_t encode(CUtensorMap* m, laplex_dtype dt, const LinRows& x, int dim, int heads, int64_t T, int tokens) {
     EncodeTiled f = encode_fn();
     if (!f) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)heads, (cuuint64_t)T};
     const cuuint64_t strides[2] = {(cuuint64_t)x.hs * 2, (cuuint64_t)x.ts * 2};
-    const cuuint32_t box[3] = {64, 1, TC_C}, es[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)tokens}, es[3] = {1, 1, 1};
     const CUresult r = f(m, dt == LAPLEX_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
                          const_cast<void*>(x.p), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -1083,18 +1104,20 @@ int tc_segment(int64_t T, int N, int H, int roles, bool equal) {
 template <typename T, int DK, int DV, bool OUT>
 static cudaError_t tc_launch(const TcArgs& A, cudaStream_t st) {
     constexpr auto kern = k_lin_tc<T, DK, DV, OUT>;
-    constexpr size_t smem = TcSize<DK, DV, OUT>::BYTES;
+    using Z = TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloat16>::value>;
+    constexpr size_t smem = Z::BYTES;
     int dev = 0, sms = 0, per = 0;
     cudaError_t e = current_device_sms(&dev, &sms);
-    if (e == cudaSuccess) e = blocks_per_sm<kern>(dev, TcSize<DK, DV, OUT>::NT, smem, &per);
+    if (e == cudaSuccess) e = blocks_per_sm<kern>(dev, Z::NT, smem, &per);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(A.S.slots * A.nroles), (unsigned)A.H);
     if (grid.x == 0) return cudaSuccess;
-    kern<<<grid, TcSize<DK, DV, OUT>::NT, smem, st>>>(A);
+    kern<<<grid, Z::NT, smem, st>>>(A);
     return cudaGetLastError();
 }
 
-static_assert(TcSize<128, 128, true>::BYTES <= 232448, "shared memory of a block");
+static_assert(TcSize<128, 128, true, true>::BYTES <= 232448 && TcSize<128, 128, false, true>::BYTES <= 232448 &&
+                  TcSize<128, 128, false, false>::BYTES <= 232448, "shared memory of a block");
 
 template <typename T, bool OUT>
 static cudaError_t tc_dims(const TcArgs& A, int dk, int dv, cudaStream_t st) {
@@ -1128,7 +1151,7 @@ cudaError_t tc_run(laplex_dtype dt, const LinRole* roles, int count, const LinSe
                         return cudaSuccess;
                 if (maps == 4) return cudaErrorInvalidValue;
                 key[maps++] = {x, dim, heads};
-                return S.T > 0 ? encode(&A.map[*m], dt, x, dim, heads, S.T) : cudaSuccess;
+                return S.T > 0 ? encode(&A.map[*m], dt, x, dim, heads, S.T, state_only && dt == LAPLEX_BF16 ? 64 : TC_C) : cudaSuccess;
             };
             cudaError_t e = state_only ? cudaSuccess : map_of(L.q, L.dk, H * L.nq, &R.mq);
             if (e == cudaSuccess) e = map_of(L.k, L.dk, H * L.nk, &R.mk);
@@ -1146,6 +1169,9 @@ cudaError_t tc_run(laplex_dtype dt, const LinRole* roles, int count, const LinSe
             R.exact = !state_only || !L.skip_last;
             R.sq = (float)L.sq;
             R.sk = (float)L.sk;
+            R.q = L.q.p;
+            R.q_ts = L.q.ts;
+            R.q_hs = L.q.hs;
             R.k = L.k.p;
             R.k_ts = L.k.ts;
             R.k_hs = L.k.hs;
