@@ -108,15 +108,16 @@ struct TcShared {
     float red[2][8];     // fp16: maxima of the state warps
 };
 
-// CH tokens at a time.  The state pass of bf16 takes 64, in four stages: it only streams K and
-// V, and two stages of 128 left the copies' latency (about 3500 cycles under load) in the open.
+// CH tokens at a time.  The state pass of bf16 takes 64, with two blocks on an SM: it only streams
+// K and V, and one block with two stages of 128 left the copies' latency (about 3500 cycles under
+// load) in the open.
 template <int DK, int DV, bool OUT, bool BF> struct TcSize {
-    static constexpr int CH = OUT || !BF ? 128 : 64, STAGES = CH == 64 ? 4 : 2;
+    static constexpr int CH = OUT || !BF ? 128 : 64, STAGES = 2, BLOCKS = CH == 64 ? 2 : 1;
     static constexpr uint32_t TB = CH * 128;  // bytes of a tile of 64 columns
     static constexpr uint32_t KBY = DK / 64 * TB, VBY = DV / 64 * TB;
     // K's lower parts.  Products: the second in LO, the third (bf16) in the place of the rounded
-    // state between O2 and the next state.  State pass of bf16: two buffers of both.
-    static constexpr uint32_t SBY = OUT && DK * 128 * (DV / 64) > KBY ? DK * 128 * (DV / 64) : OUT ? KBY : BF ? 3 * KBY : 0;
+    // state between O2 and the next state.  State pass of bf16: the third, or a second buffer of the second.
+    static constexpr uint32_t SBY = OUT && DK * 128 * (DV / 64) > KBY ? DK * 128 * (DV / 64) : OUT || BF ? KBY : 0;
     static constexpr uint32_t K = 0, V = STAGES * KBY, LO = V + STAGES * VBY, S = LO + KBY, Q = S + SBY;
     static constexpr uint32_t TILES = Q + (OUT ? KBY : 0);
     static constexpr uint32_t BYTES = TILES + sizeof(TcShared);
@@ -303,8 +304,8 @@ struct TcBlock {
     }
     // where the second (1) and third (2) part of K go for the us-th U
     __device__ __forceinline__ uint32_t part(int x, int us) const {
-        if (OUT || !BF) return x == 1 ? Z::LO : Z::S;
-        return Z::LO + (2 * (us & 1) + x - 1) * Z::KBY;
+        if (OUT || !BF || exact) return x == 1 ? Z::LO : Z::S;
+        return us & 1 ? Z::S : Z::LO;
     }
     __device__ __forceinline__ void commit(uint64_t* bar) const {
         if (elect()) mma_commit(bar);
@@ -665,14 +666,15 @@ struct TcBlock {
         if (!wait(&sh.kv_full[0], 0)) return;
         if constexpr (BF && !OUT) {
             // The state pass of bf16: K's weights reach to the segment's end, U adds up over all
-            // chunks, and the state is read once.  K's lower parts have two buffers: a chunk is
-            // weighed while the last one is multiplied.
+            // chunks, and the state is read once.  Where K takes two parts, the second has two
+            // buffers: a chunk is weighed while the last one is multiplied.
             if (in) pass(tid, 1.0f, false, 0, true, exp2f(l2 * (float)len), nullptr);
             const int n_kv = nch * nk;
             for (int kv = 0; kv < n_kv; ++kv) {
                 a = chunk_at(kv / nk, &n);
                 if (kv > 0 && !wait(&sh.kv_full[kv % NS], kv / NS)) return;
-                if (kv > 1 && !wait(&sh.u_done[kv & 1], (kv - 2) >> 1)) return;  // the parts' buffer is free
+                const int last = kv - (exact ? 1 : 2);  // the parts' buffer is free
+                if (last >= 0 && !wait(&sh.u_done[last & 1], last >> 1)) return;
                 const int64_t far = rev ? a - t0 : t0 + len - a - n;
                 scan(kv, n, tid);
                 weigh(kv, n, 1.0f, tid, exp2f(l2 * (float)far), kv);
@@ -946,7 +948,8 @@ struct TcBlock {
 };
 
 template <typename T, int DK, int DV, bool OUT>
-__global__ void __launch_bounds__(TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloat16>::value>::NT, 1) k_lin_tc(const __grid_constant__ TcArgs A) {
+__global__ void __launch_bounds__(TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloat16>::value>::NT,
+                                  TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloat16>::value>::BLOCKS) k_lin_tc(const __grid_constant__ TcArgs A) {
     using Z = TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloat16>::value>;
     extern __shared__ __align__(1024) unsigned char sm[];
     TcShared& sh = *reinterpret_cast<TcShared*>(sm + Z::TILES);
@@ -1116,7 +1119,7 @@ static cudaError_t tc_launch(const TcArgs& A, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-static_assert(TcSize<128, 128, true, true>::BYTES <= 232448 && TcSize<128, 128, false, true>::BYTES <= 232448 &&
+static_assert(TcSize<128, 128, true, true>::BYTES <= 232448 && TcSize<128, 128, false, true>::BYTES <= 232448 / 2 - 1024 &&
                   TcSize<128, 128, false, false>::BYTES <= 232448, "shared memory of a block");
 
 template <typename T, bool OUT>
