@@ -1069,29 +1069,33 @@ static cudaError_t encode(CUtensorMap* m, laplex_dtype dt, const LinRows& x, int
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Tokens per segment (a multiple of 128).  A block takes an SM, so a launch of
-// `roles` products runs ceil(blocks / 148) rounds of one segment each; a cut
-// adds the state pass (about half of a product's time, over all but each
-// sequence's last segment) and two launches.  Sequences of one known length take
-// the cheapest number of cuts by that count.  Lengths that only the device knows:
-// pieces for two rounds where the heads do not fill the GPU, else only sequences
-// four times longer than the mean are cut.
+// Tokens per segment (a multiple of 128).  A block of the products takes an SM, so a launch of
+// `roles` products runs ceil(blocks / 148) rounds of one segment each; a round costs its tokens
+// (28 a microsecond) and about 160 tokens' time to start and end.  A cut adds the state pass (0.35
+// of a product's time a token, two blocks on an SM, over all but each sequence's last segment),
+// per direction, and the join of the states.  Sequences of one known length take the cheapest
+// number of cuts by that count.  Lengths that only the device knows: pieces of a third (with three
+// roles a quarter) of an SM's share of all tokens, so that the longest sequence does not decide
+// (24 ragged sequences, 16384 tokens, 8 heads of 4 q-heads: 259 us against 490 us with cuts of 2816).
 int tc_segment(int64_t T, int N, int H, int roles, bool equal) {
     const int64_t whole = std::min<int64_t>(std::max<int64_t>(T, 1) + 1, INT32_MAX);
     if (N == 0 || T == 0) return (int)whole;
-    constexpr int64_t SMS = 148;
+    constexpr int64_t SMS = 148, ENDS = 160;
     const auto up = [](int64_t x) { return (x + TC_C - 1) / TC_C * TC_C; };
     const int64_t heads = (int64_t)N * H;
     int64_t seg;
     if (equal) {
         const int64_t L = T / N;
+        const int dirs = roles > 1 ? 2 : 1;
         double best = 0;
         seg = whole;
         for (int64_t m = 1; m <= 512 && (m == 1 || L / m >= 2 * TC_C); ++m) {
             const int64_t s = up((L + m - 1) / m), pieces = (L + s - 1) / s;
-            const double rounds = (double)((heads * pieces * roles + SMS - 1) / SMS);
-            const double state = (double)((heads * (pieces - 1) + SMS - 1) / SMS) * (roles > 1 ? 2 : 1);
-            const double cost = rounds * s + (m > 1 ? 0.5 * state * s + 400.0 : 0.0);
+            double cost = (double)((heads * pieces * roles + SMS - 1) / SMS) * (s + ENDS);
+            if (m > 1) {
+                cost += 0.35 * (double)((heads * (pieces - 1) * dirs + 2 * SMS - 1) / (2 * SMS)) * 2 * (s + ENDS);
+                cost += dirs * (300.0 + 0.7 * heads * pieces);
+            }
             if (m == 1 || cost < best) {
                 best = cost;
                 seg = m == 1 ? whole : s;
@@ -1099,8 +1103,7 @@ int tc_segment(int64_t T, int N, int H, int roles, bool equal) {
         }
         return (int)seg;
     }
-    if (heads < SMS) seg = std::max<int64_t>(512, up(T * H / (2 * SMS)));
-    else seg = std::max<int64_t>(2048, up(4 * T / N));
+    seg = std::max<int64_t>(512, up(T * H * roles / ((roles > 1 ? 4 : 3) * SMS)));
     return (int)(seg >= T ? whole : seg);
 }
 
