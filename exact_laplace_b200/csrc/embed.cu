@@ -10,16 +10,23 @@
 // Lookup: bound by memory, each row read and written once; a warp moves pieces
 // of 32 lanes x 16 bytes x 4, all four loads in flight.
 //
-// Gradient: the tokens are sorted with their positions (sort.cu), which turns
-// the gradient into sums over runs.  Adding rows into the table with atomics
-// would need fp32 atomics on every value, a pass of rounding for 16-bit tables,
-// and would change from run to run.  k_embed_sum gives each warp R consecutive
-// sorted positions and 32 lanes x 16 bytes of columns: it reads the rows of g
-// (the next rows' loads in flight), sums in fp32 in position order, and writes
-// the rows whose run lies inside its R positions.  A run that crosses a boundary
-// leaves one partial sum per side, joined in order by k_embed_join.  Rows
-// without a token are zeroed by further blocks of the same launch, from a bitmap
-// of the tokens that occur, so that each row of the table is written once.
+// Gradient: the tokens are sorted with their positions, which turns the gradient
+// into sums over runs.  Adding rows into the table with atomics would need fp32
+// atomics on every value, a pass of rounding for 16-bit tables, and would change
+// from run to run.
+//   k_token_sort (up to 65536 tokens): one cluster of up to 8 blocks keeps the
+//     tokens in its shared memory through the stable digit passes and scatters
+//     through distributed shared memory; one launch in place of seven to ten.  More
+//     tokens take the digit passes of sort.cu.
+//   k_embed_sum: a warp takes R consecutive sorted positions and 32 lanes x 16
+//     bytes of columns, reads the rows of g (eight in flight), sums in fp32 in
+//     position order, and writes the rows whose run lies inside its R positions.
+//     A run that crosses a boundary leaves one partial sum per side.  Blocks that
+//     zero the rows without a token, by a bitmap of the tokens that occur, lie
+//     between them, so that reads and writes overlap (write-only traffic ran at
+//     3.8 TB/s) and each row of the table is written once.
+//   k_embed_join: the partial sums of the runs that cross boundaries, in a fixed
+//     order, eight warps to a run.
 #include <algorithm>
 
 #include "devcache.h"
@@ -94,14 +101,193 @@ cudaError_t embed_run(laplex_dtype dt, const EmbedArgs& A, cudaStream_t st) {
 
 // sort keys of the tokens (one outside [0, rows): rows, which sorts last), and
 // the bitmap of the rows that occur
+__device__ __forceinline__ int64_t token_at(const void* tokens, int tok64, int64_t i) {
+    return tok64 ? static_cast<const int64_t*>(tokens)[i] : (int64_t)static_cast<const int32_t*>(tokens)[i];
+}
+
 __global__ void __launch_bounds__(256) k_embed_keys(const void* tokens, int tok64, int64_t n, int64_t rows,
                                                     uint32_t* __restrict__ keys, uint32_t* __restrict__ seen) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= n) return;
-    const int64_t tok = tok64 ? static_cast<const int64_t*>(tokens)[i] : (int64_t)static_cast<const int32_t*>(tokens)[i];
+    const int64_t tok = token_at(tokens, tok64, i);
     const bool known = tok >= 0 && tok < rows;
     keys[i] = known ? (uint32_t)tok : (uint32_t)rows;
     if (known && seen) atomicOr(seen + (tok >> 5), 1u << (tok & 31));  // an or: the order does not matter
+}
+
+// ---- up to TS_MAX tokens: one cluster
+constexpr int TS_NT = 512, TS_NW = TS_NT / 32, TS_CAP = 8192, TS_MAX = 8 * TS_CAP, TS_BINS = 1024;
+
+struct TokenSort {
+    const void* tokens;
+    int tok64;
+    int n, shift;      // a block holds 1 << shift tokens
+    int64_t rows;
+    int passes, bits;  // digits of `bits` bits
+    uint32_t* skeys;
+    int32_t* perm;
+    uint32_t* seen;    // or NULL
+    int64_t words;     // of seen
+};
+
+struct TokenSortShared {
+    uint2 pair[2][TS_CAP];         // key, position
+    uint32_t cnt[TS_NW][TS_BINS];  // per warp: counts, then the earlier warps' counts
+    uint32_t hist[TS_BINS];        // this block's counts, read by the whole cluster
+    uint32_t base[TS_BINS];
+    uint32_t wsum[TS_NW];
+};
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote(const void* p, int rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ uint32_t ld_remote(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_remote(uint32_t a, uint2 v) {
+    asm volatile("st.shared::cluster.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
+}
+
+// Stable LSD passes.  Block b holds the positions b << shift .. of the current
+// order, each warp a contiguous part; a key's place is the count of smaller digits
+// in the cluster, of its digit in earlier blocks, in earlier warps of its block,
+// and before it in its warp.
+__global__ void __launch_bounds__(TS_NT) k_token_sort(const __grid_constant__ TokenSort P) {
+    extern __shared__ __align__(16) unsigned char raw[];
+    TokenSortShared& sh = *reinterpret_cast<TokenSortShared*>(raw);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int me = blockIdx.x, blocks = gridDim.x;  // the grid is one cluster
+    const int lo = me << P.shift, count = max(0, min(1 << P.shift, P.n - lo));
+    const int bins = 1 << P.bits;
+    if (P.seen)
+        for (int64_t i = (int64_t)me * TS_NT + tid; i < P.words; i += (int64_t)blocks * TS_NT) P.seen[i] = 0;
+    cluster_sync();  // the bitmap is clear (and every block of the cluster runs)
+    for (int i = tid; i < count; i += TS_NT) {
+        const int64_t tok = token_at(P.tokens, P.tok64, lo + i);
+        const bool known = tok >= 0 && tok < P.rows;
+        sh.pair[0][i] = make_uint2(known ? (uint32_t)tok : (uint32_t)P.rows, (uint32_t)(lo + i));
+        if (known && P.seen) atomicOr(P.seen + (tok >> 5), 1u << (tok & 31));
+    }
+    const int per = ((1 << P.shift) / TS_NW + 31) / 32 * 32;  // positions of a warp
+    const int w0 = warp * per, w1 = min(count, w0 + per);
+    for (int pass = 0; pass < P.passes; ++pass) {
+        const uint2* pair = sh.pair[pass & 1];
+        const int down = P.bits * pass;
+        for (int i = lane; i < bins; i += 32) sh.cnt[warp][i] = 0;
+        __syncthreads();
+        uint32_t rank[TS_CAP / TS_NT];
+#pragma unroll
+        for (int r = 0; r < TS_CAP / TS_NT; ++r) {
+            const int i = w0 + r * 32 + lane;
+            if (w0 + r * 32 >= w1) break;
+            const bool in = i < w1;
+            const uint32_t d = in ? pair[i].x >> down & (bins - 1) : TS_BINS;
+            const uint32_t same = __match_any_sync(FULL, d);
+            const uint32_t before = in ? sh.cnt[warp][d] : 0;
+            rank[r] = before + __popc(same & ((1u << lane) - 1));
+            __syncwarp();
+            if (in && lane == 31 - __clz(same)) sh.cnt[warp][d] = rank[r] + 1;
+            __syncwarp();
+        }
+        __syncthreads();
+        for (int d = tid; d < bins; d += TS_NT) {
+            uint32_t s = 0;
+#pragma unroll
+            for (int w = 0; w < TS_NW; ++w) {
+                const uint32_t c = sh.cnt[w][d];
+                sh.cnt[w][d] = s;
+                s += c;
+            }
+            sh.hist[d] = s;
+        }
+        cluster_sync();
+        // exclusive sums over the digits (a warp takes bins / 16 consecutive ones), plus the earlier blocks'
+        const int span = max(1, bins / TS_NW);
+        uint32_t sum = 0;
+        for (int x = 0; x < span; x += 32) {
+            const int d = warp * span + x + lane;
+            uint32_t mine = 0, all = 0;
+            if (x + lane < span && d < bins)
+                for (int b = 0; b < blocks; ++b) {
+                    const uint32_t c = ld_remote(remote(&sh.hist[d], b));
+                    if (b < me) mine += c;
+                    all += c;
+                }
+            uint32_t scan = all;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(FULL, scan, o);
+                if (lane >= o) scan += v;
+            }
+            if (x + lane < span && d < bins) sh.base[d] = sum + scan - all + mine;
+            sum += __shfl_sync(FULL, scan, 31);
+        }
+        if (lane == 0) sh.wsum[warp] = sum;
+        __syncthreads();
+        uint32_t lead = 0;
+        for (int w = 0; w < warp; ++w) lead += sh.wsum[w];
+        for (int x = lane; x < span; x += 32)
+            if (warp * span + x < bins) sh.base[warp * span + x] += lead;
+        __syncthreads();
+        const bool last = pass == P.passes - 1;
+#pragma unroll
+        for (int r = 0; r < TS_CAP / TS_NT; ++r) {
+            const int i = w0 + r * 32 + lane;
+            if (i >= w1) break;
+            const uint2 v = pair[i];
+            const uint32_t d = v.x >> down & (bins - 1);
+            const uint32_t at = sh.base[d] + sh.cnt[warp][d] + rank[r];
+            if (last) {
+                P.skeys[at] = v.x;
+                P.perm[at] = (int32_t)v.y;
+            } else
+                st_remote(remote(&sh.pair[~pass & 1][at & ((1u << P.shift) - 1)], at >> P.shift), v);
+        }
+        cluster_sync();  // the keys have arrived (and no block leaves while its memory is read)
+    }
+}
+
+static cudaError_t token_sort(const EmbedArgs& A, uint32_t* skeys, int32_t* perm, uint32_t* seen, cudaStream_t st) {
+    TokenSort P;
+    P.tokens = A.tokens;
+    P.tok64 = A.tok64;
+    P.n = (int)A.n;
+    P.rows = A.rows;
+    P.skeys = skeys;
+    P.perm = perm;
+    P.seen = seen;
+    P.words = (A.rows + 31) / 32;
+    int bits = 1;
+    while (bits < 31 && (A.rows >> bits) != 0) ++bits;
+    P.passes = (bits + 9) / 10;  // as few as 1024 digits allow
+    P.bits = (bits + P.passes - 1) / P.passes;
+    P.shift = 10;  // from 1024 tokens a block: fewer leave most of its warps idle
+    while (((int64_t)8 << P.shift) < A.n) ++P.shift;
+    const unsigned blocks = (unsigned)((A.n + (1 << P.shift) - 1) >> P.shift);
+    int dev = 0, sms = 0, per = 0;
+    cudaError_t e = current_device_sms(&dev, &sms);
+    if (e == cudaSuccess) e = blocks_per_sm<&k_token_sort>(dev, TS_NT, sizeof(TokenSortShared), &per);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(TS_NT);
+    cfg.dynamicSmemBytes = sizeof(TokenSortShared);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = blocks;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_token_sort, P);
 }
 
 struct EmbedSum {
@@ -112,7 +298,7 @@ struct EmbedSum {
     void* part;             // [tiles][2][dim]: sums of the runs that enter / leave a tile
     int64_t tiles;
     int R;                  // sorted positions per tile
-    int64_t sum_blocks;     // blocks of the sums; the rest zero the rows without a token
+    int64_t sum_blocks, zero_blocks;  // blocks of the sums, and those that zero the rows without a token
 };
 
 template <typename T, typename W, int VN>
@@ -137,21 +323,26 @@ __global__ void __launch_bounds__(EMB_NT) k_embed_sum(const __grid_constant__ Em
     constexpr int U = 8;  // rows in flight
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const EmbedArgs& E = P.A;
-    if ((int64_t)blockIdx.x >= P.sum_blocks) {
-        // zero rows: a warp per row
-        const int64_t zb = (int64_t)gridDim.x - P.sum_blocks;
-        for (int64_t r = ((int64_t)blockIdx.x - P.sum_blocks) * (EMB_NT / 32) + warp; r < E.rows; r += zb * (EMB_NT / 32)) {
-            if (P.seen[r >> 5] >> (r & 31) & 1) continue;
-            W* p = static_cast<W*>(E.dst) + r * E.dst_ld;
-            Pack<W, VN> z;
+    // the zeroing blocks lie evenly between the others: block b is the (b zero / all)-th of them
+    const int64_t all = P.sum_blocks + P.zero_blocks, b = blockIdx.x;
+    const int64_t z = b * P.zero_blocks / all, z1 = (b + 1) * P.zero_blocks / all;
+    if (z1 > z) {
+        // a warp takes 8 rows at a time
+        Pack<W, VN> o;
 #pragma unroll
-            for (int e = 0; e < VN; ++e) z.v[e] = from_acc<W, typename AccOf<W>::A>(0);
-            for (int64_t c = lane * VN; c < E.dim; c += 32 * VN) *reinterpret_cast<Pack<W, VN>*>(p + c) = z;
+        for (int e = 0; e < VN; ++e) o.v[e] = from_acc<W, typename AccOf<W>::A>(0);
+        for (int64_t r = (z * (EMB_NT / 32) + warp) * 8; r < E.rows; r += P.zero_blocks * (EMB_NT / 32) * 8) {
+            const uint32_t word = P.seen[r >> 5] >> (r & 31);
+            for (int k = 0; k < 8 && r + k < E.rows; ++k) {
+                if (word >> k & 1) continue;
+                W* p = static_cast<W*>(E.dst) + (r + k) * E.dst_ld;
+                for (int64_t c = lane * VN; c < E.dim; c += 32 * VN) *reinterpret_cast<Pack<W, VN>*>(p + c) = o;
+            }
         }
         return;
     }
     const int64_t cols = (E.dim + 32 * VN - 1) / (32 * VN);
-    const int64_t w = (int64_t)blockIdx.x * (EMB_NT / 32) + warp;
+    const int64_t w = (b - z) * (EMB_NT / 32) + warp;
     const int64_t tile = w / cols;
     if (tile >= P.tiles) return;
     const int64_t c = ((w - tile * cols) * 32 + lane) * VN;
@@ -166,35 +357,41 @@ __global__ void __launch_bounds__(EMB_NT) k_embed_sum(const __grid_constant__ Em
     uint32_t cur = P.keys[p0];
     bool entered = cur == before;  // the run began in an earlier tile
     A* part = static_cast<A*>(P.part) + tile * 2 * E.dim + c;
-    for (int64_t p = p0; p < p1; p += U) {
-        Pack<T, VN> v[U];
-        uint32_t key[U];
+    for (int64_t q0 = p0; q0 < p1; q0 += 32) {
+        // 32 positions at once: a lane has the key and the row of one
+        const bool has = q0 + lane < p1;
+        const uint32_t mykey = has ? P.keys[q0 + lane] : none;
+        const int32_t myrow = has ? P.perm[q0 + lane] : 0;
+        const int m = (int)min((int64_t)32, p1 - q0);
+        for (int p = 0; p < m; p += U) {
+            Pack<T, VN> v[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            key[u] = p + u < p1 ? P.keys[p + u] : none;
-            if (in && key[u] != none) {
-                const int64_t i = P.perm[p + u];
-                v[u] = *reinterpret_cast<const Pack<T, VN>*>(static_cast<const T*>(E.src) + i * E.src_ld + c);
+            for (int u = 0; u < U; ++u) {
+                const uint32_t key = __shfl_sync(FULL, mykey, (p + u) & 31);
+                const int64_t i = __shfl_sync(FULL, myrow, (p + u) & 31);
+                if (in && key != none && p + u < m)
+                    v[u] = *reinterpret_cast<const Pack<T, VN>*>(static_cast<const T*>(E.src) + i * E.src_ld + c);
             }
-        }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (p + u >= p1) break;
-            if (key[u] != cur) {
-                if (in && cur != none) {
-                    if (entered) {
+            for (int u = 0; u < U; ++u) {
+                const uint32_t key = __shfl_sync(FULL, mykey, (p + u) & 31);
+                if (p + u >= m) break;
+                if (key != cur) {
+                    if (in && cur != none) {
+                        if (entered) {
 #pragma unroll
-                        for (int e = 0; e < VN; ++e) part[e] = s[e];
-                    } else embed_write<T, W, VN>(E, cur, c, s);
+                            for (int e = 0; e < VN; ++e) part[e] = s[e];
+                        } else embed_write<T, W, VN>(E, cur, c, s);
+                    }
+#pragma unroll
+                    for (int e = 0; e < VN; ++e) s[e] = 0;
+                    cur = key;
+                    entered = false;
                 }
+                if (in && cur != none)
 #pragma unroll
-                for (int e = 0; e < VN; ++e) s[e] = 0;
-                cur = key[u];
-                entered = false;
+                    for (int e = 0; e < VN; ++e) s[e] += to_acc<A, T>(v[u].v[e]);
             }
-            if (in && cur != none)
-#pragma unroll
-                for (int e = 0; e < VN; ++e) s[e] += to_acc<A, T>(v[u].v[e]);
         }
     }
     if (!in || cur == none) return;
@@ -207,28 +404,70 @@ __global__ void __launch_bounds__(EMB_NT) k_embed_sum(const __grid_constant__ Em
     } else embed_write<T, W, VN>(E, cur, c, s);
 }
 
-// The runs that cross tile boundaries: the tile a run leaves joins its parts in order.
-template <typename T, typename W>
+// The runs that cross tile boundaries, by the tile that a run leaves: eight warps
+// sum an eighth of its parts each, in order, and the eight are joined in order.
+// VN columns a lane.
+template <typename T, typename W, int VN>
 __global__ void __launch_bounds__(EMB_NT) k_embed_join(const __grid_constant__ EmbedSum P) {
     using A = typename AccOf<T>::A;
+    constexpr int NW = EMB_NT / 32;
+    __shared__ __align__(16) A red[NW][32 * VN];
     const EmbedArgs& E = P.A;
-    const int64_t tile = blockIdx.x, p0 = tile * P.R, p1 = p0 + P.R;
-    if (p1 >= E.n) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // this block's tiles: those of blockIdx.x + t gridDim.x that a run leaves which began in them
+    __shared__ int64_t todo[EMB_NT];
+    __shared__ int found;
+    for (int64_t t0 = blockIdx.x; t0 < P.tiles - 1; t0 += (int64_t)gridDim.x * EMB_NT) {
+    if (threadIdx.x == 0) found = 0;
+    __syncthreads();
+    {
+        const int64_t t = t0 + (int64_t)threadIdx.x * gridDim.x;
+        if (t < P.tiles - 1) {  // (the last tile leaves nothing)
+            const int64_t a = t * P.R, b = a + P.R;
+            const uint32_t k = P.keys[b - 1];
+            if (k != (uint32_t)E.rows && P.keys[b] == k && !(a > 0 && P.keys[a] == k && P.keys[a - 1] == k))
+                todo[atomicAdd(&found, 1)] = t;  // (in any order: each has its own row)
+        }
+    }
+    __syncthreads();
+    for (int f = 0; f < found; ++f) {
+    const int64_t tile = todo[f], p1 = (tile + 1) * P.R;
     const uint32_t key = P.keys[p1 - 1];
-    if (key == (uint32_t)E.rows || P.keys[p1] != key) return;
-    if (P.keys[p0] == key && p0 > 0 && P.keys[p0 - 1] == key) return;  // it began earlier
     // tiles that the run enters: as long as their first key is this one
-    int64_t lo = tile + 1, hi = P.tiles;  // the first tile past the run (keys ascend)
+    int64_t lo = tile + 1, hi = P.tiles;  // the first tile past the run (equal keys lie together)
     while (lo < hi) {
         const int64_t mid = (lo + hi) >> 1;
         if (P.keys[mid * P.R] == key) lo = mid + 1; else hi = mid;
     }
-    const A* part = static_cast<const A*>(P.part);
-    for (int64_t c = (int64_t)blockIdx.y * EMB_NT + threadIdx.x; c < E.dim; c += (int64_t)gridDim.y * EMB_NT) {
-        A s = part[(tile * 2 + 1) * E.dim + c];
+    // part 0 is the one of this tile's end, part i > 0 the one of tile + i's start
+    const int64_t parts = lo - tile, a0 = parts * warp / NW, a1 = parts * (warp + 1) / NW;
+    const A* part = static_cast<const A*>(P.part) + tile * 2 * E.dim;
+    for (int64_t cb = (int64_t)blockIdx.y * 32 * VN; cb < E.dim; cb += (int64_t)gridDim.y * 32 * VN) {
+        const int64_t c = cb + lane * VN;
+        A s[VN];
+#pragma unroll
+        for (int e = 0; e < VN; ++e) s[e] = 0;
+        if (c < E.dim) {
 #pragma unroll 8
-        for (int64_t t = tile + 1; t < lo; ++t) s += part[t * 2 * E.dim + c];
-        embed_write<T, W, 1>(E, key, c, &s);
+            for (int64_t i = a0; i < a1; ++i) {
+                const Pack<A, VN> v = *reinterpret_cast<const Pack<A, VN>*>(part + (i == 0 ? E.dim : i * 2 * E.dim) + c);
+#pragma unroll
+                for (int e = 0; e < VN; ++e) s[e] += v.v[e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < VN; ++e) red[warp][lane * VN + e] = s[e];
+        __syncthreads();
+        for (int x = threadIdx.x; x < 32 * VN; x += EMB_NT) {
+            A t = 0;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) t += red[w][x];
+            if (cb + x < E.dim) embed_write<T, W, 1>(E, key, cb + x, &t);
+        }
+        __syncthreads();
+    }
+    }
+    __syncthreads();  // `found` has been read
     }
 }
 
@@ -252,7 +491,7 @@ static EmbedWs embed_ws(int64_t n, int64_t rows, int64_t dim, laplex_dtype dt) {
     W.perm = Carve::need((size_t)n, 4);
     W.seen = Carve::need((size_t)((rows + 31) / 32), 4);
     W.part = Carve::need((size_t)(tiles * 2 * dim), acc_bytes(dt));
-    W.sort = sort_keys_ws_bytes(n);
+    W.sort = n <= TS_MAX ? 0 : sort_keys_ws_bytes(n);
     return W;
 }
 
@@ -267,15 +506,19 @@ static cudaError_t embed_sum_launch(EmbedSum S, int sms, cudaStream_t st) {
     const bool vec = vec_ok(S.A, VN, sizeof(T), sizeof(W), std::min<int>(16, VN * sizeof(W)));
     const int64_t cols = (S.A.dim + 32 * (vec ? VN : 1) - 1) / (32 * (vec ? VN : 1));
     S.sum_blocks = (S.tiles * cols + EMB_NT / 32 - 1) / (EMB_NT / 32);
-    const int64_t zero = S.A.accumulate ? 0 : std::min<int64_t>((S.A.rows + EMB_NT / 32 - 1) / (EMB_NT / 32), 8 * (int64_t)sms);
-    const int64_t grid = S.sum_blocks + zero;
+    S.zero_blocks = S.A.accumulate ? 0 : std::min<int64_t>((S.A.rows + 63) / 64, 8 * (int64_t)sms);
+    const int64_t grid = S.sum_blocks + S.zero_blocks;
     if (grid > 0) {
         if (vec) k_embed_sum<T, W, VN><<<(unsigned)grid, EMB_NT, 0, st>>>(S);
         else k_embed_sum<T, W, 1><<<(unsigned)grid, EMB_NT, 0, st>>>(S);
     }
     if (S.tiles > 1) {
-        const dim3 jg((unsigned)(S.tiles - 1), (unsigned)std::min<int64_t>((S.A.dim + EMB_NT - 1) / EMB_NT, 65535));
-        k_embed_join<T, W><<<jg, EMB_NT, 0, st>>>(S);
+        constexpr int JN = 16 / (int)sizeof(typename AccOf<T>::A);
+        const bool jvec = S.A.dim % JN == 0;
+        const int64_t jcols = (S.A.dim + 32 * (jvec ? JN : 1) - 1) / (32 * (jvec ? JN : 1));
+        const dim3 jg((unsigned)std::min<int64_t>(S.tiles - 1, 2 * (int64_t)sms), (unsigned)std::min<int64_t>(jcols, 8));
+        if (jvec) k_embed_join<T, W, JN><<<jg, EMB_NT, 0, st>>>(S);
+        else k_embed_join<T, W, 1><<<jg, EMB_NT, 0, st>>>(S);
     }
     return cudaGetLastError();
 }
@@ -295,16 +538,18 @@ cudaError_t embed_bwd_run(laplex_dtype dt, laplex_dtype out_dt, const EmbedArgs&
     uint32_t* seen = (uint32_t*)(p += Z.perm);
     void* part = p += Z.seen;
     void* sort = p += Z.part;
-    if (!A.accumulate) {
-        e = cudaMemsetAsync(seen, 0, (size_t)((A.rows + 31) / 32) * 4, st);
+    uint32_t* bits = A.accumulate ? nullptr : seen;
+    if (A.n > 0 && A.n <= TS_MAX) {
+        e = token_sort(A, skeys, perm, bits, st);
         if (e != cudaSuccess) return e;
-    }
-    if (A.n > 0) {
-        k_embed_keys<<<(unsigned)((A.n + 255) / 256), 256, 0, st>>>(A.tokens, A.tok64, A.n, A.rows, keys,
-                                                                   A.accumulate ? nullptr : seen);
-        e = cudaGetLastError();
-        if (e == cudaSuccess)
-            e = sort_keys_run(keys, A.n, (uint32_t)A.rows, skeys, perm, sort, Z.sort, status, st);
+    } else {
+        if (bits) e = cudaMemsetAsync(seen, 0, (size_t)((A.rows + 31) / 32) * 4, st);
+        if (e == cudaSuccess && A.n > 0) {
+            k_embed_keys<<<(unsigned)((A.n + 255) / 256), 256, 0, st>>>(A.tokens, A.tok64, A.n, A.rows, keys, bits);
+            e = cudaGetLastError();
+            if (e == cudaSuccess)
+                e = sort_keys_run(keys, A.n, (uint32_t)A.rows, skeys, perm, sort, Z.sort, status, st);
+        }
         if (e != cudaSuccess) return e;
     }
     EmbedSum S;
@@ -315,7 +560,7 @@ cudaError_t embed_bwd_run(laplex_dtype dt, laplex_dtype out_dt, const EmbedArgs&
     S.part = part;
     S.R = embed_tile(A.n, A.dim, (int)elem_bytes(dt));
     S.tiles = (A.n + S.R - 1) / S.R;
-    S.sum_blocks = 0;
+    S.sum_blocks = S.zero_blocks = 0;
     const bool f32 = out_dt == LAPLEX_F32;
     switch (dt) {
         case LAPLEX_F32: return embed_sum_launch<float, float>(S, sms, st);
