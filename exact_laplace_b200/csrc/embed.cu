@@ -19,9 +19,10 @@
 //     through distributed shared memory; one launch in place of seven to ten.  More
 //     tokens take the digit passes of sort.cu.
 //   k_embed_sum: a warp takes R consecutive sorted positions and 32 lanes x 16
-//     bytes of columns, reads the rows of g (eight in flight), sums in fp32 in
+//     bytes of columns, reads the rows of g (16 to 32 in flight), sums in fp32 in
 //     position order, and writes the rows whose run lies inside its R positions.
-//     A run that crosses a boundary leaves one partial sum per side.  Blocks that
+//     A run that crosses a boundary by up to 16 positions belongs to the warp before
+//     it; a longer one leaves one partial sum per side.  Blocks that
 //     zero the rows without a token, by a bitmap of the tokens that occur, lie
 //     between them, so that reads and writes overlap (write-only traffic ran at
 //     3.8 TB/s) and each row of the table is written once.
@@ -132,10 +133,11 @@ struct TokenSort {
 
 struct TokenSortShared {
     uint2 pair[2][TS_CAP];         // key, position
-    uint32_t cnt[TS_NW][TS_BINS];  // per warp: counts, then the earlier warps' counts
+    uint32_t cnt[TS_NW][TS_BINS];  // per warp: counts, then the earlier warps' counts and the smaller digits'
     uint32_t hist[TS_BINS];        // this block's counts, read by the whole cluster
-    uint32_t base[TS_BINS];
-    uint32_t wsum[TS_NW];
+    uint32_t hist2[TS_BINS];       // where a digit starts in this block's order
+    uint32_t delta[TS_BINS];       // from a place in this block's order to the one in the cluster's
+    uint32_t wsum[2][TS_NW];
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -173,7 +175,6 @@ __global__ void __launch_bounds__(TS_NT) k_token_sort(const __grid_constant__ To
         const int64_t tok = token_at(P.tokens, P.tok64, lo + i);
         const bool known = tok >= 0 && tok < P.rows;
         sh.pair[0][i] = make_uint2(known ? (uint32_t)tok : (uint32_t)P.rows, (uint32_t)(lo + i));
-        if (known && P.seen) atomicOr(P.seen + (tok >> 5), 1u << (tok & 31));
     }
     const int per = ((1 << P.shift) / TS_NW + 31) / 32 * 32;  // positions of a warp
     const int w0 = warp * per, w1 = min(count, w0 + per);
@@ -182,14 +183,23 @@ __global__ void __launch_bounds__(TS_NT) k_token_sort(const __grid_constant__ To
         const int down = P.bits * pass;
         for (int i = lane; i < bins; i += 32) sh.cnt[warp][i] = 0;
         __syncthreads();
+        // ranks in the warp; the pairs move to registers
         uint32_t rank[TS_CAP / TS_NT];
+        uint2 v[TS_CAP / TS_NT];
 #pragma unroll
         for (int r = 0; r < TS_CAP / TS_NT; ++r) {
             const int i = w0 + r * 32 + lane;
             if (w0 + r * 32 >= w1) break;
             const bool in = i < w1;
-            const uint32_t d = in ? pair[i].x >> down & (bins - 1) : TS_BINS;
-            const uint32_t same = __match_any_sync(FULL, d);
+            v[r] = in ? pair[i] : make_uint2(0, 0);
+            const uint32_t d = in ? v[r].x >> down & (bins - 1) : TS_BINS;
+            // the lanes with this digit, a ballot per bit (a warp match takes a step per distinct digit)
+            uint32_t same = __ballot_sync(FULL, in);
+            for (int k = 0; k < P.bits; ++k) {
+                const bool bit = d >> k & 1;
+                const uint32_t m = __ballot_sync(FULL, bit);
+                same &= bit ? m : ~m;
+            }
             const uint32_t before = in ? sh.cnt[warp][d] : 0;
             rank[r] = before + __popc(same & ((1u << lane) - 1));
             __syncwarp();
@@ -208,47 +218,80 @@ __global__ void __launch_bounds__(TS_NT) k_token_sort(const __grid_constant__ To
             sh.hist[d] = s;
         }
         cluster_sync();
-        // exclusive sums over the digits (a warp takes bins / 16 consecutive ones), plus the earlier blocks'
+        // exclusive sums over the digits (a warp takes bins / 16 consecutive ones) of the cluster's
+        // and of this block's counts; the first plus the earlier blocks' is where a digit goes
         const int span = max(1, bins / TS_NW);
-        uint32_t sum = 0;
+        uint32_t sum = 0, own = 0;
         for (int x = 0; x < span; x += 32) {
             const int d = warp * span + x + lane;
-            uint32_t mine = 0, all = 0;
-            if (x + lane < span && d < bins)
-                for (int b = 0; b < blocks; ++b) {
-                    const uint32_t c = ld_remote(remote(&sh.hist[d], b));
-                    if (b < me) mine += c;
-                    all += c;
+            const bool in = x + lane < span && d < bins;
+            uint32_t mine = 0, all = 0, here = 0;
+            if (in) {
+                uint32_t c[8];
+#pragma unroll
+                for (int b = 0; b < 8; ++b) c[b] = b < blocks ? ld_remote(remote(&sh.hist[d], b)) : 0;
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    if (b < me) mine += c[b];
+                    if (b == me) here = c[b];
+                    all += c[b];
                 }
-            uint32_t scan = all;
+            }
+            uint32_t sa = all, so = here;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(FULL, scan, o);
-                if (lane >= o) scan += v;
+                const uint32_t p = __shfl_up_sync(FULL, sa, o), q = __shfl_up_sync(FULL, so, o);
+                if (lane >= o) {
+                    sa += p;
+                    so += q;
+                }
             }
-            if (x + lane < span && d < bins) sh.base[d] = sum + scan - all + mine;
-            sum += __shfl_sync(FULL, scan, 31);
+            if (in) {
+                sh.delta[d] = (sum + sa - all + mine) - (own + so - here);
+                sh.hist2[d] = own + so - here;
+            }
+            sum += __shfl_sync(FULL, sa, 31);
+            own += __shfl_sync(FULL, so, 31);
         }
-        if (lane == 0) sh.wsum[warp] = sum;
+        if (lane == 0) {
+            sh.wsum[0][warp] = sum;
+            sh.wsum[1][warp] = own;
+        }
         __syncthreads();
-        uint32_t lead = 0;
-        for (int w = 0; w < warp; ++w) lead += sh.wsum[w];
+        uint32_t lead = 0, mylead = 0;
+        for (int w = 0; w < warp; ++w) {
+            lead += sh.wsum[0][w];
+            mylead += sh.wsum[1][w];
+        }
         for (int x = lane; x < span; x += 32)
-            if (warp * span + x < bins) sh.base[warp * span + x] += lead;
+            if (warp * span + x < bins) {
+                sh.delta[warp * span + x] += lead - mylead;
+                sh.hist2[warp * span + x] += mylead;
+            }
         __syncthreads();
-        const bool last = pass == P.passes - 1;
+        // into this block's order first: scattered writes of single pairs to other blocks, and of
+        // single words to device memory, take a cycle each (38 us for 65536 tokens, 19 a pass)
+        uint2* order = sh.pair[pass & 1];
 #pragma unroll
         for (int r = 0; r < TS_CAP / TS_NT; ++r) {
-            const int i = w0 + r * 32 + lane;
-            if (i >= w1) break;
-            const uint2 v = pair[i];
-            const uint32_t d = v.x >> down & (bins - 1);
-            const uint32_t at = sh.base[d] + sh.cnt[warp][d] + rank[r];
+            if (w0 + r * 32 + lane >= w1) break;
+            const uint32_t d = v[r].x >> down & (bins - 1);
+            order[sh.hist2[d] + sh.cnt[warp][d] + rank[r]] = v[r];
+        }
+        __syncthreads();
+        const bool last = pass == P.passes - 1;
+        for (int i = tid; i < count; i += TS_NT) {
+            const uint2 x = order[i];
+            const uint32_t at = i + sh.delta[x.x >> down & (bins - 1)];
             if (last) {
-                P.skeys[at] = v.x;
-                P.perm[at] = (int32_t)v.y;
+                P.skeys[at] = x.x;
+                P.perm[at] = (int32_t)x.y;
+                // once per run and block (equal keys lie together): atomics on the word of a frequent
+                // token, one per occurrence, took a third of the kernel
+                if (P.seen && x.x != (uint32_t)P.rows && (i == 0 || order[i - 1].x != x.x))
+                    atomicOr(P.seen + (x.x >> 5), 1u << (x.x & 31));
             } else
-                st_remote(remote(&sh.pair[~pass & 1][at & ((1u << P.shift) - 1)], at >> P.shift), v);
+                st_remote(remote(&sh.pair[~pass & 1][at & ((1u << P.shift) - 1)], at >> P.shift), x);
         }
         cluster_sync();  // the keys have arrived (and no block leaves while its memory is read)
     }
@@ -317,10 +360,38 @@ __device__ __forceinline__ void embed_write(const EmbedArgs& A, int64_t row, int
     *reinterpret_cast<Pack<W, VN>*>(p) = o;
 }
 
+// Whether the run across position p (a tile's start) is long, that is, reaches more than SUM_H
+// positions past p: its parts are joined later.  A short one belongs to the tile before p, and
+// *end is where it ends (p: no run crosses).
+constexpr int SUM_H = 16;
+__device__ __forceinline__ bool long_run(const uint32_t* keys, int64_t p, int64_t n) {
+    return p > 0 && p + SUM_H < n && keys[p - 1] == keys[p + SUM_H];  // (keys ascend)
+}
+__device__ __forceinline__ bool border(const uint32_t* keys, int64_t p, int64_t n, int lane, int64_t* end) {
+    *end = min(p, n);
+    if (p <= 0 || p >= n) return false;
+    const uint32_t k = keys[p - 1];
+    const bool same = lane <= SUM_H && p + lane < n && keys[p + lane] == k;
+    const int run = __ffs(~__ballot_sync(FULL, same)) - 1;  // (lane 31 never has it)
+    *end = p + run;
+    return run > SUM_H;
+}
+
+constexpr int SUM_NT = 128;
+
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+
+// VN > 1: rows come through a ring in shared memory by asynchronous copies, 16 in flight
+// while 16 are summed (a lane reads only what it copied).  Loads into registers, eight
+// at a time, left the latency of each round in the open (1.5 TB/s).
 template <typename T, typename W, int VN>
-__global__ void __launch_bounds__(EMB_NT) k_embed_sum(const __grid_constant__ EmbedSum P) {
+__global__ void __launch_bounds__(SUM_NT) k_embed_sum(const __grid_constant__ EmbedSum P) {
     using A = typename AccOf<T>::A;
-    constexpr int U = 8;  // rows in flight
+    constexpr bool RING = VN > 1;
+    constexpr int NW = SUM_NT / 32;
+    extern __shared__ __align__(16) unsigned char raw[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const EmbedArgs& E = P.A;
     // the zeroing blocks lie evenly between the others: block b is the (b zero / all)-th of them
@@ -331,7 +402,7 @@ __global__ void __launch_bounds__(EMB_NT) k_embed_sum(const __grid_constant__ Em
         Pack<W, VN> o;
 #pragma unroll
         for (int e = 0; e < VN; ++e) o.v[e] = from_acc<W, typename AccOf<W>::A>(0);
-        for (int64_t r = (z * (EMB_NT / 32) + warp) * 8; r < E.rows; r += P.zero_blocks * (EMB_NT / 32) * 8) {
+        for (int64_t r = (z * NW + warp) * 8; r < E.rows; r += P.zero_blocks * NW * 8) {
             const uint32_t word = P.seen[r >> 5] >> (r & 31);
             for (int k = 0; k < 8 && r + k < E.rows; ++k) {
                 if (word >> k & 1) continue;
@@ -342,55 +413,80 @@ __global__ void __launch_bounds__(EMB_NT) k_embed_sum(const __grid_constant__ Em
         return;
     }
     const int64_t cols = (E.dim + 32 * VN - 1) / (32 * VN);
-    const int64_t w = (b - z) * (EMB_NT / 32) + warp;
+    const int64_t w = (b - z) * NW + warp;
     const int64_t tile = w / cols;
     if (tile >= P.tiles) return;
     const int64_t c = ((w - tile * cols) * 32 + lane) * VN;
-    const int64_t p0 = tile * P.R, p1 = min(p0 + P.R, E.n);
+    int64_t p0 = tile * P.R, p1 = p0 + P.R, e0, e1;
+    bool entered = border(P.keys, p0, E.n, lane, &e0);  // the run began in an earlier tile
+    const bool leaves = border(P.keys, p1, E.n, lane, &e1);
+    if (!entered) p0 = e0;
+    p1 = leaves ? p1 : e1;
+    if (p0 >= p1) return;
     const uint32_t none = (uint32_t)E.rows;
     const bool in = c < E.dim;
-    const uint32_t before = p0 > 0 ? P.keys[p0 - 1] : 0xffffffffu;
-    const uint32_t after = p1 < E.n ? P.keys[p1] : 0xffffffffu;
     A s[VN];
 #pragma unroll
     for (int e = 0; e < VN; ++e) s[e] = 0;
     uint32_t cur = P.keys[p0];
-    bool entered = cur == before;  // the run began in an earlier tile
     A* part = static_cast<A*>(P.part) + tile * 2 * E.dim + c;
-    for (int64_t q0 = p0; q0 < p1; q0 += 32) {
-        // 32 positions at once: a lane has the key and the row of one
-        const bool has = q0 + lane < p1;
-        const uint32_t mykey = has ? P.keys[q0 + lane] : none;
-        const int32_t myrow = has ? P.perm[q0 + lane] : 0;
-        const int m = (int)min((int64_t)32, p1 - q0);
-        for (int p = 0; p < m; p += U) {
-            Pack<T, VN> v[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t key = __shfl_sync(FULL, mykey, (p + u) & 31);
-                const int64_t i = __shfl_sync(FULL, myrow, (p + u) & 31);
-                if (in && key != none && p + u < m)
-                    v[u] = *reinterpret_cast<const Pack<T, VN>*>(static_cast<const T*>(E.src) + i * E.src_ld + c);
+    Pack<T, VN>* ring = reinterpret_cast<Pack<T, VN>*>(raw) + warp * 2 * SUM_H * 32 + lane;
+    const T* src = static_cast<const T*>(E.src) + c;
+    const int halves = (int)((p1 - p0 + SUM_H - 1) / SUM_H);
+    // a lane's key and row of the half being copied
+    uint32_t key_of[2] = {none, none};
+    int32_t row_of[2] = {0, 0};
+    const auto fetch = [&](int h, uint32_t& k, int32_t& i) {
+        const int64_t p = p0 + (int64_t)h * SUM_H + lane;
+        const bool has = lane < SUM_H && h < halves && p < p1;
+        k = has ? P.keys[p] : none;
+        i = has ? P.perm[p] : 0;
+    };
+    const auto start = [&](int h, uint32_t k, int32_t i) {
+        if constexpr (RING) {
+#pragma unroll 4
+            for (int u = 0; u < SUM_H; ++u) {
+                const uint32_t key = __shfl_sync(FULL, k, u);
+                const int64_t row = __shfl_sync(FULL, i, u);
+                if (in && key != none) copy16(ring + ((h & 1) * SUM_H + u) * 32, src + row * E.src_ld);
             }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+    };
+    fetch(0, key_of[0], row_of[0]);
+    start(0, key_of[0], row_of[0]);
+    fetch(1, key_of[1], row_of[1]);
+    for (int h = 0; h < halves; ++h) {
+        const uint32_t mykey = key_of[0];
+        const int32_t myrow = row_of[0];
+        start(h + 1, key_of[1], row_of[1]);
+        key_of[0] = key_of[1];
+        row_of[0] = row_of[1];
+        fetch(h + 2, key_of[1], row_of[1]);
+        if constexpr (RING) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        const int m = (int)min((int64_t)SUM_H, p1 - p0 - (int64_t)h * SUM_H);
+#pragma unroll 2
+        for (int u = 0; u < m; ++u) {
+            const uint32_t key = __shfl_sync(FULL, mykey, u);
+            const int64_t row = __shfl_sync(FULL, myrow, u);
+            if (key != cur) {
+                if (in && cur != none) {
+                    if (entered) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t key = __shfl_sync(FULL, mykey, (p + u) & 31);
-                if (p + u >= m) break;
-                if (key != cur) {
-                    if (in && cur != none) {
-                        if (entered) {
-#pragma unroll
-                            for (int e = 0; e < VN; ++e) part[e] = s[e];
-                        } else embed_write<T, W, VN>(E, cur, c, s);
-                    }
-#pragma unroll
-                    for (int e = 0; e < VN; ++e) s[e] = 0;
-                    cur = key;
-                    entered = false;
+                        for (int e = 0; e < VN; ++e) part[e] = s[e];
+                    } else embed_write<T, W, VN>(E, cur, c, s);
                 }
-                if (in && cur != none)
 #pragma unroll
-                    for (int e = 0; e < VN; ++e) s[e] += to_acc<A, T>(v[u].v[e]);
+                for (int e = 0; e < VN; ++e) s[e] = 0;
+                cur = key;
+                entered = false;
+            }
+            if (in && cur != none) {
+                Pack<T, VN> v;
+                if constexpr (RING) v = ring[((h & 1) * SUM_H + u) * 32];
+                else v = *reinterpret_cast<const Pack<T, VN>*>(src + row * E.src_ld);
+#pragma unroll
+                for (int e = 0; e < VN; ++e) s[e] += to_acc<A, T>(v.v[e]);
             }
         }
     }
@@ -398,7 +494,7 @@ __global__ void __launch_bounds__(EMB_NT) k_embed_sum(const __grid_constant__ Em
     if (entered) {
 #pragma unroll
         for (int e = 0; e < VN; ++e) part[e] = s[e];
-    } else if (cur == after) {
+    } else if (leaves) {
 #pragma unroll
         for (int e = 0; e < VN; ++e) part[E.dim + e] = s[e];
     } else embed_write<T, W, VN>(E, cur, c, s);
@@ -414,60 +510,69 @@ __global__ void __launch_bounds__(EMB_NT) k_embed_join(const __grid_constant__ E
     __shared__ __align__(16) A red[NW][32 * VN];
     const EmbedArgs& E = P.A;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // this block's tiles: those of blockIdx.x + t gridDim.x that a run leaves which began in them
+    // this block's tiles: those of blockIdx.x + t gridDim.x that a long run leaves which began in them
     __shared__ int64_t todo[EMB_NT];
-    __shared__ int found;
-    for (int64_t t0 = blockIdx.x; t0 < P.tiles - 1; t0 += (int64_t)gridDim.x * EMB_NT) {
-    if (threadIdx.x == 0) found = 0;
-    __syncthreads();
-    {
-        const int64_t t = t0 + (int64_t)threadIdx.x * gridDim.x;
-        if (t < P.tiles - 1) {  // (the last tile leaves nothing)
-            const int64_t a = t * P.R, b = a + P.R;
-            const uint32_t k = P.keys[b - 1];
-            if (k != (uint32_t)E.rows && P.keys[b] == k && !(a > 0 && P.keys[a] == k && P.keys[a - 1] == k))
-                todo[atomicAdd(&found, 1)] = t;  // (in any order: each has its own row)
-        }
-    }
-    __syncthreads();
-    for (int f = 0; f < found; ++f) {
-    const int64_t tile = todo[f], p1 = (tile + 1) * P.R;
-    const uint32_t key = P.keys[p1 - 1];
-    // tiles that the run enters: as long as their first key is this one
-    int64_t lo = tile + 1, hi = P.tiles;  // the first tile past the run (equal keys lie together)
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (P.keys[mid * P.R] == key) lo = mid + 1; else hi = mid;
-    }
-    // part 0 is the one of this tile's end, part i > 0 the one of tile + i's start
-    const int64_t parts = lo - tile, a0 = parts * warp / NW, a1 = parts * (warp + 1) / NW;
-    const A* part = static_cast<const A*>(P.part) + tile * 2 * E.dim;
-    for (int64_t cb = (int64_t)blockIdx.y * 32 * VN; cb < E.dim; cb += (int64_t)gridDim.y * 32 * VN) {
-        const int64_t c = cb + lane * VN;
-        A s[VN];
-#pragma unroll
-        for (int e = 0; e < VN; ++e) s[e] = 0;
-        if (c < E.dim) {
-#pragma unroll 8
-            for (int64_t i = a0; i < a1; ++i) {
-                const Pack<A, VN> v = *reinterpret_cast<const Pack<A, VN>*>(part + (i == 0 ? E.dim : i * 2 * E.dim) + c);
-#pragma unroll
-                for (int e = 0; e < VN; ++e) s[e] += v.v[e];
+    __shared__ int found, past;
+    const auto join = [&](int64_t tile) {
+        const uint32_t key = P.keys[(tile + 1) * P.R - 1];
+        // the first tile past the run: it enters a tile as long as it is long at its start
+        int64_t lo = tile + 1;
+        for (;; lo += EMB_NT) {
+            if (threadIdx.x == 0) past = EMB_NT;
+            __syncthreads();
+            const int64_t t = lo + threadIdx.x;
+            if (!(t < P.tiles && P.keys[t * P.R] == key && long_run(P.keys, t * P.R, E.n))) atomicMin(&past, (int)threadIdx.x);
+            __syncthreads();
+            const int p = past;
+            __syncthreads();
+            if (p < EMB_NT) {
+                lo += p;
+                break;
             }
         }
+        // part 0 is the one of this tile's end, part i > 0 the one of tile + i's start
+        const int64_t parts = lo - tile, a0 = parts * warp / NW, a1 = parts * (warp + 1) / NW;
+        const A* part = static_cast<const A*>(P.part) + tile * 2 * E.dim;
+        for (int64_t cb = (int64_t)blockIdx.y * 32 * VN; cb < E.dim; cb += (int64_t)gridDim.y * 32 * VN) {
+            const int64_t c = cb + lane * VN;
+            A s[VN];
 #pragma unroll
-        for (int e = 0; e < VN; ++e) red[warp][lane * VN + e] = s[e];
+            for (int e = 0; e < VN; ++e) s[e] = 0;
+            if (c < E.dim) {
+#pragma unroll 8
+                for (int64_t i = a0; i < a1; ++i) {
+                    const Pack<A, VN> v = *reinterpret_cast<const Pack<A, VN>*>(part + (i == 0 ? E.dim : i * 2 * E.dim) + c);
+#pragma unroll
+                    for (int e = 0; e < VN; ++e) s[e] += v.v[e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < VN; ++e) red[warp][lane * VN + e] = s[e];
+            __syncthreads();
+            for (int x = threadIdx.x; x < 32 * VN; x += EMB_NT) {
+                A t = 0;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) t += red[w][x];
+                if (cb + x < E.dim) embed_write<T, W, 1>(E, key, cb + x, &t);
+            }
+            __syncthreads();
+        }
+    };
+    for (int64_t t0 = blockIdx.x; t0 < P.tiles - 1; t0 += (int64_t)gridDim.x * EMB_NT) {
+        if (threadIdx.x == 0) found = 0;
         __syncthreads();
-        for (int x = threadIdx.x; x < 32 * VN; x += EMB_NT) {
-            A t = 0;
-#pragma unroll
-            for (int w = 0; w < NW; ++w) t += red[w][x];
-            if (cb + x < E.dim) embed_write<T, W, 1>(E, key, cb + x, &t);
+        {
+            const int64_t t = t0 + (int64_t)threadIdx.x * gridDim.x;
+            if (t < P.tiles - 1) {  // (the last tile leaves nothing)
+                const int64_t a = t * P.R, b = a + P.R;
+                const uint32_t k = P.keys[b - 1];
+                if (k != (uint32_t)E.rows && long_run(P.keys, b, E.n) && !(P.keys[a] == k && long_run(P.keys, a, E.n)))
+                    todo[atomicAdd(&found, 1)] = t;  // (in any order: each has its own row)
+            }
         }
         __syncthreads();
-    }
-    }
-    __syncthreads();  // `found` has been read
+        for (int f = 0; f < found; ++f) join(todo[f]);
+        __syncthreads();  // `found` has been read
     }
 }
 
@@ -505,12 +610,18 @@ static cudaError_t embed_sum_launch(EmbedSum S, int sms, cudaStream_t st) {
     constexpr int VN = VecOf<T>::N;
     const bool vec = vec_ok(S.A, VN, sizeof(T), sizeof(W), std::min<int>(16, VN * sizeof(W)));
     const int64_t cols = (S.A.dim + 32 * (vec ? VN : 1) - 1) / (32 * (vec ? VN : 1));
-    S.sum_blocks = (S.tiles * cols + EMB_NT / 32 - 1) / (EMB_NT / 32);
-    S.zero_blocks = S.A.accumulate ? 0 : std::min<int64_t>((S.A.rows + 63) / 64, 8 * (int64_t)sms);
+    constexpr int NW = SUM_NT / 32;
+    S.sum_blocks = (S.tiles * cols + NW - 1) / NW;
+    S.zero_blocks = S.A.accumulate ? 0 : std::min<int64_t>((S.A.rows + 8 * NW - 1) / (8 * NW), 16 * (int64_t)sms);
     const int64_t grid = S.sum_blocks + S.zero_blocks;
     if (grid > 0) {
-        if (vec) k_embed_sum<T, W, VN><<<(unsigned)grid, EMB_NT, 0, st>>>(S);
-        else k_embed_sum<T, W, 1><<<(unsigned)grid, EMB_NT, 0, st>>>(S);
+        constexpr size_t ring = (size_t)NW * 2 * SUM_H * 32 * 16;
+        int dev = 0, per = 0, n = 0;
+        cudaError_t e = current_device_sms(&dev, &n);
+        if (e == cudaSuccess) e = blocks_per_sm<&k_embed_sum<T, W, VN>>(dev, SUM_NT, ring, &per);
+        if (e != cudaSuccess) return e;
+        if (vec) k_embed_sum<T, W, VN><<<(unsigned)grid, SUM_NT, ring, st>>>(S);
+        else k_embed_sum<T, W, 1><<<(unsigned)grid, SUM_NT, 0, st>>>(S);
     }
     if (S.tiles > 1) {
         constexpr int JN = 16 / (int)sizeof(typename AccOf<T>::A);
