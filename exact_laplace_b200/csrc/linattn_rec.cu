@@ -8,14 +8,17 @@
 //     S_t = e^lam S_{t-1} + k_t v_t^T,      o_t = scale S_t^T q_t.
 // A block holds 64 columns of one head's state in registers (8 row groups x 4
 // columns per thread) and walks a segment of the sequence.  Tokens are taken in
-// blocks of n <= 32: the state is scaled by e^{lam n} once, and inside the block
-// k_tau carries e^{lam (n - 1 - tau)} and q_tau its inverse, so that a token
-// costs two multiply-adds per state element and the rounding of e^lam enters
-// once per n tokens (a product of 2000 rounded e^lam would be off by 6e-5).  n is
-// at most 4 / |lam|: neither factor leaves [e^-4, e^4].
+// blocks of n: the state is scaled by e^{lam n} once, and inside the block v_tau
+// carries e^{lam (n - 1 - tau)} and the output its inverse, so that a token costs
+// two multiply-adds per state element and the rounding of e^lam enters once per n
+// tokens (a product of 2000 rounded e^lam would be off by 6e-5).  n is at most
+// 4 / |lam|: neither factor leaves [e^-4, e^4].
 //
-// Bound by those multiply-adds (4 dk dv flops a token and head): 65536 fp32
-// values of q, k, v and o a microsecond and SM at dk = dv = 128.  Long sequences
+// Rows of the type that it computes in come by asynchronous copies, a block of
+// tokens ahead; 16-bit rows (whose products run elsewhere: linattn_tc.cu) are
+// converted on their way in.
+//
+// Bound by those multiply-adds (4 dk dv flops a token and head).  Long sequences
 // are cut into segments (see LinSeqs): a first pass sums each segment's own
 // state, carry_run joins them, and the product starts each segment from its
 // state.
@@ -29,7 +32,7 @@ namespace lx {
 
 constexpr int REC_NT = 128;
 constexpr int REC_COLS = 64;  // state columns of a block
-constexpr int REC_ROWS = 32;  // rows of k, v, q in shared memory: tokens times heads of a group
+constexpr int REC_MAX = 32;   // most rows (tokens times heads of a group) in one stage
 
 struct RecArgs {
     LinRole R;
@@ -40,24 +43,32 @@ struct RecArgs {
     const void* w_in;    // derivative: by slot, or NULL (zero)
     const void* dstate;  // derivative: the last state's cotangent, or NULL
     double* part;        // derivative: one sum per block
+    int rows;            // rows of k, v, q in one of the two stages: 16, or 32 for more than 16 heads
 };
 
-// rows (token tau of the block, head g) of X, weighted, into dst[row][PITCH]; c0: first column
+// rows (token tau of the block, head g) of X into dst[row][PITCH], from column c0; a warp to a row
 template <typename T, typename A, int PITCH>
 __device__ __forceinline__ void rec_load(A* dst, const LinRows& X, int heads, int h, int64_t t0, int len, int base,
-                                         int n, bool rev, int dim, int c0, A lam, A scale, int sign) {
+                                         int n, bool rev, int dim, int c0) {
     constexpr int VN = VecOf<T>::N;
-    const int cols = min(PITCH, dim - c0);  // a multiple of 8
-    const int per = cols / VN;
-    for (int i = threadIdx.x; i < n * heads * per; i += REC_NT) {
-        const int row = i / per, c = (i - row * per) * VN;
-        const int tau = row / heads, g = row - tau * heads;
+    const int per = min(PITCH, dim - c0) / VN;  // (dims are multiples of 8)
+    const int lane = threadIdx.x & 31;
+    for (int row = threadIdx.x >> 5; row < n * heads; row += REC_NT / 32) {
+        const int tau = heads == 1 ? row : row / heads, g = row - tau * heads;
         const int64_t t = t0 + (rev ? len - 1 - base - tau : base + tau);
-        const T* src = static_cast<const T*>(X.p) + t * X.ts + (int64_t)(h * heads + g) * X.hs + c0 + c;
-        const Pack<T, VN> v = *reinterpret_cast<const Pack<T, VN>*>(src);
-        const A w = sign == 0 ? scale : scale * decay(lam, (A)(sign * (n - 1 - tau)));
+        const T* src = static_cast<const T*>(X.p) + t * X.ts + (int64_t)(h * heads + g) * X.hs + c0;
+        for (int c = lane; c < per; c += 32) {
+            if constexpr (sizeof(T) == sizeof(A)) {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                 (uint32_t)__cvta_generic_to_shared(dst + row * PITCH + c * VN)),
+                             "l"(src + c * VN)
+                             : "memory");
+            } else {
+                const Pack<T, VN> v = *reinterpret_cast<const Pack<T, VN>*>(src + c * VN);
 #pragma unroll
-        for (int e = 0; e < VN; ++e) dst[row * PITCH + c + e] = to_acc<A, T>(v.v[e]) * w;
+                for (int e = 0; e < VN; ++e) dst[row * PITCH + c * VN + e] = to_acc<A, T>(v.v[e]);
+            }
+        }
     }
 }
 
@@ -85,10 +96,11 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
     using A = typename AccOf<T>::A;
     constexpr int DKP = RPT * 8;
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    A* ks = reinterpret_cast<A*>(smem_raw);
-    A* vs = ks + REC_ROWS * DKP;
-    A* qs = vs + REC_ROWS * REC_COLS;
-    A* os = qs + (READ ? REC_ROWS * DKP : 0);  // outputs, or their cotangents
+    constexpr int STAGE = DKP * (READ ? 2 : 1) + REC_COLS * (READ == 2 ? 2 : 1);  // values of a row in all operands
+    const int cap = P.rows;
+    A* const stages = reinterpret_cast<A*>(smem_raw);
+    A* const os = stages + 2 * cap * STAGE;  // outputs of a block
+    __shared__ A up[REC_MAX + 1], down[REC_MAX + 1];  // e^{-lam j}, e^{lam j}
     const LinRole& R = P.R;
     const int slot = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * REC_COLS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -102,18 +114,30 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
     if (READ == 0 && R.skip_last && (R.reverse ? t0 == P.S.at(seq) : t0 + len == P.S.at(seq + 1))) return;
     const A lam = clamp_lam(static_cast<const A*>(P.lam)[h]);
     const int heads = R.nq > R.nk ? R.nq : R.nk;
-    int nb = REC_ROWS / heads;
+    int nb = cap / heads;
     const A al = lam < 0 ? -lam : lam;
     if (al * nb > (A)4) nb = max(1, (int)((A)4 / al));
+    if (threadIdx.x <= nb) {
+        up[threadIdx.x] = decay(lam, -(A)threadIdx.x);
+        down[threadIdx.x] = decay(lam, (A)threadIdx.x);
+    }
+    for (int i = threadIdx.x; i < 2 * cap * STAGE; i += REC_NT) stages[i] = 0;  // columns past dk, dv stay 0
+    __syncthreads();
+    const bool rev = R.reverse;
+    const auto load = [&](int base, int s) {
+        if (base < len) {
+            const int n = min(nb, len - base);
+            A* ks = stages + s * cap * STAGE;
+            A *vs = ks + cap * DKP, *qs = vs + cap * REC_COLS, *ds = qs + cap * DKP;
+            rec_load<T, A, DKP>(ks, R.k, R.nk, h, t0, len, base, n, rev, R.dk, 0);
+            rec_load<T, A, REC_COLS>(vs, R.v, R.nk, h, t0, len, base, n, rev, R.dv, c0);
+            if constexpr (READ != 0) rec_load<T, A, DKP>(qs, R.q, R.nq, h, t0, len, base, n, rev, R.dk, 0);
+            if constexpr (READ == 2) rec_load<T, A, REC_COLS>(ds, P.dout, R.nq, h, t0, len, base, n, rev, R.dv, c0);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    load(0, 0);
 
-    for (int i = threadIdx.x; i < REC_ROWS * DKP; i += REC_NT) {  // rows past dk stay 0
-        ks[i] = 0;
-        if (READ) qs[i] = 0;
-    }
-    for (int i = threadIdx.x; i < REC_ROWS * REC_COLS; i += REC_NT) {
-        vs[i] = 0;
-        if (READ == 2) os[i] = 0;
-    }
     A S[RPT][4], W[DER ? RPT : 1][4];
 #pragma unroll
     for (int r = 0; r < RPT; ++r)
@@ -128,17 +152,15 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
     if constexpr (DER)
         if (P.w_in) rec_state_io<A, RPT>(W, R, (A*)const_cast<void*>(P.w_in), by_slot, rg, col, false);
     A dsum = 0;
-    const bool rev = R.reverse;
-    for (int base = 0; base < len; base += nb) {
+    int stage = 0;
+    for (int base = 0; base < len; base += nb, stage ^= 1) {
         const int n = min(nb, len - base);
-        __syncthreads();  // the last block's rows have been read
-        rec_load<T, A, DKP>(ks, R.k, R.nk, h, t0, len, base, n, rev, R.dk, 0, lam, (A)R.sk, 1);
-        rec_load<T, A, REC_COLS>(vs, R.v, R.nk, h, t0, len, base, n, rev, R.dv, c0, lam, (A)1, 0);
-        if constexpr (READ != 0) rec_load<T, A, DKP>(qs, R.q, R.nq, h, t0, len, base, n, rev, R.dk, 0, lam, (A)R.sq, -1);
-        if constexpr (READ == 2)
-            rec_load<T, A, REC_COLS>(os, P.dout, R.nq, h, t0, len, base, n, rev, R.dv, c0, lam, (A)1, 0);
+        load(base + nb, stage ^ 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
-        const A pre = decay(lam, (A)(rev ? n - 1 : n));
+        const A* ks = stages + stage * cap * STAGE;
+        const A *vs = ks + cap * DKP, *qs = vs + cap * REC_COLS, *ds = qs + cap * DKP;
+        const A pre = down[rev ? n - 1 : n];
 #pragma unroll
         for (int r = 0; r < RPT; ++r)
 #pragma unroll
@@ -146,7 +168,10 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
                 S[r][c] *= pre;
                 if constexpr (DER) W[r][c] *= pre;
             }
-        for (int tau = 0; tau < n; ++tau) {
+        const int last = c0 + warp * 16 < R.dv ? n : 0;  // (a warp past dv has no column)
+#pragma unroll 2
+        for (int tau = 0; tau < last; ++tau) {
+            const A wk = (A)R.sk * down[n - 1 - tau], wq = (A)R.sq * up[n - 1 - tau];
             if constexpr (DER) {
 #pragma unroll
                 for (int r = 0; r < RPT; ++r)
@@ -156,7 +181,9 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
             for (int g = 0; g < R.nk; ++g) {
                 const A* kr = ks + (tau * R.nk + g) * DKP;
                 const A* vr = vs + (tau * R.nk + g) * REC_COLS + cl;
-                const Pack<A, 4> vv = *reinterpret_cast<const Pack<A, 4>*>(vr);
+                Pack<A, 4> vv = *reinterpret_cast<const Pack<A, 4>*>(vr);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) vv.v[c] *= wk;
 #pragma unroll
                 for (int m = 0; m < RPT / 4; ++m) {
                     const Pack<A, 4> kk = *reinterpret_cast<const Pack<A, 4>*>(kr + m * 32 + rg * 4);
@@ -183,9 +210,11 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
                             }
                     }
                     if constexpr (READ == 2) {
-                        const Pack<A, 4> d = *reinterpret_cast<const Pack<A, 4>*>(os + row * REC_COLS + cl);
+                        const Pack<A, 4> d = *reinterpret_cast<const Pack<A, 4>*>(ds + row * REC_COLS + cl);
+                        A x = 0;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) dsum = dfma(d.v[c], p[c], dsum);
+                        for (int c = 0; c < 4; ++c) x = dfma(d.v[c], p[c], x);
+                        dsum = dfma(wq, x, dsum);
                     } else {
                         // sum over the 8 row groups (lane bits 0-2), halving the columns kept at each step
                         const bool b0 = lane & 1, b1 = lane & 2;
@@ -195,13 +224,13 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
                         A w = b1 ? u1 : u0;
                         w += __shfl_xor_sync(FULL, b1 ? u0 : u1, 2);
                         w += __shfl_xor_sync(FULL, w, 4);
-                        if (rg < 4) os[row * REC_COLS + cl + (b0 ? 2 : 0) + (b1 ? 1 : 0)] = w;
+                        if (rg < 4) os[row * REC_COLS + cl + (b0 ? 2 : 0) + (b1 ? 1 : 0)] = w * wq;
                     }
                 }
             }
         }
         if (rev) {
-            const A post = decay(lam, (A)1);
+            const A post = down[1];
 #pragma unroll
             for (int r = 0; r < RPT; ++r)
 #pragma unroll
@@ -218,6 +247,7 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
                 static_cast<T*>(R.o)[t * R.o_ts + (int64_t)(h * R.nq + g) * R.o_hs + c0 + c] = from_acc<T, A>(os[i]);
             }
         }
+        __syncthreads();  // this stage, and the outputs, have been read
     }
     if (R.state_out)
         rec_state_io<A, RPT>(S, R, (A*)R.state_out, R.out_by_slot ? by_slot : by_seq, rg, col, true);
@@ -338,7 +368,7 @@ __global__ void __launch_bounds__(128) k_carry(const __grid_constant__ LinCarry 
 // ---------------------------------------------------------------- host side
 
 // Tokens per segment.  Enough blocks for two rounds of the resident ones (148
-// SMs x 4); not under 256 tokens, below which the extra pass over k and v and
+// SMs x 4); not under 128 tokens, below which the extra pass over k and v and
 // the states' traffic cost more than they spread.  Sequences of one known length
 // that fill the GPU by themselves are not cut.
 int rec_segment(int64_t T, int N, int H, int dv, bool equal) {
@@ -346,7 +376,7 @@ int rec_segment(int64_t T, int N, int H, int dv, bool equal) {
     const int64_t whole = std::max<int64_t>(T, 1) + 1;
     if (equal && (int64_t)N * H * cb >= 592) return (int)std::min<int64_t>(whole, INT32_MAX);
     int64_t seg = (T * H * cb / 1184 + 63) / 64 * 64;
-    seg = std::max<int64_t>(seg, 256);
+    seg = std::max<int64_t>(seg, 128);
     return (int)std::min<int64_t>(seg >= T ? whole : seg, INT32_MAX);
 }
 
@@ -354,10 +384,12 @@ template <typename T, int RPT, int READ, bool DER>
 static cudaError_t rec_launch(const RecArgs& P, cudaStream_t st) {
     using A = typename AccOf<T>::A;
     constexpr auto kern = k_rec<T, RPT, READ, DER>;
-    constexpr size_t smem = sizeof(A) * REC_ROWS * (RPT * 8 * (READ ? 2 : 1) + REC_COLS * (READ ? 2 : 1));
+    constexpr size_t row = sizeof(A) * (2 * (RPT * 8 * (READ ? 2 : 1) + REC_COLS * (READ == 2 ? 2 : 1)) + (READ == 1 ? REC_COLS : 0));
+    constexpr size_t most = row * REC_MAX;
+    const size_t smem = row * P.rows;
     int dev = 0, sms = 0, per = 0;
     cudaError_t e = current_device_sms(&dev, &sms);
-    if (e == cudaSuccess) e = blocks_per_sm<kern>(dev, REC_NT, smem, &per);
+    if (e == cudaSuccess) e = blocks_per_sm<kern>(dev, REC_NT, most, &per);  // (raises the limit)
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)P.S.slots, (unsigned)P.H, (unsigned)((P.R.dv + REC_COLS - 1) / REC_COLS));
     if (grid.x == 0) return cudaSuccess;
@@ -366,8 +398,11 @@ static cudaError_t rec_launch(const RecArgs& P, cudaStream_t st) {
 }
 
 template <typename T, int READ, bool DER>
-static cudaError_t rec_dim(const RecArgs& P, cudaStream_t st) {
-    return P.R.dk <= 64 ? rec_launch<T, 8, READ, DER>(P, st) : rec_launch<T, 16, READ, DER>(P, st);
+static cudaError_t rec_dim(RecArgs P, cudaStream_t st) {
+    P.rows = std::max(P.R.nq, P.R.nk) > 16 ? 32 : 16;
+    return P.R.dk <= 64   ? rec_launch<T, 8, READ, DER>(P, st)
+           : P.R.dk <= 96 ? rec_launch<T, 12, READ, DER>(P, st)
+                          : rec_launch<T, 16, READ, DER>(P, st);
 }
 
 template <typename F>

@@ -1103,7 +1103,7 @@ int tc_segment(int64_t T, int N, int H, int roles, bool equal) {
         }
         return (int)seg;
     }
-    seg = std::max<int64_t>(512, up(T * H * roles / ((roles > 1 ? 4 : 3) * SMS)));
+    seg = std::max<int64_t>(T * H * roles <= SMS * 256 ? 256 : 512, up(T * H * roles / ((roles > 1 ? 4 : 3) * SMS)));
     return (int)(seg >= T ? whole : seg);
 }
 

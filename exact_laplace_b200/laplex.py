@@ -485,36 +485,49 @@ class LinattnGrads(NamedTuple):
     dlog_decay: Optional[torch.Tensor]
 
 
+_HERE_CTX = contextlib.nullcontext()
+
+
 def _on(dev):
     """The device of the tensors made current: the library works on the current one."""
-    return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _HERE_CTX if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _raw_stream(dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _seq_dt(*ts) -> int:
+    first = ts[0].dtype
     for t in ts:
-        if t is not None and t.dtype != ts[0].dtype:
-            raise LaplexError(EINVAL, f"rows of {ts[0].dtype} and of {t.dtype}")
-    if ts[0].dtype not in _SEQ_DTYPES:
-        raise LaplexError(EINVAL, f"dtype {ts[0].dtype} is not float16, bfloat16, float32 or float64")
-    return _SEQ_DTYPES[ts[0].dtype]
+        if t is not None and t.dtype != first:
+            raise LaplexError(EINVAL, f"rows of {first} and of {t.dtype}")
+    dt = _SEQ_DTYPES.get(first)
+    if dt is None:
+        raise LaplexError(EINVAL, f"dtype {first} is not float16, bfloat16, float32 or float64")
+    return dt
 
 
 def _seq_dev(*ts):
-    dev = None
+    """The tensors' common CUDA device."""
+    at = None
     for t in ts:
         if t is None:
             continue
-        if not t.is_cuda:
+        d = t.get_device()  # -1: not CUDA
+        if d < 0:
             raise LaplexError(EINVAL, "tensors must be on a CUDA device")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
+        if at is None:
+            at = d
+        elif d != at:
             raise LaplexError(EINVAL, "tensors are on different devices")
-    return dev
+    return ts[0].device
 
 
 def _packed(name, x):
     """[tokens, heads, dim] of x, which may also be [seqs, length, heads, dim]."""
+    if x.dim() == 3 and x.stride(2) == 1:
+        return x
     if x.dim() == 4:
         n, m = x.shape[:2]
         if n > 1 and m > 1 and x.stride(0) != m * x.stride(1):
@@ -529,7 +542,14 @@ def _packed(name, x):
 
 
 def _rows(x):
-    return None if x is None else ctypes.byref(_Rows(x.data_ptr(), x.stride(0), x.stride(1)))
+    if x is None:
+        return None
+    st = x.stride()
+    return ctypes.byref(_Rows(x.data_ptr(), st[0], st[1]))
+
+
+def _addr(x):
+    return None if x is None else x.data_ptr()
 
 
 def _like(x):
@@ -565,22 +585,34 @@ def _seqs(q, cu):
     return cu.numel() - 1
 
 
-def _seq_ws(dev, nbytes):
-    """Workspace of a sequence operator: the stream's, or while a graph is captured
-    one of the graph's own memory (the stream's may be replaced by a larger one
-    while the graph lives, and two graphs may run at the same time)."""
+def _seq_ws(dev, raw, nbytes):
+    """Workspace of a sequence operator on stream `raw`: the stream's, or while a
+    graph is captured one of the graph's own memory (the stream's may be replaced
+    by a larger one while the graph lives, and two graphs may run at the same time)."""
     if not torch.cuda.is_current_stream_capturing():
-        buf = Workspace.get(dev, nbytes)
+        buf = Workspace._cache.get((dev, raw))
+        if buf is None or buf.numel() < nbytes:
+            buf = Workspace.get(dev, nbytes)
     else:
         buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _check(lib().laplex_workspace_init(_ptr(buf), nbytes, _stream(dev)))
-    return buf, buf.numel()
+        _check(lib().laplex_workspace_init(buf.data_ptr(), nbytes, raw))
+    return buf
 
 
-def _linattn_ws(s, call, dev):
-    out = ctypes.c_size_t(0)
-    _check(lib().laplex_linattn_workspace_size(ctypes.byref(s), call, ctypes.byref(out)))
-    return _seq_ws(dev, out.value)
+_ws_sizes: dict = {}  # workspace bytes by shape
+
+
+def _linattn_ws(s, call, dev, raw):
+    key = (s.tokens, s.seqs, s.cu_seqlens is None, s.hq, s.hkv, s.dk, s.dv, s.dtype, call)
+    nbytes = _ws_sizes.get(key)
+    if nbytes is None:
+        out = ctypes.c_size_t(0)
+        _check(lib().laplex_linattn_workspace_size(ctypes.byref(s), call, ctypes.byref(out)))
+        nbytes = out.value
+        if len(_ws_sizes) >= 4096:
+            _ws_sizes.clear()
+        _ws_sizes[key] = nbytes
+    return _seq_ws(dev, raw, nbytes)
 
 
 def linattn(q, k, v, log_decay, scale=None, cu_seqlens=None, state=None, return_state=False, out=None,
@@ -611,9 +643,10 @@ def linattn(q, k, v, log_decay, scale=None, cu_seqlens=None, state=None, return_
             raise LaplexError(EINVAL, f"out must have the shape {tuple(q.shape[:-1]) + (s.dv,)}")
         if return_state and state_out is None:
             state_out = torch.empty(shape, dtype=acc, device=dev)
-        ws, nb = _linattn_ws(s, LINATTN_FORWARD, dev)
-        _check(lib().laplex_linattn(ctypes.byref(s), _rows(q3), _rows(k3), _rows(v3), _ptr(state),
-                                    _rows(_packed("out", out)), _ptr(state_out), _ptr(ws), nb, _stream(dev)))
+        raw = _raw_stream(dev)
+        ws = _linattn_ws(s, LINATTN_FORWARD, dev, raw)
+        _check(lib().laplex_linattn(ctypes.byref(s), _rows(q3), _rows(k3), _rows(v3), _addr(state),
+                                    _rows(_packed("out", out)), _addr(state_out), ws.data_ptr(), ws.numel(), raw))
     return out if state_out is None else (out, state_out)
 
 
@@ -645,11 +678,12 @@ def linattn_backward(q, k, v, log_decay, dout, scale=None, cu_seqlens=None, stat
         if return_dstate or (return_dstate is None and state is not None):
             ds = torch.empty(shape, dtype=acc, device=dev)
         dl = torch.empty(s.hkv, dtype=acc, device=dev) if return_dlog_decay else None
-        ws, nb = _linattn_ws(s, LINATTN_BACKWARD_DECAY if return_dlog_decay else LINATTN_BACKWARD, dev)
+        raw = _raw_stream(dev)
+        ws = _linattn_ws(s, LINATTN_BACKWARD_DECAY if return_dlog_decay else LINATTN_BACKWARD, dev, raw)
         _check(lib().laplex_linattn_backward(
-            ctypes.byref(s), _rows(q3), _rows(k3), _rows(v3), _rows(do3), _ptr(state), _ptr(dstate),
-            _rows(_packed("dq", dq)), _rows(_packed("dk", dk)), _rows(_packed("dv", dv)), _ptr(ds), _ptr(dl),
-            _ptr(ws), nb, _stream(dev)))
+            ctypes.byref(s), _rows(q3), _rows(k3), _rows(v3), _rows(do3), _addr(state), _addr(dstate),
+            _rows(_packed("dq", dq)), _rows(_packed("dk", dk)), _rows(_packed("dv", dv)), _addr(ds), _addr(dl),
+            ws.data_ptr(), ws.numel(), raw))
     return LinattnGrads(dq, dk, dv, ds, dl)
 
 
@@ -676,8 +710,8 @@ def linattn_step(q, k, v, log_decay, states, slots=None, scale=None, out=None):
             out = torch.empty((s.tokens, s.hq, s.dv), dtype=q.dtype, device=dev)
         elif tuple(out.shape) != (s.tokens, s.hq, s.dv):
             raise LaplexError(EINVAL, f"out must have the shape {(s.tokens, s.hq, s.dv)}")
-        _check(lib().laplex_linattn_step(ctypes.byref(s), _rows(q3), _rows(k3), _rows(v3), _ptr(states),
-                                         states.shape[0], _ptr(slots), _rows(_packed("out", out)), _stream(dev)))
+        _check(lib().laplex_linattn_step(ctypes.byref(s), _rows(q3), _rows(k3), _rows(v3), states.data_ptr(),
+                                         states.shape[0], _addr(slots), _rows(_packed("out", out)), _raw_stream(dev)))
     return out
 
 
@@ -706,8 +740,8 @@ def embed(table, tokens, scale=1.0, out=None):
         elif tuple(out.shape) != shape or (out.dim() != 2 and not out.is_contiguous()):
             raise LaplexError(EINVAL, f"out must have the shape {shape}")
         o2 = out if out.dim() == 2 else out.view(-1, table.shape[1])
-        _check(lib().laplex_embed(_ptr(table), ld, table.shape[0], table.shape[1], _ptr(tokens), tb, tokens.numel(),
-                                  float(scale), _ptr(o2), _table("out", o2), dt, _stream(dev)))
+        _check(lib().laplex_embed(table.data_ptr(), ld, table.shape[0], table.shape[1], tokens.data_ptr(), tb,
+                                  tokens.numel(), float(scale), o2.data_ptr(), _table("out", o2), dt, _raw_stream(dev)))
     return out
 
 
@@ -734,12 +768,17 @@ def embed_backward(tokens, g, rows, scale=1.0, out=None, accumulate=False, dtype
             out = torch.empty((rows, dim), dtype=dtype or g.dtype, device=dev)
         if out.shape[0] != rows or out.dtype not in (g.dtype, torch.float32):
             raise LaplexError(EINVAL, f"out must have {rows} rows of {g.dtype} or float32")
-        size = ctypes.c_size_t(0)
-        _check(lib().laplex_embed_backward_workspace_size(tokens.numel(), rows, dim, dt, ctypes.byref(size)))
-        ws, nb = _seq_ws(dev, size.value)
-        _check(lib().laplex_embed_backward(_ptr(tokens), tb, tokens.numel(), _ptr(g), ld, rows, dim, float(scale),
-                                           int(bool(accumulate)), _ptr(out), _table("out", out, dim), dt,
-                                           _SEQ_DTYPES[out.dtype], _ptr(ws), nb, _stream(dev)))
+        key = (tokens.numel(), rows, dim, dt)
+        nbytes = _ws_sizes.get(key)
+        if nbytes is None:
+            size = ctypes.c_size_t(0)
+            _check(lib().laplex_embed_backward_workspace_size(*key, ctypes.byref(size)))
+            nbytes = _ws_sizes[key] = size.value
+        raw = _raw_stream(dev)
+        ws = _seq_ws(dev, raw, nbytes)
+        _check(lib().laplex_embed_backward(tokens.data_ptr(), tb, tokens.numel(), g.data_ptr(), ld, rows, dim,
+                                           float(scale), int(bool(accumulate)), out.data_ptr(), _table("out", out, dim),
+                                           dt, _SEQ_DTYPES[out.dtype], ws.data_ptr(), ws.numel(), raw))
     return out
 
 

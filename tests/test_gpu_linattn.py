@@ -253,8 +253,12 @@ def test_equal_lengths_four_dimensions_and_head_major_rows(dt):
     c = Case(dt, [150] * 3, 4, 2, 64, 64)
     want, _ = c.run_forward()
     four = [x.contiguous().view(3, 150, *x.shape[1:]) for x in (c.q, c.k, c.v)]
-    o, _ = X.linattn(*four, c.lam, scale=c.scale, state=c.s0, return_state=True)
-    assert o.shape == (3, 150, 4, 64) and torch.equal(o.view_as(want), want)
+    o, end = X.linattn(*four, c.lam, scale=c.scale, state=c.s0, return_state=True)
+    assert o.shape == (3, 150, 4, 64)
+    # (known and unknown lengths may be cut differently, and so round differently: the same bounds, not the same bits)
+    c.check_forward(o.view_as(want), end)
+    again, _ = X.linattn(*four, c.lam, scale=c.scale, state=c.s0, return_state=True)
+    assert torch.equal(again, o)
     major = [x.transpose(0, 1).contiguous().transpose(0, 1) for x in (c.q, c.k, c.v)]
     o, _ = X.linattn(*major, c.lam, scale=c.scale, cu_seqlens=c.cu, state=c.s0, return_state=True)
     assert torch.equal(o, want)
@@ -296,11 +300,11 @@ def test_gradients_that_are_not_asked_for(dt):
     r, n = c.backward_ref()
     for keep in ("dq", "dk", "dv", "dstate"):
         new = {n: torch.empty_like(getattr(g, n)) if n == keep else None for n in ("dq", "dk", "dv", "dstate")}
-        ws, nb = X._linattn_ws(s, X.LINATTN_BACKWARD, c.q.device)
+        ws = X._linattn_ws(s, X.LINATTN_BACKWARD, c.q.device, X._raw_stream(c.q.device))
         X._check(X.lib().laplex_linattn_backward(
             ctypes.byref(s), X._rows(c.q), X._rows(c.k), X._rows(c.v), X._rows(c.do), X._ptr(c.s0), X._ptr(c.ds),
-            X._rows(new["dq"]), X._rows(new["dk"]), X._rows(new["dv"]), X._ptr(new["dstate"]), None, X._ptr(ws), nb,
-            X._stream(c.q.device)))
+            X._rows(new["dq"]), X._rows(new["dk"]), X._rows(new["dv"]), X._ptr(new["dstate"]), None, X._ptr(ws),
+            ws.numel(), X._stream(c.q.device)))
         check(new[keep], r[keep], n[keep], tol_acc(dt) if keep == "dstate" else tol_rows(dt), keep)
         if dt == "fp32":
             assert torch.equal(new[keep], getattr(g, keep)), keep
