@@ -245,7 +245,12 @@ laplex_status laplex_linattn(const laplex_linattn_shape* shape, const laplex_row
         R.in_by_slot = 1;
         R.state_out = nullptr;
     }
-    if (e == cudaSuccess) e = run(s, &R, 1, S, false, status, st);
+    // (tensor cores: a state that leaves the call comes from the state pass)
+    const bool apart = tensor_cores(s) && R.state_out;
+    lx::LinRole P = R;
+    if (apart) P.state_out = nullptr;
+    if (e == cudaSuccess) e = run(s, &P, 1, S, false, status, st);
+    if (e == cudaSuccess && apart) e = run(s, &R, 1, S, true, status, st);
     return done(e, "laplex_linattn");
 }
 
@@ -318,13 +323,17 @@ laplex_status laplex_linattn_backward(const laplex_linattn_shape* shape, const l
         out(&Rk, rdk);
         roles[count++] = Rk;
     }
-    if (!cut) Rv.state_out = dstate_in;
+    const bool apart = dstate_in && !cut && (tensor_cores(s) || !dv);
+    if (!cut && !apart) Rv.state_out = dstate_in;
     if (dv) {
         out(&Rv, rdv);
         roles[count++] = Rv;
     }
     e = run(s, roles, count, S, false, status, st);
-    if (e == cudaSuccess && !dv && dstate_in && !cut) e = run(s, &Rv, 1, S, true, status, st);
+    if (e == cudaSuccess && apart) {
+        Rv.state_out = dstate_in;
+        e = run(s, &Rv, 1, S, true, status, st);
+    }
     return done(e, "laplex_linattn_backward");
 }
 

@@ -21,15 +21,20 @@
 //                      rows' type, to shared memory (for O2 alone) and scales it
 //                      by the next chunk's e^{lam n}, on which the next U adds.
 //                      K is weighed as a sum of two 16-bit values (hi in place,
-//                      lo beside it), so that U carries 2^-17, not 2^-9; where
-//                      the state leaves the call, from fp32 products, and in
-//                      three parts for bf16;
+//                      lo beside it), so that U carries 2^-17, not 2^-9;
 //   rows (8 warps):    P's weights, rounded once to the rows' type and put back
 //                      into tensor memory as the A operand of O1, and the outputs.
 // One group of 8 warps that did all of this in turn took 8.9 us a chunk of
 // dk = dv = 128 (issue slots 21 % busy, the rest latencies of the chain).  The
 // tiles leave hardly any L1: a spilled register is a trip to L2, so nothing is
 // kept in registers from chunk to chunk, and the loops over columns are not unrolled.
+//
+// States that leave the call, and those at the starts of segments, come from a
+// second kernel, the state pass: U alone, over chunks of 64 tokens, each chunk's
+// added to the state in fp32 registers.  (Sums in tensor memory are cut off, not
+// rounded, at each product: 3e-8 of the sum each, always downwards, 1e-5 over the
+// 300 products that a slow decay remembers.)  There K's weights come from fp32
+// products, for bf16 in three parts, where the state is a result.
 //
 // fp16: weights, states and weighted K are scaled by powers of two (per row, per
 // state, per chunk) to 2^14..2^15 before they are rounded, so that nothing
@@ -61,7 +66,7 @@ constexpr int TC_C = 128;  // tokens per chunk
 struct TcRole {
     int mq, mk, mv;  // maps of the operands
     int nq, nk, dk, dv, reverse, transposed, in_by_slot, out_by_slot, skip_last;
-    int exact;       // the state that leaves is a result, not only rounded for O2
+    int exact;       // state pass: the state is a result, not only rounded for O2
     float sq, sk;
     const void* q;   // rows of q, k and v (for repair)
     int64_t q_ts, q_hs;
@@ -97,34 +102,33 @@ struct TcShared {
     uint32_t dead;       // a wait ran out
     alignas(16) float grow[16];  // e^{lam j}, 16 columns of P towards the row's end
     float wt[TC_C + 32]; // P's weights scale e^{lam |x|} at 32 + x (reversed: 127 + x), x = row - column; 0 up to 31 past the diagonal
-    // K's weights g1 e^{lam d}, d >= 0, as sums of 16-bit values, each twice
-    uint2 dec2[TC_C];
-    union {
-        uint32_t dec3[TC_C];  // bf16, products: the third
-        float dec[TC_C];      // fp16, and the state pass: in fp32
+    union {                // K's weights g1 e^{lam d}, d >= 0
+        float dec[TC_C];   // in fp32 (exact)
+        uint2 dec2[TC_C];  // as sums of two 16-bit values, each twice
     };
     float s_inv[2];      // fp16: what the rounded state is to be multiplied by, by chunk
     uint8_t rexp[2][TC_C];  // fp16: the exponent of a row's largest weight, by half
     float red[2][8];     // fp16: maxima of the state warps
 };
 
-// CH tokens at a time.  The state pass of bf16 takes 64, with two blocks on an SM: it only streams
-// K and V, and one block with two stages of 128 left the copies' latency (about 3500 cycles under
-// load) in the open.
-template <int DK, int DV, bool OUT, bool BF> struct TcSize {
-    static constexpr int CH = OUT || !BF ? 128 : 64, STAGES = 2, BLOCKS = CH == 64 ? 2 : 1;
+// Products: chunks of 128 tokens.  The state pass takes 64, with two blocks on an SM: it only
+// streams K and V, and one block with two stages of 128 left the copies' latency (about 3500
+// cycles under load) in the open.
+template <int DK, int DV, bool OUT> struct TcSize {
+    static constexpr int CH = OUT ? 128 : 64, STAGES = 2, BLOCKS = OUT ? 1 : 2;
     static constexpr uint32_t TB = CH * 128;  // bytes of a tile of 64 columns
     static constexpr uint32_t KBY = DK / 64 * TB, VBY = DV / 64 * TB;
-    // K's lower parts.  Products: the second in LO, the third (bf16) in the place of the rounded
-    // state between O2 and the next state.  State pass of bf16: the third, or a second buffer of the second.
-    static constexpr uint32_t SBY = OUT && DK * 128 * (DV / 64) > KBY ? DK * 128 * (DV / 64) : OUT || BF ? KBY : 0;
+    // LO: K's second part.  S: the rounded state; in the state pass K's third part, or a second buffer
+    // of the second.
+    static constexpr uint32_t SBY = OUT ? DK * 128 * (DV / 64) : KBY;
     static constexpr uint32_t K = 0, V = STAGES * KBY, LO = V + STAGES * VBY, S = LO + KBY, Q = S + SBY;
     static constexpr uint32_t TILES = Q + (OUT ? KBY : 0);
     static constexpr uint32_t BYTES = TILES + sizeof(TcShared);
     // tensor memory columns: P, O1, O2, U.  The rounded weights of P's columns 0-63
     // take columns 0-31, those of 64-127 columns 64-95: each warp writes over what it alone read.
+    // The state pass: U and, behind it, the state.
     static constexpr uint32_t P = 0, O1 = 128, O2 = 256, U = OUT ? 384 : 0;
-    static constexpr uint32_t COLS = OUT ? 512 : DV;
+    static constexpr uint32_t COLS = OUT ? 512 : 2 * DV;
     // the issuing warp brings three idle ones: registers are moved between groups of four warps
     static constexpr int NT = OUT ? 2 * TC_GROUP + 128 : TC_GROUP + 32;
 };
@@ -234,7 +238,7 @@ template <int ID> __device__ __forceinline__ void group_sync() {
 template <typename T, int DK, int DV, bool OUT>
 struct TcBlock {
     static constexpr bool BF = std::is_same<T, __nv_bfloat16>::value;
-    using Z = TcSize<DK, DV, OUT, BF>;
+    using Z = TcSize<DK, DV, OUT>;
     static constexpr int CH = Z::CH, NS = Z::STAGES;
     static constexpr uint32_t TB = Z::TB;
     static constexpr int HV = DV / 2;  // columns of a thread of the state and of the outputs
@@ -246,7 +250,7 @@ struct TcBlock {
     uint32_t smb, tm;
     int slot, h, seq, len, nch, nq, nk, G;
     int64_t t0;
-    bool rev, exact;  // exact: K's weights from fp32, in three parts for bf16
+    bool rev, exact;  // exact (state pass): K's weights from fp32, in three parts for bf16
     float l2, g1, up1;  // K's largest weight (e^lam sk reversed, sk forward), times up1, a power of two (fp16)
 
     __device__ __forceinline__ int64_t chunk_at(int c, int* n) const {
@@ -304,7 +308,7 @@ struct TcBlock {
     }
     // where the second (1) and third (2) part of K go for the us-th U
     __device__ __forceinline__ uint32_t part(int x, int us) const {
-        if (OUT || !BF || exact) return x == 1 ? Z::LO : Z::S;
+        if (OUT || (BF && exact)) return x == 1 ? Z::LO : Z::S;
         return us & 1 ? Z::S : Z::LO;
     }
     __device__ __forceinline__ void commit(uint64_t* bar) const {
@@ -337,7 +341,7 @@ struct TcBlock {
                             mma_ss(tm + Z::P, dq + off, dk + off, id, s > 0);
                         }
                         mma_commit(&sh.p_done);
-                        if (conv && !(BF && exact)) mma_commit(&sh.k_free);
+                        if (conv) mma_commit(&sh.k_free);
                     }
                     __syncwarp();
                 }
@@ -364,8 +368,7 @@ struct TcBlock {
                         }
                         commit(&sh.o2_done);
                     }
-                    if (conv && BF && exact) commit(&sh.k_free);  // K's third part takes the state's place
-                    if (emit && new_q) {                          // P and O2 have read Q
+                    if (emit && new_q) {  // P and O2 have read Q
                         if (!wait(&sh.o2_done, qi)) return;
                         load_q(qi + 1);
                     }
@@ -391,17 +394,20 @@ struct TcBlock {
                     constexpr uint32_t id = mma_desc(BF, true, true, 128, DV), lead = DK == 64 ? 0 : TB;
                     const uint64_t dv = tile_desc(Va, TB, 1024), d0 = tile_desc(Ka, lead, 1024),
                                    d1 = tile_desc(smb + part(1, us), lead, 1024), d2 = tile_desc(smb + part(2, us), lead, 1024);
-                    const bool add = us > 0 || R.state_in;
+                    // products: onto the scaled state.  State pass: each chunk's by itself, small parts first
+                    const bool add = OUT && (us > 0 || R.state_in);
+                    const uint32_t U = tm + Z::U;
                     if (elect()) {
+                        if (!OUT && BF && exact) {
+#pragma unroll
+                            for (int s = 0; s < CH / 16; ++s) mma_ss(U, d2 + s * (2048 >> 4), dv + s * (2048 >> 4), id, s > 0);
+                        }
+                        const bool third = !OUT && BF && exact;
 #pragma unroll
                         for (int s = 0; s < CH / 16; ++s)
-                            mma_ss(tm + Z::U, d0 + s * (2048 >> 4), dv + s * (2048 >> 4), id, add || s > 0);
+                            mma_ss(U, d1 + s * (2048 >> 4), dv + s * (2048 >> 4), id, add || third || s > 0);
 #pragma unroll
-                        for (int s = 0; s < CH / 16; ++s) mma_ss(tm + Z::U, d1 + s * (2048 >> 4), dv + s * (2048 >> 4), id, true);
-                        if (BF && exact) {
-#pragma unroll
-                            for (int s = 0; s < CH / 16; ++s) mma_ss(tm + Z::U, d2 + s * (2048 >> 4), dv + s * (2048 >> 4), id, true);
-                        }
+                        for (int s = 0; s < CH / 16; ++s) mma_ss(U, d0 + s * (2048 >> 4), dv + s * (2048 >> 4), id, true);
                         mma_commit(&sh.u_done[us & 1]);
                     }
                     __syncwarp();
@@ -446,8 +452,8 @@ struct TcBlock {
     }
 
     // K of load kv, times g1 e^{lam d} (and k_up, fp16), as a sum of 16-bit parts
-    // The state pass of bf16: times `far` as well (us: the number of this U).
-    __device__ __forceinline__ void weigh(int kv, int n, float k_up, int tid, float far, int us) const {
+    // (us: the number of the U that takes it)
+    __device__ __forceinline__ void weigh(int kv, int n, float k_up, int tid, int us) const {
         const uint32_t at0 = tile_at(tid >> 3, tid & 7);
         unsigned char* Ks = sm + Z::K + (kv % NS) * Z::KBY + at0;
         unsigned char* Ls = sm + part(1, us) + at0;
@@ -461,43 +467,32 @@ struct TcBlock {
             const int d = (d0 + (x % (CH / 32)) * dd) & 127;
             const uint32_t q[4] = {w.x, w.y, w.z, w.w};
             uint32_t a0[4], a1[4], a2[4];
-            if (!BF && exact) {
-                // from fp32 products: weights below fp16's smallest still count
+            if (!OUT && exact) {
+                // from fp32 products, what one part rounds off goes to the next: 2^-24 after three of bf16
+                // (and weights below fp16's smallest still count)
                 const float f = sh.dec[d] * k_up;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     float2 v = unpack2<T>(q[e]);
                     v = make_float2(v.x * f, v.y * f);
                     a0[e] = pack2<T>(v.x, v.y);
-                    const float2 g = unpack2<T>(a0[e]);
-                    a1[e] = pack2<T>(v.x - g.x, v.y - g.y);
+                    float2 g = unpack2<T>(a0[e]);
+                    v = make_float2(v.x - g.x, v.y - g.y);
+                    a1[e] = pack2<T>(v.x, v.y);
+                    if constexpr (BF) {
+                        g = unpack2<T>(a1[e]);
+                        a2[e] = pack2<T>(v.x - g.x, v.y - g.y);
+                    }
                 }
             } else {
-                // k (f1 + f2 (+ f3)): the first part rn(k f1); k f1 less it is exact, and with k f2 gives
-                // the second; what that rounds off, with k f3, the third
-                uint2 f;
-                uint32_t f3 = 0;
-                if (BF && !OUT) {
-                    float y = sh.dec[d] * far;
-                    f.x = pack2<T>(y, y);
-                    y -= unpack2<T>(f.x).x;
-                    f.y = pack2<T>(y, y);
-                    if (exact) {
-                        y -= unpack2<T>(f.y).x;
-                        f3 = pack2<T>(y, y);
-                    }
-                } else {
-                    f = sh.dec2[d];
-                    if (BF && exact) f3 = sh.dec3[d];
-                }
+                // k (f1 + f2): the first part rn(k f1); k f1 less it is exact, and with k f2 gives the second
+                const uint2 f = sh.dec2[d];
                 const uint32_t up = BF ? 0u : pack2<T>(k_up, k_up);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t k = BF ? q[e] : H::mul(q[e], up);  // (exact)
                     a0[e] = H::mul(k, f.x);
-                    const uint32_t left = H::fms(k, f.x, a0[e]);
-                    a1[e] = H::fma(k, f.y, left);
-                    if (BF && exact) a2[e] = H::fma(k, f3, H::fma(k, f.y, H::sub(left, a1[e])));
+                    a1[e] = H::fma(k, f.y, H::fms(k, f.x, a0[e]));
                 }
             }
             if (n < CH && r0 + 32 * (x % (CH / 32)) >= n) {  // not 0 * NaN
@@ -506,14 +501,14 @@ struct TcBlock {
             }
             *reinterpret_cast<uint4*>(Ks + at) = make_uint4(a0[0], a0[1], a0[2], a0[3]);
             *reinterpret_cast<uint4*>(Ls + at) = make_uint4(a1[0], a1[1], a1[2], a1[3]);
-            if (BF && exact) *reinterpret_cast<uint4*>(Ms + at) = make_uint4(a2[0], a2[1], a2[2], a2[3]);
+            if (!OUT && BF && exact) *reinterpret_cast<uint4*>(Ms + at) = make_uint4(a2[0], a2[1], a2[2], a2[3]);
         }
         fence_proxy_async();
     }
 
     // The state, in tensor memory in units of 1 / up: rounded into shared memory as the B operand of O2 (which: its number);
     // scaled for the next U; or out into memory.
-    __device__ __forceinline__ void pass(int tid, float up, bool round, int which, bool scale, float factor, float* out) const {
+    __device__ __forceinline__ void pass(int tid, float up, bool round, int which, bool scale, float factor) const {
         const int warp = tid >> 5, lane = tid & 31, wg = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t St = tm + ((uint32_t)((warp & 3) * 32) << 16) + Z::U + wg * HV;
         float s_up = 1.0f / up;
@@ -571,31 +566,6 @@ struct TcBlock {
                 __syncwarp();
                 tmem_st32(St + cb, r);
             }
-            if (out && row < R.dk) {
-                const float inv = 1.0f / up;
-                const int64_t ri = R.transposed ? 1 : R.dv, ci = R.transposed ? R.dk : 1;
-                if (ci == 1) {
-                    const bool whole = (reinterpret_cast<uintptr_t>(out + row * ri) & 31) == 0;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * inv);
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        float* p = out + row * ri + wg * HV + cb + j;
-                        if (wg * HV + cb + j >= R.dv) break;
-                        if (whole) st32(p, r + j, r + j + 4);
-                        else {
-                            *reinterpret_cast<uint4*>(p) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
-                            *reinterpret_cast<uint4*>(p + 4) = make_uint4(r[j + 4], r[j + 5], r[j + 6], r[j + 7]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int col = wg * HV + cb + j;
-                        if (col < R.dv) out[row * ri + col * ci] = __uint_as_float(r[j]) * inv;
-                    }
-                }
-            }
         }
         if (round) {
             fence_proxy_async();
@@ -617,102 +587,154 @@ struct TcBlock {
         return fminf(scale_to_fp16(m), 32768.0f);
     }
 
+    // 32 columns from `col` of a state's row in memory (in: where the row starts, or NULL for zeros)
+    __device__ __forceinline__ void read_row(const float* in, int64_t ci, bool has, int col, uint32_t (&r)[32]) const {
+        if (ci == 1) {  // (a row is dv values, a multiple of 8)
+            const bool whole = (reinterpret_cast<uintptr_t>(in) & 31) == 0;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) r[j + e] = 0;
+                if (has && col + j < R.dv) {
+                    if (whole) ld32(in + col + j, r + j);
+                    else {
+                        const uint4 x = *reinterpret_cast<const uint4*>(in + col + j), y = *reinterpret_cast<const uint4*>(in + col + j + 4);
+                        r[j] = x.x, r[j + 1] = x.y, r[j + 2] = x.z, r[j + 3] = x.w;
+                        r[j + 4] = y.x, r[j + 5] = y.y, r[j + 6] = y.z, r[j + 7] = y.w;
+                    }
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = has && col + j < R.dv ? __float_as_uint(in[(col + j) * ci]) : 0u;
+        }
+    }
+    __device__ __forceinline__ void write_row(float* out, int64_t ci, int col, const uint32_t (&r)[32]) const {
+        if (ci == 1) {
+            const bool whole = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+                float* p = out + col + j;
+                if (col + j >= R.dv) break;
+                if (whole) st32(p, r + j, r + j + 4);
+                else {
+                    *reinterpret_cast<uint4*>(p) = make_uint4(r[j], r[j + 1], r[j + 2], r[j + 3]);
+                    *reinterpret_cast<uint4*>(p + 4) = make_uint4(r[j + 4], r[j + 5], r[j + 6], r[j + 7]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (col + j < R.dv) out[(col + j) * ci] = __uint_as_float(r[j]);
+        }
+    }
+
+    // The state pass: thread = row `row` of dk, columns wg * HV .. of the state, which lies in tensor
+    // memory but is summed in registers.  A chunk is weighed while the one before is multiplied.
+    __device__ __forceinline__ void sum_states(int tid) const {
+        const int warp = tid >> 5, lane = tid & 31, wg = warp >> 2, row = (warp & 3) * 32 + lane;
+        const int64_t at = ((R.out_by_slot ? (int64_t)slot : (int64_t)seq) * A.H + h) * R.dk * R.dv;
+        const int64_t from = ((R.in_by_slot ? (int64_t)slot : (int64_t)seq) * A.H + h) * R.dk * R.dv;
+        const int64_t ri = R.transposed ? 1 : R.dv, ci = R.transposed ? R.dk : 1;
+        const uint32_t Ut = tm + ((uint32_t)((warp & 3) * 32) << 16) + Z::U + wg * HV, St = Ut + DV;
+        const float whole = exp2f(l2 * (float)len);
+#pragma unroll 1
+        for (int b = 0; b < HV; b += 32) {
+            uint32_t r[32];
+            read_row(R.state_in ? R.state_in + from + row * ri : nullptr, ci, R.state_in && row < R.dk, wg * HV + b, r);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(__uint_as_float(r[j]) * whole);
+            __syncwarp();
+            tmem_st32(St + b, r);
+        }
+        tmem_wait_st();
+        float unit = 0.0f;  // of the last chunk's U
+        const auto add = [&](int us) -> bool {
+            if (!wait(&sh.u_done[us & 1], us >> 1)) return false;
+            tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < HV; b += 16) {
+                uint32_t r[16], s[16];
+                __syncwarp();
+                tmem_ld16(Ut + b, r);
+                tmem_ld16(St + b, s);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 16; ++j) s[j] = __float_as_uint(fmaf(unit, __uint_as_float(r[j]), __uint_as_float(s[j])));
+                __syncwarp();
+                tmem_st16(St + b, s);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            return true;
+        };
+        const int n_kv = nch * nk;
+        for (int kv = 0; kv < n_kv; ++kv) {
+            int n;
+            const int64_t a = chunk_at(kv / nk, &n);
+            if (!wait(&sh.kv_full[kv % NS], kv / NS)) return;
+            const float k_up = k_scale(scan(kv, n, tid), tid);
+            const bool alone = BF && exact;  // the parts have one buffer
+            if (alone && kv > 0 && !add(kv - 1)) return;
+            weigh(kv, n, k_up, tid, kv);
+            if (!alone && kv > 0 && !add(kv - 1)) return;
+            arrive(&sh.k_ready[kv & 1]);
+            unit = exp2f(l2 * (float)(rev ? a - t0 : t0 + len - a - n)) / (k_up * up1);
+        }
+        if (n_kv > 0 && !add(n_kv - 1)) return;
+#pragma unroll 1
+        for (int b = 0; b < HV; b += 32) {
+            uint32_t r[32];
+            __syncwarp();
+            tmem_ld32(St + b, r);
+            tmem_wait_ld();
+            if (row < R.dk) write_row(R.state_out + at + row * ri, ci, wg * HV + b, r);
+        }
+    }
+
+    // The state warps of the products.
     __device__ __forceinline__ void states(int tid) const {
         const int warp = tid >> 5, lane = tid & 31, wg = warp >> 2, row = (warp & 3) * 32 + lane;
-        const int64_t by_slot = (int64_t)slot * A.H + h, by_seq = (int64_t)seq * A.H + h;
-        const int64_t ri = R.transposed ? 1 : R.dv, ci = R.transposed ? R.dk : 1;
-        const float* in = R.state_in ? R.state_in + (R.in_by_slot ? by_slot : by_seq) * R.dk * R.dv + row * ri : nullptr;
-        float* out = R.state_out ? R.state_out + (R.out_by_slot ? by_slot : by_seq) * R.dk * R.dv : nullptr;
-        if (nch == 0) {
-            if (out && row < R.dk)
-                for (int c = wg * HV; c < min(R.dv, wg * HV + HV); ++c) out[row * ri + c * ci] = in ? in[c * ci] : 0.0f;
-            return;
-        }
+        if (nch == 0) return;
         int n;
-        int64_t a = chunk_at(0, &n);
-        if (in) {
+        chunk_at(0, &n);
+        if (R.state_in) {
+            const int64_t ri = R.transposed ? 1 : R.dv, ci = R.transposed ? R.dk : 1;
+            const float* in = R.state_in + ((R.in_by_slot ? (int64_t)slot : (int64_t)seq) * A.H + h) * R.dk * R.dv + row * ri;
             const uint32_t St = tm + ((uint32_t)((warp & 3) * 32) << 16) + Z::U + wg * HV;
 #pragma unroll 1
             for (int cb = 0; cb < HV; cb += 32) {
                 uint32_t r[32];
-                if (ci == 1) {  // (a row is dv values, a multiple of 8)
-                    const bool whole = (reinterpret_cast<uintptr_t>(in) & 31) == 0;
-#pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        const int col = wg * HV + cb + j;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) r[j + e] = 0;
-                        if (row < R.dk && col < R.dv) {
-                            if (whole) ld32(in + col, r + j);
-                            else {
-                                const uint4 x = *reinterpret_cast<const uint4*>(in + col), y = *reinterpret_cast<const uint4*>(in + col + 4);
-                                r[j] = x.x, r[j + 1] = x.y, r[j + 2] = x.z, r[j + 3] = x.w;
-                                r[j + 4] = y.x, r[j + 5] = y.y, r[j + 6] = y.z, r[j + 7] = y.w;
-                            }
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const int col = wg * HV + cb + j;
-                        r[j] = row < R.dk && col < R.dv ? __float_as_uint(in[col * ci]) : 0u;
-                    }
-                }
+                read_row(in, ci, row < R.dk, wg * HV + cb, r);
                 __syncwarp();
                 tmem_st32(St + cb, r);
             }
             tmem_wait_st();
         }
         if (!wait(&sh.kv_full[0], 0)) return;
-        if constexpr (BF && !OUT) {
-            // The state pass of bf16: K's weights reach to the segment's end, U adds up over all
-            // chunks, and the state is read once.  Where K takes two parts, the second has two
-            // buffers: a chunk is weighed while the last one is multiplied.
-            if (in) pass(tid, 1.0f, false, 0, true, exp2f(l2 * (float)len), nullptr);
-            const int n_kv = nch * nk;
-            for (int kv = 0; kv < n_kv; ++kv) {
-                a = chunk_at(kv / nk, &n);
-                if (kv > 0 && !wait(&sh.kv_full[kv % NS], kv / NS)) return;
-                const int last = kv - (exact ? 1 : 2);  // the parts' buffer is free
-                if (last >= 0 && !wait(&sh.u_done[last & 1], last >> 1)) return;
-                const int64_t far = rev ? a - t0 : t0 + len - a - n;
-                scan(kv, n, tid);
-                weigh(kv, n, 1.0f, tid, exp2f(l2 * (float)far), kv);
-                arrive(&sh.k_ready[kv & 1]);
-            }
-            if (!wait(&sh.u_done[(n_kv - 1) & 1], (n_kv - 1) >> 1)) return;  // (and with it all before)
-            tc_fence_after();
-            pass(tid, 1.0f, false, 0, false, 1.0f, out);
-            return;
-        }
         float k_up = k_scale(scan(0, n, tid), tid);
-        if (in) pass(tid, 1.0f, OUT, 0, true, exp2f(l2 * (float)n) * (k_up * up1), nullptr);
+        if (R.state_in) pass(tid, 1.0f, true, 0, true, exp2f(l2 * (float)n) * (k_up * up1));
         const int n_kv = nch * nk;
-        for (int kv = 0, us = 0; kv < n_kv; ++kv) {  // (a chunk's q-heads share one load)
-            const int c = kv / nk;
-            a = chunk_at(c, &n);
-            // P has read K (and O2 the state, in whose place the third part goes)
-            if (OUT && !wait(&sh.k_free, us)) return;
-            weigh(kv, n, k_up, tid, 1.0f, us);
-            arrive(&sh.k_ready[us & 1]);
+        for (int kv = 0; kv < n_kv; ++kv) {  // (a chunk's q-heads share one load)
+            const int c = kv / nk, c2 = (kv + 1) / nk;
+            chunk_at(c, &n);
+            if (!wait(&sh.k_free, kv)) return;  // P has read K
+            weigh(kv, n, k_up, tid, kv);
+            arrive(&sh.k_ready[kv & 1]);
             const float up = k_up * up1;
-            const bool more = kv + 1 < n_kv;
-            const int c2 = (kv + 1) / nk;
-            int n2 = 0;
-            if (more) {  // the next load's scan, while U runs
-                chunk_at(c2, &n2);
-                if (!wait(&sh.kv_full[(kv + 1) % NS], (kv + 1) / NS)) return;
-                k_up = k_scale(scan(kv + 1, n2, tid), tid);
+            if (kv + 1 == n_kv) {
+                wait(&sh.u_done[kv & 1], kv >> 1);  // (before the tensor memory goes)
+                return;
             }
-            float factor = 1.0f;
-            if (more) factor = (c2 != c ? exp2f(l2 * (float)n2) : 1.0f) * (BF ? 1.0f : k_up * up1 / up);
-            if (!wait(&sh.u_done[us & 1], us >> 1)) return;
-            ++us;
+            // the next load's scan, while U runs
+            int n2;
+            chunk_at(c2, &n2);
+            if (!wait(&sh.kv_full[(kv + 1) % NS], (kv + 1) / NS)) return;
+            k_up = k_scale(scan(kv + 1, n2, tid), tid);
+            const float factor = (c2 != c ? exp2f(l2 * (float)n2) : 1.0f) * (BF ? 1.0f : k_up * up1 / up);
+            if (!wait(&sh.u_done[kv & 1], kv >> 1)) return;
             tc_fence_after();
-            if (more) {
-                if (!BF || c2 != c) pass(tid, up, OUT && c2 != c, R.state_in ? c2 : c2 - 1, true, factor, nullptr);
-            } else if (out)
-                pass(tid, up, false, 0, false, 1.0f, out);
+            if (!BF || c2 != c) pass(tid, up, c2 != c, R.state_in ? c2 : c2 - 1, true, factor);
         }
     }
 
@@ -948,9 +970,9 @@ struct TcBlock {
 };
 
 template <typename T, int DK, int DV, bool OUT>
-__global__ void __launch_bounds__(TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloat16>::value>::NT,
-                                  TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloat16>::value>::BLOCKS) k_lin_tc(const __grid_constant__ TcArgs A) {
-    using Z = TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloat16>::value>;
+__global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT,
+                                  TcSize<DK, DV, OUT>::BLOCKS) k_lin_tc(const __grid_constant__ TcArgs A) {
+    using Z = TcSize<DK, DV, OUT>;
     extern __shared__ __align__(1024) unsigned char sm[];
     TcShared& sh = *reinterpret_cast<TcShared*>(sm + Z::TILES);
     const TcRole& R = A.role[blockIdx.x % A.nroles];
@@ -976,7 +998,7 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloa
     __syncwarp();
     if (tid / 32 == ISSUE) tmem_alloc(&sh.tmem, Z::COLS);
     const float l2 = clamp_lam(A.lam[h]) * 1.44269504088896341f;
-    const bool exact = R.state_out && R.exact;
+    const bool exact = !OUT && R.exact;
     // K's weights are g1 e^{lam d}, d >= 0.  fp16: a fast decay (reversed) or a small scale
     // would sink all of them, so a power of two goes from g1 into the state's unit.
     float g1 = R.sk * (rev ? exp2f(l2) : 1.0f), up1 = 1.0f;
@@ -990,14 +1012,11 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloa
         if (tid < 16) sh.grow[rev ? tid : 15 - tid] = e;
         sh.wt[rev ? TC_C - 1 - tid : 32 + tid] = R.sq * R.sk * e;
         if (tid < 32) sh.wt[rev ? TC_C + tid : tid] = 0.0f;
-        const uint32_t hi = pack2<T>(d, d);
-        float left = d - unpack2<T>(hi).x;
-        const uint32_t lo = pack2<T>(left, left);
-        sh.dec2[tid] = make_uint2(hi, lo);
-        if (std::is_same<T, __half>::value || !OUT) sh.dec[tid] = d;
+        if (exact) sh.dec[tid] = d;
         else {
-            left -= unpack2<T>(lo).x;
-            sh.dec3[tid] = pack2<T>(left, left);
+            const uint32_t hi = pack2<T>(d, d);
+            const float left = d - unpack2<T>(hi).x;
+            sh.dec2[tid] = make_uint2(hi, pack2<T>(left, left));
         }
     }
     tc_fence_before();
@@ -1019,7 +1038,7 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloa
             if (tid < 2 * TC_GROUP + 32) B.issue();
         }
     } else {
-        if (tid < TC_GROUP) B.states(tid);
+        if (tid < TC_GROUP) B.sum_states(tid);
         else B.issue();
     }
     __syncwarp();
@@ -1110,7 +1129,7 @@ int tc_segment(int64_t T, int N, int H, int roles, bool equal) {
 template <typename T, int DK, int DV, bool OUT>
 static cudaError_t tc_launch(const TcArgs& A, cudaStream_t st) {
     constexpr auto kern = k_lin_tc<T, DK, DV, OUT>;
-    using Z = TcSize<DK, DV, OUT, std::is_same<T, __nv_bfloat16>::value>;
+    using Z = TcSize<DK, DV, OUT>;
     constexpr size_t smem = Z::BYTES;
     int dev = 0, sms = 0, per = 0;
     cudaError_t e = current_device_sms(&dev, &sms);
@@ -1122,8 +1141,8 @@ static cudaError_t tc_launch(const TcArgs& A, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-static_assert(TcSize<128, 128, true, true>::BYTES <= 232448 && TcSize<128, 128, false, true>::BYTES <= 232448 / 2 - 1024 &&
-                  TcSize<128, 128, false, false>::BYTES <= 232448, "shared memory of a block");
+static_assert(TcSize<128, 128, true>::BYTES <= 232448 && TcSize<128, 128, false>::BYTES <= 232448 / 2 - 1024,
+              "shared memory of a block");
 
 template <typename T, bool OUT>
 static cudaError_t tc_dims(const TcArgs& A, int dk, int dv, cudaStream_t st) {
@@ -1157,7 +1176,7 @@ cudaError_t tc_run(laplex_dtype dt, const LinRole* roles, int count, const LinSe
                         return cudaSuccess;
                 if (maps == 4) return cudaErrorInvalidValue;
                 key[maps++] = {x, dim, heads};
-                return S.T > 0 ? encode(&A.map[*m], dt, x, dim, heads, S.T, state_only && dt == LAPLEX_BF16 ? 64 : TC_C) : cudaSuccess;
+                return S.T > 0 ? encode(&A.map[*m], dt, x, dim, heads, S.T, state_only ? 64 : TC_C) : cudaSuccess;
             };
             cudaError_t e = state_only ? cudaSuccess : map_of(L.q, L.dk, H * L.nq, &R.mq);
             if (e == cudaSuccess) e = map_of(L.k, L.dk, H * L.nk, &R.mk);
@@ -1172,7 +1191,7 @@ cudaError_t tc_run(laplex_dtype dt, const LinRole* roles, int count, const LinSe
             R.in_by_slot = L.in_by_slot;
             R.out_by_slot = L.out_by_slot;
             R.skip_last = L.skip_last;
-            R.exact = !state_only || !L.skip_last;
+            R.exact = state_only && !L.skip_last;
             R.sq = (float)L.sq;
             R.sk = (float)L.sk;
             R.q = L.q.p;
