@@ -6,9 +6,14 @@
 // bytes in fp32), against 3 + 2 (q-heads per state) flops a value.  A block
 // holds a [dk, TC] piece of one state in registers: all of its loads are in
 // flight before the first is used, and the state is not read again for the
-// outputs.  TC = 128 columns (32 lanes x 16 bytes) where there are enough blocks
-// to fill the GPU, 32 where there are few, so that one token's states spread
-// over more SMs.
+// outputs.  TC = 64 columns of fp32 (16 lanes x 16 bytes) where there are enough
+// blocks to fill the GPU, 32 where there are few, so that one token's states
+// spread over more SMs.
+//
+// 4096 states of 128 x 128 (543 MB in all): 101 us, 5.4 TB/s, five blocks of 256
+// threads on an SM (48 registers; without that limit four: 107 us; two: 154).
+// TC = 128: 111 us, and 62 against 35 us for 64 x 64, whose blocks were half idle;
+// TC = 32: 142 us.  One row of 16 states: 3.5 us, launch and latency.
 #include <algorithm>
 
 #include "devcache.h"
@@ -23,7 +28,7 @@ constexpr int STEP_DK = 128;
 
 // LANES lanes across the columns, STEP_NT / LANES row groups
 template <typename T, int LANES>
-__global__ void __launch_bounds__(STEP_NT) k_step(const __grid_constant__ LinStep P) {
+__global__ void __launch_bounds__(STEP_NT, sizeof(T) == 8 ? 2 : 5) k_step(const __grid_constant__ LinStep P) {
     using A = typename AccOf<T>::A;
     constexpr int VN = 16 / (int)sizeof(A), TC = LANES * VN, RG = STEP_NT / LANES, RPT = STEP_DK / RG;
     constexpr int NW = STEP_NT / 32;
@@ -52,12 +57,37 @@ __global__ void __launch_bounds__(STEP_NT) k_step(const __grid_constant__ LinSte
         for (int c = 0; c < VN; ++c) S[r].v[c] = 0;
         if (in && i < P.dk) S[r] = *reinterpret_cast<const Pack<A, VN>*>(st + (int64_t)i * P.dv);
     }
+    const auto load_q = [&](int g0, int gn) {
+        for (int i = tid; i < gn * STEP_DK; i += STEP_NT) {
+            const int g = i / STEP_DK, c = i % STEP_DK;
+            qs[g][c] = c < P.dk ? to_acc<A, T>(static_cast<const T*>(
+                                      P.q.p)[row * P.q.ts + (int64_t)(h * G + g0 + g) * P.q.hs + c])
+                                : (A)0;
+        }
+    };
+    const auto load_kv = [&]() {
+        for (int i = tid; i < STEP_DK; i += STEP_NT)
+            ks[i] = i < P.dk ? to_acc<A, T>(static_cast<const T*>(P.k.p)[row * P.k.ts + (int64_t)h * P.k.hs + i]) : (A)0;
+        for (int i = tid; i < TC; i += STEP_NT)
+            vs[i] = c0 + i < P.dv ? to_acc<A, T>(static_cast<const T*>(P.v.p)[row * P.v.ts + (int64_t)h * P.v.hs + c0 + i])
+                                  : (A)0;
+    };
+    // all loads of the row before the first barrier
+    load_kv();
+    load_q(0, min(STEP_GB, G));
+    if (tid == 0) next = INT32_MAX;
     // Rows that name one slot are applied in row order: the first one's block
     // takes them all, the others leave.
+    bool more = false;
     if (P.slot) {
-        int earlier = 0;
-        for (int64_t m = tid; m < row; m += STEP_NT) earlier |= P.slot[m] == (int32_t)slot;
+        int earlier = 0, later = 0;
+        for (int64_t m = tid; m < P.rows; m += STEP_NT) {
+            const int same = P.slot[m] == (int32_t)slot;
+            if (m < row) earlier |= same;
+            if (m > row) later |= same;
+        }
         if (__syncthreads_or(earlier)) return;
+        more = __syncthreads_or(later);
     }
     // e^lam as a sum of two values: rounded once to fp32, its error would add
     // up over the tokens that a slow decay remembers
@@ -65,12 +95,6 @@ __global__ void __launch_bounds__(STEP_NT) k_step(const __grid_constant__ LinSte
     const A ghi = (A)g2, glo = (A)(g2 - (double)ghi);
     const A scale = (A)P.scale;
     while (true) {
-        for (int i = tid; i < STEP_DK; i += STEP_NT)
-            ks[i] = i < P.dk ? to_acc<A, T>(static_cast<const T*>(P.k.p)[row * P.k.ts + (int64_t)h * P.k.hs + i]) : (A)0;
-        for (int i = tid; i < TC; i += STEP_NT)
-            vs[i] = c0 + i < P.dv ? to_acc<A, T>(static_cast<const T*>(P.v.p)[row * P.v.ts + (int64_t)h * P.v.hs + c0 + i])
-                                  : (A)0;
-        if (tid == 0) next = INT32_MAX;
         __syncthreads();
 #pragma unroll
         for (int r = 0; r < RPT; ++r) {
@@ -81,13 +105,10 @@ __global__ void __launch_bounds__(STEP_NT) k_step(const __grid_constant__ LinSte
         }
         for (int g0 = 0; g0 < G; g0 += STEP_GB) {
             const int gn = min(STEP_GB, G - g0);
-            for (int i = tid; i < gn * STEP_DK; i += STEP_NT) {
-                const int g = i / STEP_DK, c = i % STEP_DK;
-                qs[g][c] = c < P.dk ? to_acc<A, T>(static_cast<const T*>(
-                                          P.q.p)[row * P.q.ts + (int64_t)(h * G + g0 + g) * P.q.hs + c])
-                                    : (A)0;
+            if (g0 > 0) {
+                load_q(g0, gn);
+                __syncthreads();
             }
-            __syncthreads();
             for (int g = 0; g < gn; ++g) {
                 A p[VN];
 #pragma unroll
@@ -120,7 +141,7 @@ __global__ void __launch_bounds__(STEP_NT) k_step(const __grid_constant__ LinSte
                         from_acc<T, A>(s * scale);
             }
         }
-        if (!P.slot) break;
+        if (!more) break;
         int mine = INT32_MAX;
         for (int64_t m = row + 1 + tid; m < P.rows; m += STEP_NT)
             if (P.slot[m] == (int32_t)slot) { mine = (int)m; break; }
@@ -129,6 +150,9 @@ __global__ void __launch_bounds__(STEP_NT) k_step(const __grid_constant__ LinSte
         __syncthreads();
         row = next;
         __syncthreads();
+        if (tid == 0) next = INT32_MAX;
+        load_kv();
+        load_q(0, min(STEP_GB, G));
     }
 #pragma unroll
     for (int r = 0; r < RPT; ++r) {
@@ -144,14 +168,12 @@ static cudaError_t step_launch(const LinStep& P, cudaStream_t st) {
     int dev = 0, sms = 0;
     cudaError_t e = current_device_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
-    const int64_t wide = P.rows * P.hkv * ((P.dv + 32 * VN - 1) / (32 * VN));
-    if (wide >= 2 * sms) {
-        const dim3 grid((unsigned)P.rows, (unsigned)P.hkv, (unsigned)((P.dv + 32 * VN - 1) / (32 * VN)));
-        k_step<T, 32><<<grid, STEP_NT, 0, st>>>(P);
-    } else {
-        const dim3 grid((unsigned)P.rows, (unsigned)P.hkv, (unsigned)((P.dv + 8 * VN - 1) / (8 * VN)));
-        k_step<T, 8><<<grid, STEP_NT, 0, st>>>(P);
-    }
+    const auto grid = [&](int lanes) {
+        return dim3((unsigned)P.rows, (unsigned)P.hkv, (unsigned)((P.dv + lanes * VN - 1) / (lanes * VN)));
+    };
+    const dim3 g = grid(16);
+    if ((int64_t)g.x * g.y * g.z >= 2 * sms) k_step<T, 16><<<g, STEP_NT, 0, st>>>(P);
+    else k_step<T, 8><<<grid(8), STEP_NT, 0, st>>>(P);
     return cudaGetLastError();
 }
 
