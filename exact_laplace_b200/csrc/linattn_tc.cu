@@ -62,6 +62,7 @@ namespace lx {
 
 constexpr int TC_GROUP = 256;  // threads of the state warps, and of the rows warps
 constexpr int TC_C = 128;  // tokens per chunk
+constexpr int WORK_REGS = 104, ISSUE_REGS = 64;  // a thread's registers in the products kernel
 
 struct TcRole {
     int mq, mk, mv;  // maps of the operands
@@ -91,13 +92,14 @@ struct alignas(64) TcArgs {
 
 // shared memory behind the tiles
 struct TcShared {
-    uint64_t kv_full[4], q_full;             // copies
+    uint64_t kv_full[2], q_full;             // copies
     // A waiter names a phase by its parity, so no barrier may run two phases ahead of one of
     // its waiters.  (p_done is waited for by the rows warps at every item; k_free says the same
     // to the state warps where they weigh K; v_ready, k_ready and u_done run one load ahead: two of each.)
     uint64_t p_done, k_free, o2_done, o_done, u_done[2];  // products
     uint64_t v_ready[2], k_ready[2], s_ready;          // from the state warps
     uint64_t p_ready, o_read;                          // from the rows warps
+    uint64_t k_max, s_max, p_max[4];                   // fp16: maxima exchanged among the state warps, in a pair of rows warps
     uint32_t tmem;
     uint32_t dead;       // a wait ran out
     alignas(16) float grow[16];  // e^{lam j}, 16 columns of P towards the row's end
@@ -107,8 +109,8 @@ struct TcShared {
         uint2 dec2[TC_C];  // as sums of two 16-bit values, each twice
     };
     float s_inv[2];      // fp16: what the rounded state is to be multiplied by, by chunk
-    uint8_t rexp[2][TC_C];  // fp16: the exponent of a row's largest weight, by half
-    float red[2][8];     // fp16: maxima of the state warps
+    uint8_t rexp[2][2][TC_C];  // fp16: the exponent of a row's largest weight, by item and half
+    float red[3][8];     // fp16: maxima of the state warps: of K, by load, and of the state
 };
 
 // Products: chunks of 128 tokens.  The state pass takes 64, with two blocks on an SM: it only
@@ -132,12 +134,6 @@ template <int DK, int DV, bool OUT> struct TcSize {
     // the issuing warp brings three idle ones: registers are moved between groups of four warps
     static constexpr int NT = OUT ? 2 * TC_GROUP + 128 : TC_GROUP + 32;
 };
-
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 // two values to 16 bits, the first in the low half
 template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
@@ -207,11 +203,6 @@ template <typename T> struct Pair;
                 : "r"(a), "r"(b), "r"(c));                                                                 \
             return r;                                                                                      \
         }                                                                                                  \
-        static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {                           \
-            uint32_t r;                                                                                    \
-            asm("sub.rn." S " %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));                                     \
-            return r;                                                                                      \
-        }                                                                                                  \
     };
 LX_PAIR(__nv_bfloat16, "bf16x2")
 LX_PAIR(__half, "f16x2")
@@ -228,10 +219,6 @@ __device__ __forceinline__ void ld32(const float* p, uint32_t* r) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "l"(p)
                  : "memory");
-}
-
-template <int ID> __device__ __forceinline__ void group_sync() {
-    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(TC_GROUP) : "memory");
 }
 
 // What every warp of a block knows.
@@ -276,6 +263,12 @@ struct TcBlock {
     __device__ __forceinline__ void arrive(uint64_t* bar) const {
         __syncwarp();
         if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+    }
+
+    // a barrier of the warps that arrive there; bounded, unlike bar.sync, since a warp whose wait ran out does not come
+    __device__ __forceinline__ bool meet(uint64_t* bar, uint32_t parity) const {
+        arrive(bar);
+        return wait(bar, parity);
     }
 
     // ---- copies and products: by one warp, all lanes of which walk through them together (the
@@ -507,8 +500,8 @@ struct TcBlock {
     }
 
     // The state, in tensor memory in units of 1 / up: rounded into shared memory as the B operand of O2 (which: its number);
-    // scaled for the next U; or out into memory.
-    __device__ __forceinline__ void pass(int tid, float up, bool round, int which, bool scale, float factor) const {
+    // scaled for the next U.
+    __device__ __forceinline__ bool pass(int tid, float up, bool round, int which, float factor) const {
         const int warp = tid >> 5, lane = tid & 31, wg = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t St = tm + ((uint32_t)((warp & 3) * 32) << 16) + Z::U + wg * HV;
         float s_up = 1.0f / up;
@@ -529,10 +522,10 @@ struct TcBlock {
             if (row >= R.dk) m = 0.0f;  // (dk < 128: rows that repeat others or hold nothing)
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, s));
-            if (lane == 0) sh.red[1][warp] = m;
-            group_sync<1>();
+            if (lane == 0) sh.red[2][warp] = m;
+            if (!meet(&sh.s_max, which)) return false;
 #pragma unroll
-            for (int w = 0; w < 8; ++w) m = fmaxf(m, sh.red[1][w]);
+            for (int w = 0; w < 8; ++w) m = fmaxf(m, sh.red[2][w]);
             s_up = scale_to_fp16(m);
             if (tid == 0) sh.s_inv[which & 1] = 1.0f / (s_up * up);
         }
@@ -556,16 +549,14 @@ struct TcBlock {
                     *reinterpret_cast<uint4*>(sm + Z::S + (at >> 6) * (DK * 128) + tile_at(row, (at & 63) >> 3)) = w;
                 }
             }
-            if (scale) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const float2 x = mul2(pair(r[j], r[j + 1]), make_float2(factor, factor));
-                    r[j] = __float_as_uint(x.x);
-                    r[j + 1] = __float_as_uint(x.y);
-                }
-                __syncwarp();
-                tmem_st32(St + cb, r);
+            for (int j = 0; j < 32; j += 2) {
+                const float2 x = mul2(pair(r[j], r[j + 1]), make_float2(factor, factor));
+                r[j] = __float_as_uint(x.x);
+                r[j + 1] = __float_as_uint(x.y);
             }
+            __syncwarp();
+            tmem_st32(St + cb, r);
         }
         if (round) {
             fence_proxy_async();
@@ -573,17 +564,19 @@ struct TcBlock {
         }
         tmem_wait_st();
         tc_fence_before();
+        return true;
     }
 
-    // fp16: the power of two for K, from the warps' maxima
-    __device__ __forceinline__ float k_scale(float km, int tid) const {
+    // fp16: the power of two for the K of load kv, from the warps' maxima; 0 after a wait that ran out.  (A buffer's
+    // second use is behind the U of its first, for which all warps have read it.)
+    __device__ __forceinline__ float k_scale(float km, int tid, int kv) const {
         if constexpr (BF) return 1.0f;
-        group_sync<1>();
-        if ((tid & 31) == 0) sh.red[0][tid >> 5] = km;
-        group_sync<1>();
+        float* red = sh.red[kv & 1];
+        if ((tid & 31) == 0) red[tid >> 5] = km;
+        if (!meet(&sh.k_max, kv)) return 0.0f;
         float m = 0.0f;
 #pragma unroll
-        for (int w = 0; w < 8; ++w) m = fmaxf(m, sh.red[0][w]);
+        for (int w = 0; w < 8; ++w) m = fmaxf(m, red[w]);
         return fminf(scale_to_fp16(m), 32768.0f);
     }
 
@@ -673,7 +666,8 @@ struct TcBlock {
             int n;
             const int64_t a = chunk_at(kv / nk, &n);
             if (!wait(&sh.kv_full[kv % NS], kv / NS)) return;
-            const float k_up = k_scale(scan(kv, n, tid), tid);
+            const float k_up = k_scale(scan(kv, n, tid), tid, kv);
+            if (k_up == 0.0f) return;
             const bool alone = BF && exact;  // the parts have one buffer
             if (alone && kv > 0 && !add(kv - 1)) return;
             weigh(kv, n, k_up, tid, kv);
@@ -712,8 +706,9 @@ struct TcBlock {
             tmem_wait_st();
         }
         if (!wait(&sh.kv_full[0], 0)) return;
-        float k_up = k_scale(scan(0, n, tid), tid);
-        if (R.state_in) pass(tid, 1.0f, true, 0, true, exp2f(l2 * (float)n) * (k_up * up1));
+        float k_up = k_scale(scan(0, n, tid), tid, 0);
+        if (k_up == 0.0f) return;
+        if (R.state_in && !pass(tid, 1.0f, true, 0, exp2f(l2 * (float)n) * (k_up * up1))) return;
         const int n_kv = nch * nk;
         for (int kv = 0; kv < n_kv; ++kv) {  // (a chunk's q-heads share one load)
             const int c = kv / nk, c2 = (kv + 1) / nk;
@@ -730,11 +725,12 @@ struct TcBlock {
             int n2;
             chunk_at(c2, &n2);
             if (!wait(&sh.kv_full[(kv + 1) % NS], (kv + 1) / NS)) return;
-            k_up = k_scale(scan(kv + 1, n2, tid), tid);
+            k_up = k_scale(scan(kv + 1, n2, tid), tid, kv + 1);
+            if (k_up == 0.0f) return;
             const float factor = (c2 != c ? exp2f(l2 * (float)n2) : 1.0f) * (BF ? 1.0f : k_up * up1 / up);
             if (!wait(&sh.u_done[kv & 1], kv >> 1)) return;
             tc_fence_after();
-            if (!BF || c2 != c) pass(tid, up, c2 != c, R.state_in ? c2 : c2 - 1, true, factor);
+            if ((!BF || c2 != c) && !pass(tid, up, c2 != c, R.state_in ? c2 : c2 - 1, factor)) return;
         }
     }
 
@@ -880,10 +876,10 @@ struct TcBlock {
                 }
                 if constexpr (!BF) {
                     const int e = (int)(__float_as_uint(m) >> 23);  // (m is finite)
-                    sh.rexp[wg][row] = (uint8_t)e;
-                    group_sync<2>();
-                    const float fresh = scale_of_exponent(max(e, (int)sh.rexp[wg ^ 1][row]));
-                    group_sync<2>();
+                    uint8_t(*const rexp)[TC_C] = sh.rexp[item & 1];
+                    rexp[wg][row] = (uint8_t)e;
+                    if (!meet(&sh.p_max[warp & 3], item)) return;
+                    const float fresh = scale_of_exponent(max(e, (int)rexp[wg ^ 1][row]));
                     // heads that sum into one O1 share a scale that only falls
                     const bool sum = nk > 1 && i > 0;
                     up = sum ? fminf(before, fresh) : fresh;
@@ -988,10 +984,11 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT,
     }
     constexpr int ISSUE = (OUT ? 2 : 1) * TC_GROUP / 32;  // the issuing warp
     if (tid == 0) {
-        for (uint64_t* b : {&sh.kv_full[0], &sh.kv_full[1], &sh.kv_full[2], &sh.kv_full[3], &sh.q_full, &sh.p_done, &sh.k_free, &sh.o2_done, &sh.o_done, &sh.u_done[0], &sh.u_done[1]})
+        for (uint64_t* b : {&sh.kv_full[0], &sh.kv_full[1], &sh.q_full, &sh.p_done, &sh.k_free, &sh.o2_done, &sh.o_done, &sh.u_done[0], &sh.u_done[1]})
             mbar_init(b, 1);
-        for (uint64_t* b : {&sh.v_ready[0], &sh.v_ready[1], &sh.k_ready[0], &sh.k_ready[1], &sh.s_ready, &sh.p_ready, &sh.o_read})
+        for (uint64_t* b : {&sh.v_ready[0], &sh.v_ready[1], &sh.k_ready[0], &sh.k_ready[1], &sh.s_ready, &sh.p_ready, &sh.o_read, &sh.k_max, &sh.s_max})
             mbar_init(b, TC_GROUP / 32);
+        for (uint64_t& b : sh.p_max) mbar_init(&b, 2);
         sh.dead = 0;
         fence_proxy_async();
     }
@@ -1028,13 +1025,13 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT,
     if constexpr (OUT) {
         // registers: 640 threads x 96 = 512 x 104 + 128 x 64
         if (tid < TC_GROUP) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(WORK_REGS));
             B.states(tid);
         } else if (tid < 2 * TC_GROUP) {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(WORK_REGS));
             B.rows(tid - TC_GROUP);
         } else {
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(ISSUE_REGS));
             if (tid < 2 * TC_GROUP + 32) B.issue();
         }
     } else {
@@ -1135,6 +1132,16 @@ static cudaError_t tc_launch(const TcArgs& A, cudaStream_t st) {
     cudaError_t e = current_device_sms(&dev, &sms);
     if (e == cudaSuccess) e = blocks_per_sm<kern>(dev, Z::NT, smem, &per);
     if (e != cudaSuccess) return e;
+    if (OUT) {  // the warps' shares of registers have to fit into what the block is launched with
+        static std::atomic<int> regs{0};
+        int r = regs.load(std::memory_order_relaxed);
+        if (r == 0) {
+            cudaFuncAttributes at;
+            if ((e = cudaFuncGetAttributes(&at, kern)) != cudaSuccess) return e;
+            regs.store(r = at.numRegs, std::memory_order_relaxed);
+        }
+        if (r * Z::NT < 2 * TC_GROUP * WORK_REGS + 128 * ISSUE_REGS) return cudaErrorInvalidConfiguration;
+    }
     const dim3 grid((unsigned)(A.S.slots * A.nroles), (unsigned)A.H);
     if (grid.x == 0) return cudaSuccess;
     kern<<<grid, Z::NT, smem, st>>>(A);
