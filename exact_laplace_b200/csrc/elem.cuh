@@ -26,11 +26,15 @@ template <typename T> struct VecOf { static constexpr int N = 16 / (int)sizeof(T
 // N elements of T, moved in accesses of at most 16 bytes
 template <typename T, int N> struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack { T v[N]; };
 
-// e^(lam d): lam is a log decay; -inf (no memory) acts as a decay that no
-// d >= 1 survives, without the NaN of -inf * 0
-__device__ __forceinline__ float clamp_lam(float lam) { return lam < -1e30f ? -1e30f : lam; }
-__device__ __forceinline__ double clamp_lam(double lam) { return lam < -1e30 ? -1e30 : lam; }
-__device__ __forceinline__ float decay(float lam, float d) { return expf(lam * d); }
+// e^(lam d): lam is a log decay; -inf (no memory) acts as a decay that no d >= 1
+// survives, without the NaN of -inf * 0.  fp32: what the product lam d rounds off
+// (2^-24 of it, so 1e-6 of the result at lam d = 16) is put back.
+__device__ __forceinline__ float clamp_lam(float lam) { return lam < -1e25f ? -1e25f : lam; }
+__device__ __forceinline__ double clamp_lam(double lam) { return lam < -1e25 ? -1e25 : lam; }
+__device__ __forceinline__ float decay(float lam, float d) {
+    const float x = lam * d, e = expf(x);
+    return fmaf(e, fmaf(lam, d, -x), e);
+}
 __device__ __forceinline__ double decay(double lam, double d) { return exp(lam * d); }
 
 }  // namespace lx

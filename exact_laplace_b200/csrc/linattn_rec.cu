@@ -12,17 +12,25 @@
 // carries e^{lam (n - 1 - tau)} and the output its inverse, so that a token costs
 // two multiply-adds per state element and the rounding of e^lam enters once per n
 // tokens (a product of 2000 rounded e^lam would be off by 6e-5).  n is at most
-// 4 / |lam|: neither factor leaves [e^-4, e^4].
+// 16 / |lam|: neither factor leaves [e^-16, e^16], so fp32 loses nothing to its
+// range, and decay() gives both to 2^-23.  (At most 4 / |lam| made blocks of one
+// token where lam = -4: 195 against 91 us for 6000 tokens of 6 heads.)
 //
 // Rows of the type that it computes in come by asynchronous copies, a block of
-// tokens ahead; 16-bit rows (whose products run elsewhere: linattn_tc.cu) are
-// converted on their way in.
+// tokens ahead; 16-bit rows (only in the decay's derivative: their products run in
+// linattn_tc.cu) are converted on their way in.  fp32 multiply-adds go two at a time (a pair of
+// the state's rows): half the instructions to issue.
 //
-// Bound by those multiply-adds (4 dk dv flops a token and head).  Long sequences
-// are cut into segments (see LinSeqs): a first pass sums each segment's own
-// state, carry_run joins them, and the product starts each segment from its
-// state.
+// Bound by those multiply-adds (4 dk dv flops a token and head) and the latencies
+// around them: 32768 tokens, 16 heads of 128 x 128 take 972 us for the outputs, 499
+// for the states alone, 35 Tflop/s of the 72 that 128 fp32 units an SM give.  (6000
+// tokens, 6 heads of 72 x 104: 75 and 37 us; with one multiply-add an instruction and
+// outputs reduced token by token 119 and 54.)
+// Long sequences are cut into segments (see LinSeqs): a first pass sums each
+// segment's own state, carry_run joins them, and the product starts each segment
+// from its state.
 #include <algorithm>
+#include <type_traits>
 
 #include "devcache.h"
 #include "elem.cuh"
@@ -32,6 +40,7 @@ namespace lx {
 
 constexpr int REC_NT = 128;
 constexpr int REC_COLS = 64;  // state columns of a block
+constexpr int REC_OUT = 80;   // pitch of a row of outputs: four rows' stores in distinct banks
 constexpr int REC_MAX = 32;   // most rows (tokens times heads of a group) in one stage
 
 struct RecArgs {
@@ -46,52 +55,141 @@ struct RecArgs {
     int rows;            // rows of k, v, q in one of the two stages: 16, or 32 for more than 16 heads
 };
 
-// rows (token tau of the block, head g) of X into dst[row][PITCH], from column c0; a warp to a row
-template <typename T, typename A, int PITCH>
-__device__ __forceinline__ void rec_load(A* dst, const LinRows& X, int heads, int h, int64_t t0, int len, int base,
-                                         int n, bool rev, int dim, int c0) {
+// Rows (token tau of the block, head g) of X into dst[row][PITCH], from column c0; a warp to a row.  `first`: row
+// `warp` of the block in memory, at this lane's first column, where ONE; it moves on by the block's nb tokens.
+// (From the token's index, the addresses were 15 of a token's 75 instructions in the state pass.)
+template <typename T, typename A, int PITCH, bool ONE>
+__device__ __forceinline__ void rec_load(A* dst, const LinRows& X, const T*& first, int heads, int h, int64_t t0, int len,
+                                         int base, int n, int nb, bool rev, int dim, int c0) {
     constexpr int VN = VecOf<T>::N;
     const int per = min(PITCH, dim - c0) / VN;  // (dims are multiples of 8)
     const int lane = threadIdx.x & 31;
-    for (int row = threadIdx.x >> 5; row < n * heads; row += REC_NT / 32) {
-        const int tau = heads == 1 ? row : row / heads, g = row - tau * heads;
-        const int64_t t = t0 + (rev ? len - 1 - base - tau : base + tau);
-        const T* src = static_cast<const T*>(X.p) + t * X.ts + (int64_t)(h * heads + g) * X.hs + c0;
-        for (int c = lane; c < per; c += 32) {
+    const auto move = [&](int row, const T* src) {
+        for (int c = lane; c < per; c += 32, src += 32 * VN) {
             if constexpr (sizeof(T) == sizeof(A)) {
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
                                  (uint32_t)__cvta_generic_to_shared(dst + row * PITCH + c * VN)),
-                             "l"(src + c * VN)
+                             "l"(src)
                              : "memory");
             } else {
-                const Pack<T, VN> v = *reinterpret_cast<const Pack<T, VN>*>(src + c * VN);
+                const Pack<T, VN> v = *reinterpret_cast<const Pack<T, VN>*>(src);
 #pragma unroll
                 for (int e = 0; e < VN; ++e) dst[row * PITCH + c * VN + e] = to_acc<A, T>(v.v[e]);
             }
         }
+    };
+    if constexpr (ONE) {
+        const int64_t ts = rev ? -X.ts : X.ts;
+        const T* src = first;
+        for (int row = threadIdx.x >> 5; row < n; row += REC_NT / 32, src += REC_NT / 32 * ts) move(row, src);
+        first += nb * ts;
+    } else {
+        for (int row = threadIdx.x >> 5; row < n * heads; row += REC_NT / 32) {
+            const int tau = heads == 1 ? row : row / heads, g = row - tau * heads;
+            const int64_t t = t0 + (rev ? len - 1 - base - tau : base + tau);
+            move(row, static_cast<const T*>(X.p) + t * X.ts + (int64_t)(h * heads + g) * X.hs + c0 + lane * VN);
+        }
     }
 }
 
+// Two values that one multiply-add instruction takes together (fp32; fp64 in two).
+template <typename A> struct Two;
+template <> struct Two<float> {
+    unsigned long long v;
+    static __device__ __forceinline__ Two of(float x, float y) {
+        Two r;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+        return r;
+    }
+    __device__ __forceinline__ float at(int i) const {
+        float x, y;
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+        return i ? y : x;
+    }
+    static __device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+        Two r;
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+        return r;
+    }
+    static __device__ __forceinline__ Two mul(Two a, Two b) {
+        Two r;
+        asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+        return r;
+    }
+    static __device__ __forceinline__ Two add(Two a, Two b) {
+        Two r;
+        asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+        return r;
+    }
+};
+template <> struct Two<double> {
+    double x, y;
+    static __device__ __forceinline__ Two of(double x, double y) { return {x, y}; }
+    __device__ __forceinline__ double at(int i) const { return i ? y : x; }
+    static __device__ __forceinline__ Two fma(Two a, Two b, Two c) { return {dfma(a.x, b.x, c.x), dfma(a.y, b.y, c.y)}; }
+    static __device__ __forceinline__ Two mul(Two a, Two b) { return {a.x * b.x, a.y * b.y}; }
+    static __device__ __forceinline__ Two add(Two a, Two b) { return {a.x + b.x, a.y + b.y}; }
+};
+
+// A thread's part of a state: rows 32 m + 4 rg + (0..3), in pairs, of 4 columns.
 template <typename A, int RPT>
-__device__ __forceinline__ void rec_state_io(A (&S)[RPT][4], const LinRole& R, A* mem, int64_t at, int rg, int col,
+__device__ __forceinline__ void rec_state_io(Two<A> (&S)[RPT / 2][4], const LinRole& R, A* mem, int64_t at, int rg, int col,
                                              bool store) {
     const int64_t ri = R.transposed ? 1 : R.dv, ci = R.transposed ? R.dk : 1;
     A* p = mem + at * R.dk * R.dv;
 #pragma unroll
-    for (int r = 0; r < RPT; ++r)
+    for (int r = 0; r < RPT; r += 2)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int i = (r / 4) * 32 + rg * 4 + (r % 4), j = col + c;
-            if (i < R.dk && j < R.dv) {
-                if (store) p[i * ri + j * ci] = S[r][c];
-                else S[r][c] = p[i * ri + j * ci];
+            if (i < R.dk && j < R.dv) {  // (dk is even)
+                A* a = p + i * ri + j * ci;
+                if (store) {
+                    a[0] = S[r / 2][c].at(0);
+                    a[ri] = S[r / 2][c].at(1);
+                } else {
+                    S[r / 2][c] = Two<A>::of(a[0], a[ri]);
+                }
             }
         }
 }
 
+// The sums over the 8 row groups (lane bits 0-2) of p[row][column], U rows of 4 columns, times each row's wq, into os.
+// Every step halves what a lane keeps.
+template <typename A, int U>
+__device__ __forceinline__ void rec_reduce(const A (&p)[U][4], const A* wq, A* os, int lane) {
+    const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+    if constexpr (U == 4) {
+        A x[2][4], y[4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                x[u][c] = (b0 ? p[2 + u][c] : p[u][c]) + __shfl_xor_sync(FULL, b0 ? p[u][c] : p[2 + u][c], 1);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = (b1 ? x[1][c] : x[0][c]) + __shfl_xor_sync(FULL, b1 ? x[0][c] : x[1][c], 2);
+        const A z0 = (b2 ? y[2] : y[0]) + __shfl_xor_sync(FULL, b2 ? y[0] : y[2], 4);
+        const A z1 = (b2 ? y[3] : y[1]) + __shfl_xor_sync(FULL, b2 ? y[1] : y[3], 4);
+        const int u = (b0 ? 2 : 0) + (b1 ? 1 : 0);
+        Pack<A, 2> o;
+        o.v[0] = z0 * wq[u];
+        o.v[1] = z1 * wq[u];
+        *reinterpret_cast<Pack<A, 2>*>(os + u * REC_OUT + (b2 ? 2 : 0)) = o;
+    } else {
+        A u0 = b0 ? p[0][2] : p[0][0], u1 = b0 ? p[0][3] : p[0][1];
+        u0 += __shfl_xor_sync(FULL, b0 ? p[0][0] : p[0][2], 1);
+        u1 += __shfl_xor_sync(FULL, b0 ? p[0][1] : p[0][3], 1);
+        A w = b1 ? u1 : u0;
+        w += __shfl_xor_sync(FULL, b1 ? u0 : u1, 2);
+        w += __shfl_xor_sync(FULL, w, 4);
+        if (!b2) os[(b0 ? 2 : 0) + (b1 ? 1 : 0)] = w * wq[0];
+    }
+}
+
 // READ 0: states only; 1: outputs; 2: the decay's derivative.  DER: also run the
-// states' derivative in lam, W_t = e^lam (W_{t-1} + S_{t-1}).
-template <typename T, int RPT, int READ, bool DER>
+// states' derivative in lam, W_t = e^lam (W_{t-1} + S_{t-1}).  ONE: one q-head and one
+// k-head to a state.
+template <typename T, int RPT, int READ, bool DER, bool ONE>
 __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs P) {
     using A = typename AccOf<T>::A;
     constexpr int DKP = RPT * 8;
@@ -100,8 +198,10 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
     const int cap = P.rows;
     A* const stages = reinterpret_cast<A*>(smem_raw);
     A* const os = stages + 2 * cap * STAGE;  // outputs of a block
-    __shared__ A up[REC_MAX + 1], down[REC_MAX + 1];  // e^{-lam j}, e^{lam j}
+    __shared__ A down[REC_MAX + 1];  // e^{lam j}
+    __shared__ A wks[REC_MAX], wqs[REC_MAX];  // a block's weights, by token: sk e^{lam (n - 1 - j)}; by row of q: sq e^{-lam (n - 1 - j)}
     const LinRole& R = P.R;
+    const int nq = ONE ? 1 : R.nq, nk = ONE ? 1 : R.nk;
     const int slot = blockIdx.x, h = blockIdx.y, c0 = blockIdx.z * REC_COLS;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rg = lane & 7, cl = warp * 16 + (lane >> 3) * 4, col = c0 + cl;
@@ -113,38 +213,47 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
     if (!used) return;
     if (READ == 0 && R.skip_last && (R.reverse ? t0 == P.S.at(seq) : t0 + len == P.S.at(seq + 1))) return;
     const A lam = clamp_lam(static_cast<const A*>(P.lam)[h]);
-    const int heads = R.nq > R.nk ? R.nq : R.nk;
+    const int heads = nq > nk ? nq : nk;
     int nb = cap / heads;
     const A al = lam < 0 ? -lam : lam;
-    if (al * nb > (A)4) nb = max(1, (int)((A)4 / al));
-    if (threadIdx.x <= nb) {
-        up[threadIdx.x] = decay(lam, -(A)threadIdx.x);
-        down[threadIdx.x] = decay(lam, (A)threadIdx.x);
-    }
-    for (int i = threadIdx.x; i < 2 * cap * STAGE; i += REC_NT) stages[i] = 0;  // columns past dk, dv stay 0
+    if (al * nb > (A)16) nb = max(1, (int)((A)16 / al));
+    if (threadIdx.x <= nb) down[threadIdx.x] = decay(lam, (A)threadIdx.x);
+    if (R.dk < DKP || R.dv - c0 < REC_COLS)  // columns past dk, dv stay 0
+        for (int i = threadIdx.x; i < 2 * cap * STAGE; i += REC_NT) stages[i] = 0;
     __syncthreads();
     const bool rev = R.reverse;
+    const auto first = [&](const LinRows& X, int c) {
+        const int64_t t = t0 + (rev ? len - 1 - warp : warp);
+        return static_cast<const T*>(X.p) + t * X.ts + (int64_t)h * X.hs + c + lane * VecOf<T>::N;
+    };
+    const T *kp = nullptr, *vp = nullptr, *qp = nullptr, *dp = nullptr;
+    if constexpr (ONE) {
+        kp = first(R.k, 0);
+        vp = first(R.v, c0);
+        if (READ != 0) qp = first(R.q, 0);
+    }
     const auto load = [&](int base, int s) {
         if (base < len) {
             const int n = min(nb, len - base);
             A* ks = stages + s * cap * STAGE;
             A *vs = ks + cap * DKP, *qs = vs + cap * REC_COLS, *ds = qs + cap * DKP;
-            rec_load<T, A, DKP>(ks, R.k, R.nk, h, t0, len, base, n, rev, R.dk, 0);
-            rec_load<T, A, REC_COLS>(vs, R.v, R.nk, h, t0, len, base, n, rev, R.dv, c0);
-            if constexpr (READ != 0) rec_load<T, A, DKP>(qs, R.q, R.nq, h, t0, len, base, n, rev, R.dk, 0);
-            if constexpr (READ == 2) rec_load<T, A, REC_COLS>(ds, P.dout, R.nq, h, t0, len, base, n, rev, R.dv, c0);
+            rec_load<T, A, DKP, ONE>(ks, R.k, kp, nk, h, t0, len, base, n, nb, rev, R.dk, 0);
+            rec_load<T, A, REC_COLS, ONE>(vs, R.v, vp, nk, h, t0, len, base, n, nb, rev, R.dv, c0);
+            if constexpr (READ != 0) rec_load<T, A, DKP, ONE>(qs, R.q, qp, nq, h, t0, len, base, n, nb, rev, R.dk, 0);
+            if constexpr (READ == 2) rec_load<T, A, REC_COLS, ONE>(ds, P.dout, dp, nq, h, t0, len, base, n, nb, rev, R.dv, c0);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
     load(0, 0);
 
-    A S[RPT][4], W[DER ? RPT : 1][4];
+    using V = Two<A>;
+    V S[RPT / 2][4], W[DER ? RPT / 2 : 1][4];
 #pragma unroll
-    for (int r = 0; r < RPT; ++r)
+    for (int r = 0; r < RPT / 2; ++r)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            S[r][c] = 0;
-            if constexpr (DER) W[r][c] = 0;
+            S[r][c] = V::of(0, 0);
+            if constexpr (DER) W[r][c] = V::of(0, 0);
         }
     const int64_t by_slot = (int64_t)slot * P.H + h, by_seq = (int64_t)seq * P.H + h;
     if (R.state_in)
@@ -152,99 +261,134 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
     if constexpr (DER)
         if (P.w_in) rec_state_io<A, RPT>(W, R, (A*)const_cast<void*>(P.w_in), by_slot, rg, col, false);
     A dsum = 0;
-    int stage = 0;
+    int stage = 0, weights_n = 0;
     for (int base = 0; base < len; base += nb, stage ^= 1) {
         const int n = min(nb, len - base);
         load(base + nb, stage ^ 1);
+        if (n != weights_n) {
+            weights_n = n;
+            for (int j = threadIdx.x; j < n * heads; j += REC_NT) {
+                if (j < n) wks[j] = (A)R.sk * decay(lam, (A)(n - 1 - j));
+                if (j < n * nq) wqs[j] = (A)R.sq * decay(lam, -(A)(n - 1 - j / nq));
+            }
+        }
         asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncthreads();
         const A* ks = stages + stage * cap * STAGE;
         const A *vs = ks + cap * DKP, *qs = vs + cap * REC_COLS, *ds = qs + cap * DKP;
-        const A pre = down[rev ? n - 1 : n];
+        const V pre = V::of(down[rev ? n - 1 : n], down[rev ? n - 1 : n]);
 #pragma unroll
-        for (int r = 0; r < RPT; ++r)
+        for (int r = 0; r < RPT / 2; ++r)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                S[r][c] *= pre;
-                if constexpr (DER) W[r][c] *= pre;
+                S[r][c] = V::mul(S[r][c], pre);
+                if constexpr (DER) W[r][c] = V::mul(W[r][c], pre);
             }
-        const int last = c0 + warp * 16 < R.dv ? n : 0;  // (a warp past dv has no column)
-#pragma unroll 2
-        for (int tau = 0; tau < last; ++tau) {
-            const A wk = (A)R.sk * down[n - 1 - tau], wq = (A)R.sq * up[n - 1 - tau];
+        const bool some = c0 + warp * 16 < R.dv;  // (a warp past dv has no column)
+        // row r of k and v, of token tau
+        const auto update = [&](int r, int tau) {
+            const Pack<A, 4> x = *reinterpret_cast<const Pack<A, 4>*>(vs + r * REC_COLS + cl);
+            const A wk = wks[tau];
+            V vv[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) vv[c] = V::of(x.v[c] * wk, x.v[c] * wk);
+#pragma unroll
+            for (int m = 0; m < RPT / 4; ++m) {
+                const Pack<V, 2> kk = *reinterpret_cast<const Pack<V, 2>*>(ks + r * DKP + m * 32 + rg * 4);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) S[m * 2 + j][c] = V::fma(kk.v[j], vv[c], S[m * 2 + j][c]);
+            }
+        };
+        // row r of q: this thread's part of S^T q (READ 2: of W^T q)
+        const auto read = [&](int r, A (&p)[4]) {
+            V a[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) a[c] = V::of(0, 0);
+#pragma unroll
+            for (int m = 0; m < RPT / 4; ++m) {
+                const Pack<V, 2> qq = *reinterpret_cast<const Pack<V, 2>*>(qs + r * DKP + m * 32 + rg * 4);
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if constexpr (READ == 2) a[c] = V::fma(qq.v[j], W[m * 2 + j][c], a[c]);
+                        else a[c] = V::fma(qq.v[j], S[m * 2 + j][c], a[c]);
+                    }
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) p[c] = a[c].at(0) + a[c].at(1);
+        };
+        const auto advance = [&](int tau) {  // token tau's k and v into the state
             if constexpr (DER) {
 #pragma unroll
-                for (int r = 0; r < RPT; ++r)
+                for (int r = 0; r < RPT / 2; ++r)
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) W[r][c] += S[r][c];
+                    for (int c = 0; c < 4; ++c) W[r][c] = V::add(W[r][c], S[r][c]);
             }
-            for (int g = 0; g < R.nk; ++g) {
-                const A* kr = ks + (tau * R.nk + g) * DKP;
-                const A* vr = vs + (tau * R.nk + g) * REC_COLS + cl;
-                Pack<A, 4> vv = *reinterpret_cast<const Pack<A, 4>*>(vr);
+            for (int g = 0; g < nk; ++g) update(tau * nk + g, tau);
+        };
+        if (some) {
+            if constexpr (READ == 1) {
+                // rows four at a time: their sums over the row groups take 14 exchanges and one store, not 16 and four
+                const int rows = n * nq;
+                int r = 0, tau = 0, g = 0;
+                const auto batch = [&](auto U) {
+                    A p[U.value][4];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) vv.v[c] *= wk;
-#pragma unroll
-                for (int m = 0; m < RPT / 4; ++m) {
-                    const Pack<A, 4> kk = *reinterpret_cast<const Pack<A, 4>*>(kr + m * 32 + rg * 4);
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) S[m * 4 + r][c] = dfma(kk.v[r], vv.v[c], S[m * 4 + r][c]);
-                }
-            }
-            if constexpr (READ != 0) {
-                for (int g = 0; g < R.nq; ++g) {
-                    const int row = tau * R.nq + g;
-                    const A* qr = qs + row * DKP;
-                    A p[4] = {0, 0, 0, 0};
-#pragma unroll
-                    for (int m = 0; m < RPT / 4; ++m) {
-                        const Pack<A, 4> qq = *reinterpret_cast<const Pack<A, 4>*>(qr + m * 32 + rg * 4);
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                if constexpr (READ == 2) p[c] = dfma(qq.v[r], W[m * 4 + r][c], p[c]);
-                                else p[c] = dfma(qq.v[r], S[m * 4 + r][c], p[c]);
+                    for (int u = 0; u < U.value; ++u) {
+                        if (ONE) update(r + u, r + u);
+                        else {
+                            if (g == 0) advance(tau);
+                            if (++g == nq) {
+                                g = 0;
+                                ++tau;
                             }
+                        }
+                        read(r + u, p[u]);
                     }
+                    rec_reduce<A, U.value>(p, wqs + r, os + r * REC_OUT + cl, lane);
+                };
+                for (; r + 4 <= rows; r += 4) batch(std::integral_constant<int, 4>());
+                for (; r < rows; ++r) batch(std::integral_constant<int, 1>());
+            } else {
+                constexpr int U = !DER ? 4 : sizeof(A) == 8 ? 1 : 2;
+#pragma unroll U
+                for (int tau = 0; tau < n; ++tau) {
+                    advance(tau);
                     if constexpr (READ == 2) {
-                        const Pack<A, 4> d = *reinterpret_cast<const Pack<A, 4>*>(ds + row * REC_COLS + cl);
-                        A x = 0;
+                        for (int g = 0; g < nq; ++g) {
+                            const int row = tau * nq + g;
+                            A p[4], x = 0;
+                            read(row, p);
+                            const Pack<A, 4> d = *reinterpret_cast<const Pack<A, 4>*>(ds + row * REC_COLS + cl);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) x = dfma(d.v[c], p[c], x);
-                        dsum = dfma(wq, x, dsum);
-                    } else {
-                        // sum over the 8 row groups (lane bits 0-2), halving the columns kept at each step
-                        const bool b0 = lane & 1, b1 = lane & 2;
-                        A u0 = b0 ? p[2] : p[0], u1 = b0 ? p[3] : p[1];
-                        u0 += __shfl_xor_sync(FULL, b0 ? p[0] : p[2], 1);
-                        u1 += __shfl_xor_sync(FULL, b0 ? p[1] : p[3], 1);
-                        A w = b1 ? u1 : u0;
-                        w += __shfl_xor_sync(FULL, b1 ? u0 : u1, 2);
-                        w += __shfl_xor_sync(FULL, w, 4);
-                        if (rg < 4) os[row * REC_COLS + cl + (b0 ? 2 : 0) + (b1 ? 1 : 0)] = w * wq;
+                            for (int c = 0; c < 4; ++c) x = dfma(d.v[c], p[c], x);
+                            dsum = dfma(wqs[row], x, dsum);
+                        }
                     }
                 }
             }
         }
         if (rev) {
-            const A post = down[1];
+            const V post = V::of(down[1], down[1]);
 #pragma unroll
-            for (int r = 0; r < RPT; ++r)
+            for (int r = 0; r < RPT / 2; ++r)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) S[r][c] *= post;
+                for (int c = 0; c < 4; ++c) S[r][c] = V::mul(S[r][c], post);
         }
         if constexpr (READ == 1) {
             __syncthreads();
+            constexpr int Q = REC_COLS / 4;  // (dv is a multiple of 8)
             const int cols = min(REC_COLS, R.dv - c0);
-            for (int i = threadIdx.x; i < n * R.nq * REC_COLS; i += REC_NT) {
-                const int row = i / REC_COLS, c = i - row * REC_COLS;
+            for (int i = threadIdx.x; i < n * nq * Q; i += REC_NT) {
+                const int row = i / Q, c = i % Q * 4;
                 if (c >= cols) continue;
-                const int tau = row / R.nq, g = row - tau * R.nq;
+                const int tau = row / nq, g = row - tau * nq;
                 const int64_t t = t0 + (rev ? len - 1 - base - tau : base + tau);
-                static_cast<T*>(R.o)[t * R.o_ts + (int64_t)(h * R.nq + g) * R.o_hs + c0 + c] = from_acc<T, A>(os[i]);
+                *reinterpret_cast<Pack<A, 4>*>(static_cast<A*>(R.o) + t * R.o_ts + (int64_t)(h * nq + g) * R.o_hs + c0 + c) =
+                    *reinterpret_cast<const Pack<A, 4>*>(os + row * REC_OUT + c);
             }
         }
         __syncthreads();  // this stage, and the outputs, have been read
@@ -256,16 +400,17 @@ __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs 
         // the last segment of a sequence: <dstate, W_last>
         const bool last = t0 + len >= P.S.at(seq + 1);
         if (P.dstate && last) {
-            A D[RPT][4];
+            V D[RPT / 2][4], sum = V::of(0, 0);
 #pragma unroll
-            for (int r = 0; r < RPT; ++r)
+            for (int r = 0; r < RPT / 2; ++r)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) D[r][c] = 0;
+                for (int c = 0; c < 4; ++c) D[r][c] = V::of(0, 0);
             rec_state_io<A, RPT>(D, R, (A*)const_cast<void*>(P.dstate), by_seq, rg, col, false);
 #pragma unroll
-            for (int r = 0; r < RPT; ++r)
+            for (int r = 0; r < RPT / 2; ++r)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) dsum = dfma(D[r][c], W[r][c], dsum);
+                for (int c = 0; c < 4; ++c) sum = V::fma(D[r][c], W[r][c], sum);
+            dsum += sum.at(0) + sum.at(1);
         }
         double* red = reinterpret_cast<double*>(smem_raw);
         __syncthreads();
@@ -368,23 +513,26 @@ __global__ void __launch_bounds__(128) k_carry(const __grid_constant__ LinCarry 
 // ---------------------------------------------------------------- host side
 
 // Tokens per segment.  Enough blocks for two rounds of the resident ones (148
-// SMs x 4); not under 128 tokens, below which the extra pass over k and v and
-// the states' traffic cost more than they spread.  Sequences of one known length
-// that fill the GPU by themselves are not cut.
+// SMs x 4), but not under 128 tokens, below which the extra pass over k and v and
+// the states' traffic cost as much as they spread (6000 tokens, 6 heads of 72 x 104:
+// 121 us with 128, 120 with 64, 127 with 192; 560 heads of 128 tokens of 64 x 64:
+// 55 us whole, 104 cut at 64) -- or 64 where 128 leaves SMs without a block (256
+// tokens, 6 heads: 33 against 52 us).  Sequences of one known length that fill the
+// GPU by themselves are not cut.
 int rec_segment(int64_t T, int N, int H, int dv, bool equal) {
     const int64_t cb = (dv + REC_COLS - 1) / REC_COLS;
     const int64_t whole = std::max<int64_t>(T, 1) + 1;
     if (equal && (int64_t)N * H * cb >= 592) return (int)std::min<int64_t>(whole, INT32_MAX);
     int64_t seg = (T * H * cb / 1184 + 63) / 64 * 64;
-    seg = std::max<int64_t>(seg, 128);
+    seg = std::max<int64_t>(seg, T * H * cb < 128 * 148 ? 64 : 128);
     return (int)std::min<int64_t>(seg >= T ? whole : seg, INT32_MAX);
 }
 
-template <typename T, int RPT, int READ, bool DER>
+template <typename T, int RPT, int READ, bool DER, bool ONE>
 static cudaError_t rec_launch(const RecArgs& P, cudaStream_t st) {
     using A = typename AccOf<T>::A;
-    constexpr auto kern = k_rec<T, RPT, READ, DER>;
-    constexpr size_t row = sizeof(A) * (2 * (RPT * 8 * (READ ? 2 : 1) + REC_COLS * (READ == 2 ? 2 : 1)) + (READ == 1 ? REC_COLS : 0));
+    constexpr auto kern = k_rec<T, RPT, READ, DER, ONE>;
+    constexpr size_t row = sizeof(A) * (2 * (RPT * 8 * (READ ? 2 : 1) + REC_COLS * (READ == 2 ? 2 : 1)) + (READ == 1 ? REC_OUT : 0));
     constexpr size_t most = row * REC_MAX;
     const size_t smem = row * P.rows;
     int dev = 0, sms = 0, per = 0;
@@ -397,12 +545,12 @@ static cudaError_t rec_launch(const RecArgs& P, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <typename T, int READ, bool DER>
+template <typename T, int READ, bool DER, bool ONE = false>
 static cudaError_t rec_dim(RecArgs P, cudaStream_t st) {
     P.rows = std::max(P.R.nq, P.R.nk) > 16 ? 32 : 16;
-    return P.R.dk <= 64   ? rec_launch<T, 8, READ, DER>(P, st)
-           : P.R.dk <= 96 ? rec_launch<T, 12, READ, DER>(P, st)
-                          : rec_launch<T, 16, READ, DER>(P, st);
+    return P.R.dk <= 64   ? rec_launch<T, 8, READ, DER, ONE>(P, st)
+           : P.R.dk <= 96 ? rec_launch<T, 12, READ, DER, ONE>(P, st)
+                          : rec_launch<T, 16, READ, DER, ONE>(P, st);
 }
 
 template <typename F>
@@ -423,10 +571,12 @@ cudaError_t rec_run(laplex_dtype dt, const LinRole& R, const LinSeqs& S, int H, 
     P.S = S;
     P.H = H;
     P.lam = lam;
-    return with_type(dt, [&](auto t) {
+    const auto go = [&](auto t) {
         using T = decltype(t);
+        if (R.nq == 1 && R.nk == 1) return state_only ? rec_dim<T, 0, false, true>(P, st) : rec_dim<T, 1, false, true>(P, st);
         return state_only ? rec_dim<T, 0, false>(P, st) : rec_dim<T, 1, false>(P, st);
-    });
+    };
+    return dt == LAPLEX_F64 ? go(double()) : go(float());
 }
 
 cudaError_t carry_run(laplex_dtype dt, const LinCarry& C, cudaStream_t st) {
