@@ -185,19 +185,18 @@ cudaError_t segment_states(const laplex_linattn_shape& s, Direction* D, int coun
         R[i].o = nullptr;
     }
     cudaError_t e = run(s, R, count, S, true, status, st);
-    for (int i = 0; i < count && e == cudaSuccess; ++i) {
-        lx::LinCarry C = {};
-        C.S = S;
-        C.H = s.hkv;
-        C.reverse = D[i].R.reverse;
-        C.len = (int64_t)s.dk * s.dv;
-        C.lam = s.log_decay;
-        C.init = D[i].init;
-        C.states = D[i].states;
-        C.last = D[i].last;
-        e = lx::carry_run(s.dtype, C, st);
+    lx::LinCarry C[2] = {};
+    for (int i = 0; i < count; ++i) {
+        C[i].S = S;
+        C[i].H = s.hkv;
+        C[i].reverse = D[i].R.reverse;
+        C[i].len = (int64_t)s.dk * s.dv;
+        C[i].lam = s.log_decay;
+        C[i].init = D[i].init;
+        C[i].states = D[i].states;
+        C[i].last = D[i].last;
     }
-    return e;
+    return e == cudaSuccess ? lx::carry_run(s.dtype, C, count, st) : e;
 }
 
 }  // namespace

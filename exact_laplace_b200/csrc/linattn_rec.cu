@@ -446,15 +446,25 @@ __global__ void __launch_bounds__(256) k_dlam_join(const double* __restrict__ pa
 //     X_in(j + 1) = e^{lam len_j} X_in(j) + X_j            (reverse: towards smaller j)
 //     W_in(j + 1) = e^{lam len_j} (W_in(j) + len_j X_in(j)) + W_j
 // Each segment's state is read and written once; a thread walks 16 bytes, the
-// loads of the next eight segments in flight while it writes these (one value a
-// thread and four loads at a time took 86 us for 37 segments x 16 heads of
-// 128 x 128, which move 78 MB).
+// loads of the next four segments in flight while it writes these.  Both
+// directions of a backward call share a launch.  (One value a thread and four
+// loads at a time: 86 us for 37 segments x 16 heads of 128 x 128, which move 78 MB,
+// now 7.  Eight segments at a time hold so many registers that the many short
+// sequences of a ragged batch wait for a place: 29 us against 17 for 24 sequences x
+// 8 heads; two: 14 us there, but 16 against 13 us for the long backward pass.)
+struct CarryArgs {
+    LinCarry dir[2];
+    int count;
+};
+
 template <typename A, bool DER>
-__global__ void __launch_bounds__(128) k_carry(const __grid_constant__ LinCarry C) {
-    constexpr int VN = 16 / (int)sizeof(A), U = DER ? 4 : 8;
+__global__ void __launch_bounds__(128) k_carry(const __grid_constant__ CarryArgs args) {
+    const LinCarry& C = args.dir[args.count > 1 && blockIdx.x >= gridDim.x / 2];
+    const unsigned bx = args.count > 1 ? blockIdx.x % (gridDim.x / 2) : blockIdx.x;
+    constexpr int VN = 16 / (int)sizeof(A), U = DER ? 2 : 4;
     using V = Pack<A, VN>;
     const int seq = blockIdx.y, h = blockIdx.z;
-    const int64_t e = ((int64_t)blockIdx.x * 128 + threadIdx.x) * VN;
+    const int64_t e = ((int64_t)bx * 128 + threadIdx.x) * VN;
     if (e >= C.len) return;
     const A lam = clamp_lam(static_cast<const A*>(C.lam)[h]);
     const int64_t total = C.S.at(seq + 1) - C.S.at(seq);
@@ -579,17 +589,20 @@ cudaError_t rec_run(laplex_dtype dt, const LinRole& R, const LinSeqs& S, int H, 
     return dt == LAPLEX_F64 ? go(double()) : go(float());
 }
 
-cudaError_t carry_run(laplex_dtype dt, const LinCarry& C, cudaStream_t st) {
-    if (C.S.N == 0 || C.H == 0) return cudaSuccess;
+cudaError_t carry_run(laplex_dtype dt, const LinCarry* C, int count, cudaStream_t st) {
+    if (count == 0 || C->S.N == 0 || C->H == 0) return cudaSuccess;
     // sequences ride in grid.y (at most 65535): the C boundary checks their number
     const int64_t per = 128 * (16 / (int64_t)acc_bytes(dt));  // dk dv is a multiple of 64
-    const dim3 grid((unsigned)((C.len + per - 1) / per), (unsigned)C.S.N, (unsigned)C.H);
+    const dim3 grid((unsigned)((C->len + per - 1) / per * count), (unsigned)C->S.N, (unsigned)C->H);
+    CarryArgs args = {};
+    args.count = count;
+    for (int i = 0; i < count; ++i) args.dir[i] = C[i];
     if (dt == LAPLEX_F64) {
-        if (C.w) k_carry<double, true><<<grid, 128, 0, st>>>(C);
-        else k_carry<double, false><<<grid, 128, 0, st>>>(C);
+        if (C->w) k_carry<double, true><<<grid, 128, 0, st>>>(args);
+        else k_carry<double, false><<<grid, 128, 0, st>>>(args);
     } else {
-        if (C.w) k_carry<float, true><<<grid, 128, 0, st>>>(C);
-        else k_carry<float, false><<<grid, 128, 0, st>>>(C);
+        if (C->w) k_carry<float, true><<<grid, 128, 0, st>>>(args);
+        else k_carry<float, false><<<grid, 128, 0, st>>>(args);
     }
     return cudaGetLastError();
 }
@@ -648,7 +661,7 @@ cudaError_t dlam_run(laplex_dtype dt, LinRole fwd, LinRows dout, LinSeqs S0, int
         C.init = state;
         C.states = base;
         C.w = base + sb;
-        if ((e = carry_run(dt, C, st)) != cudaSuccess) return e;
+        if ((e = carry_run(dt, &C, 1, st)) != cudaSuccess) return e;
         P.R.state_in = base;
         P.R.in_by_slot = 1;
         P.w_in = base + sb;

@@ -180,6 +180,7 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
         : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
     return r;
 }
+__device__ __forceinline__ float2 sub2(float2 x, float2 y) { return fma2(y, make_float2(-1.0f, -1.0f), x); }
 __device__ __forceinline__ float2 pair(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
 
 // 16-bit pairs: a b + c, a b, a b - c, each rounded once
@@ -465,11 +466,10 @@ struct TcBlock {
                 const float f = sh.dec[d] * k_up;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    float2 v = unpack2<T>(q[e]);
-                    v = make_float2(v.x * f, v.y * f);
+                    float2 v = mul2(unpack2<T>(q[e]), make_float2(f, f));
                     a0[e] = pack2<T>(v.x, v.y);
-                    const float2 g = unpack2<T>(a0[e]);
-                    a1[e] = pack2<T>(v.x - g.x, v.y - g.y);
+                    v = sub2(v, unpack2<T>(a0[e]));
+                    a1[e] = pack2<T>(v.x, v.y);
                 }
             } else {
                 // k (f1 + f2): the first part rn(k f1); k f1 less it is exact, and with k f2 gives the second
@@ -494,7 +494,7 @@ struct TcBlock {
 
     // The same in three parts of bf16, what one rounds off going to the next: 2^-24.  The second and third have one
     // buffer, which the U before (the prev-th, or -1) reads: they wait in registers until it is done.
-    // (All of this behind that U: 156 us for the states of 32768 tokens and 16 heads of 128 x 128, 134 with this.)
+    // (All of this behind that U: 156 us for the states of 65536 tokens, 16 heads of 128 x 128, 126 with this.)
     __device__ __forceinline__ bool weigh3(int kv, int n, int tid, int prev) const {
         constexpr int X = DK / 64 * (CH / 32);
         const uint32_t at0 = tile_at(tid >> 3, tid & 7);
@@ -511,14 +511,12 @@ struct TcBlock {
             uint32_t a0[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float2 v = unpack2<T>(in ? q[e] : 0u);
-                v = make_float2(v.x * f, v.y * f);
+                float2 v = mul2(unpack2<T>(in ? q[e] : 0u), make_float2(f, f));
                 a0[e] = pack2<T>(v.x, v.y);
-                float2 g = unpack2<T>(a0[e]);
-                v = make_float2(v.x - g.x, v.y - g.y);
+                v = sub2(v, unpack2<T>(a0[e]));
                 a1[x][e] = pack2<T>(v.x, v.y);
-                g = unpack2<T>(a1[x][e]);
-                a2[x][e] = pack2<T>(v.x - g.x, v.y - g.y);
+                v = sub2(v, unpack2<T>(a1[x][e]));
+                a2[x][e] = pack2<T>(v.x, v.y);
             }
             *reinterpret_cast<uint4*>(Ks + at) = make_uint4(a0[0], a0[1], a0[2], a0[3]);
         }
@@ -687,7 +685,11 @@ struct TcBlock {
                 tmem_ld16(St + b, s);
                 tmem_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) s[j] = __float_as_uint(fmaf(unit, __uint_as_float(r[j]), __uint_as_float(s[j])));
+                for (int j = 0; j < 16; j += 2) {
+                    const float2 x = fma2(make_float2(unit, unit), pair(r[j], r[j + 1]), pair(s[j], s[j + 1]));
+                    s[j] = __float_as_uint(x.x);
+                    s[j + 1] = __float_as_uint(x.y);
+                }
                 __syncwarp();
                 tmem_st16(St + b, s);
             }

@@ -94,7 +94,7 @@ struct LinCarry {
 int rec_segment(int64_t T, int N, int H, int dv, bool equal);
 cudaError_t rec_run(laplex_dtype dt, const LinRole& R, const LinSeqs& S, int H, const void* lam, bool state_only,
                     cudaStream_t st);
-cudaError_t carry_run(laplex_dtype dt, const LinCarry& C, cudaStream_t st);
+cudaError_t carry_run(laplex_dtype dt, const LinCarry* C, int count, cudaStream_t st);  // up to two directions
 // dlam[h] = sum over the sequences of scale <do_t, W_t^T q_t> (+ <dstate, W_last>)
 size_t dlam_ws_bytes(laplex_dtype dt, int64_t T, int N, int Hkv, int dk, int dv, bool equal);
 cudaError_t dlam_run(laplex_dtype dt, LinRole fwd, LinRows dout, LinSeqs S, int H, const void* lam,
