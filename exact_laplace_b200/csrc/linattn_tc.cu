@@ -1038,7 +1038,8 @@ __global__ void __launch_bounds__(TcSize<DK, DV, OUT>::NT,
     // would sink all of them, so a power of two goes from g1 into the state's unit.
     float g1 = R.sk * (rev ? exp2f(l2) : 1.0f), up1 = 1.0f;
     if (std::is_same<T, __half>::value) {
-        const int e = (int)(__float_as_uint(g1) >> 23 & 255) - 127;
+        const float most = g1 * exp2f(fmaxf(l2, 0.0f) * (float)(TC_C - 1));  // (a positive lam: they grow)
+        const int e = (int)(__float_as_uint(most) >> 23 & 255) - 127;
         up1 = __uint_as_float((uint32_t)(127 - min(max(e, -40), 40)) << 23);
         g1 *= up1;
     }

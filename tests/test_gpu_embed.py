@@ -166,3 +166,56 @@ def test_empty():
     g = torch.empty((0, 16), device="cuda")
     assert torch.all(X.embed_backward(none, g, 5) == 0)
     assert X.embed_backward(none, g, 0).shape == (0, 16)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_tokens_past_32_bits_are_outside(dt):
+    table = values((40, 64), DT[dt], 1)
+    t = torch.tensor([3, 2 ** 32 + 3, -2 ** 32 + 3, 2 ** 63 - 1, -2 ** 63, 39, 40], dtype=torch.int64, device="cuda")
+    out = X.embed(table, t)
+    want = torch.zeros_like(out)
+    want[0], want[5] = table[3], table[39]
+    assert torch.equal(out, want)
+    g = values((7, 64), DT[dt], 2)
+    d = X.embed_backward(t, g, 40)
+    want = torch.zeros_like(table)
+    want[3], want[39] = g[0], g[5]
+    assert torch.equal(d, want)
+
+
+def test_table_past_32_bits():
+    rows, dim = (1 << 21) + 5, 1032  # 2.16e9 elements
+    if torch.cuda.mem_get_info()[0] < 4 * rows * dim * 2:
+        pytest.skip("not enough memory")
+    table = torch.empty(rows, dim, dtype=torch.bfloat16, device="cuda")
+    t = torch.tensor([rows - 1, 0, rows - 3, rows - 1], dtype=torch.int32, device="cuda")
+    x = values((3, dim), torch.bfloat16, 3)
+    table[[rows - 1, 0, rows - 3]] = x
+    assert torch.equal(X.embed(table, t), x[[0, 1, 2, 0]])
+    table.fill_(1.0)
+    d = X.embed_backward(t, x[[0, 1, 2, 0]], rows, out=table)
+    assert torch.equal(d[rows - 1], 2 * x[0]) and torch.equal(d[0], x[1]) and torch.equal(d[rows - 3], x[2])
+    assert int(torch.count_nonzero(d.view(-1)[:(1 << 20) * dim])) == int(torch.count_nonzero(x[1]))
+    assert int(torch.count_nonzero(d[1 << 20:])) == int(torch.count_nonzero(x[0]) + torch.count_nonzero(x[2]))
+
+
+def test_two_streams_and_two_graphs():
+    a = (torch.from_numpy(tokens("zipf", 5000, 700)).cuda(), values((5000, 72), torch.bfloat16, 4), 700)
+    b = (torch.from_numpy(tokens("uniform", 90000, 4000)).cuda(), values((90000, 8), torch.bfloat16, 5), 4000)
+    want = [X.embed_backward(*x) for x in (a, b)]
+    streams, graphs, res = [torch.cuda.Stream(), torch.cuda.Stream()], [], []
+    for x in (a, b):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res.append(X.embed_backward(*x))
+        graphs.append(g)
+    for _ in range(3):
+        eager = []
+        for st, g, x in zip(streams, graphs, (b, a)):
+            st.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(st):
+                g.replay()
+                eager.append(X.embed_backward(*x))
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, res))
+        assert all(torch.equal(x, y) for x, y in zip(want, eager[::-1]))

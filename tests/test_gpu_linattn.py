@@ -84,14 +84,14 @@ class Case:
         q, k, v, _, s0, _ = self.host()
         a = self.host(True)
         return (seq.linattn(q, k, v, lam, self.scale, self.lens, s0),
-                seq.linattn(a[0], a[1], a[2], lam, self.scale, self.lens, a[4]))
+                seq.linattn(a[0], a[1], a[2], lam, abs(self.scale), self.lens, a[4]))
 
     def backward_ref(self):
         lam = np64(self.lam)
         q, k, v, do, s0, ds = self.host()
         a = self.host(True)
         return (seq.linattn_backward(q, k, v, lam, do, self.scale, self.lens, s0, ds),
-                seq.linattn_backward(a[0], a[1], a[2], lam, a[3], self.scale, self.lens, a[4], a[5]))
+                seq.linattn_backward(a[0], a[1], a[2], lam, a[3], abs(self.scale), self.lens, a[4], a[5]))
 
     def used(self):
         return slice(0, sum(self.lens))
@@ -438,3 +438,176 @@ def test_tokens_to_gradients(dt):
         ro, _ = seq.linattn(full, full, full, np64(lam), d ** -0.5, [72])
         no, _ = seq.linattn(abs(full), abs(full), abs(full), np64(lam), d ** -0.5, [72])
         check(on[at], ro[70:], no[70:], tol_rows(dt), "continued")
+
+
+# ----------------------------------------------------------------------------- calls at the edges
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("hq,hkv", [(32, 1), (24, 2), (34, 2)])
+def test_large_groups(dt, hq, hkv):
+    c = Case(dt, [150, 61], hq, hkv, 64, 32)
+    c.check_forward(*c.run_forward())
+    c.check_backward(c.run_backward(return_dlog_decay=True))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+def test_states_that_grow(dt):
+    # e^{0.01 * 400} = 55: a positive log decay is a growth
+    c = Case(dt, [400, 33], 2, 2, 64, 64, lam=[0.01, 0.002])
+    c.check_forward(*c.run_forward())
+    c.check_backward(c.run_backward())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("scale", [0.0, -2.0, 1e-6])
+def test_scales(dt, scale):
+    c = Case(dt, [300, 20], 2, 1, 64, 72, state=False)
+    c.scale = scale
+    if dt == "fp16" and scale == 1e-6:  # outputs in fp16's subnormal range: rounded on its grid of 2^-24
+        o, _ = c.run_forward()
+        (ro, _), (no, _) = c.forward_ref()
+        assert np.max(np.abs(np64(o) - ro) - tol_rows(dt) * no) <= 2.0 ** -24
+        return
+    c.check_forward(*c.run_forward())
+    c.check_backward(c.run_backward())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_many_sequences(dt):
+    lens = [0] * 65535
+    for i in range(0, len(lens), 7):
+        lens[i] = i % 3 + 1
+    c = Case(dt, lens, 1, 1, 8, 8, state=False)
+    c.check_forward(*c.run_forward())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_many_heads(dt):
+    c = Case(dt, [40, 9], 300, 300, 16, 8, lam=[-0.01 * (i % 40) for i in range(300)])
+    c.check_forward(*c.run_forward())
+    c.check_backward(c.run_backward(return_dlog_decay=True))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32", "fp64"])
+def test_no_tokens(dt):
+    c = Case(dt, [0, 0, 0], 2, 1, 64, 64)
+    o, end = c.run_forward()
+    assert o.shape == (0, 2, 64) and torch.equal(end, c.s0)
+    g = c.run_backward(return_dlog_decay=True)
+    # no token: the state goes through as it came (e^lam R_0 with R_0 = e^-lam dstate)
+    assert torch.equal(g.dstate, c.ds)
+    assert torch.equal(g.dlog_decay, torch.zeros_like(g.dlog_decay))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_offsets_past_32_bits(dt):
+    # rows 2^28 elements apart: the tenth starts past 2^31 elements
+    ts, n = (1 << 28) + 64, 10
+    c = Case(dt, [n], 1, 1, 64, 64)
+    if torch.cuda.mem_get_info()[0] < 3 * n * ts * c.q.element_size():
+        pytest.skip("not enough memory")
+    far = []
+    for x in (c.q, c.k):
+        buf = torch.empty(n * ts, dtype=x.dtype, device="cuda")
+        y = buf.as_strided((n, 1, 64), (ts, 64, 1))
+        y.copy_(x)
+        far.append(y)
+    c.q, c.k = far
+    c.check_forward(*c.run_forward())
+    c.check_backward(c.run_backward())
+    one = slice(n - 1, n)
+    states = c.s0.clone()
+    o = X.linattn_step(c.q[one], c.k[one], c.v[one], c.lam, states, scale=c.scale)
+    ro, _ = seq.linattn(np64(c.q)[one], np64(c.k)[one], np64(c.v)[one], np64(c.lam), c.scale, [1], np64(c.s0))
+    no, _ = seq.linattn(abs(np64(c.q)[one]), abs(np64(c.k)[one]), abs(np64(c.v)[one]), np64(c.lam), c.scale, [1],
+                        abs(np64(c.s0)))
+    check(o, ro, no, tol_rows(dt), "step")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+def test_graph_replayed_with_other_lengths(dt):
+    """Lengths are read on the device: a captured call serves every packing of its
+    tokens, cut into segments or not."""
+    lens = [[1500, 200, 0, 1300], [0, 3000, 0, 0], [1, 999, 1000, 1000], [40, 50, 60, 70]]
+    c = Case(dt, lens[0], 2, 1, 64, 64)
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        c.run_forward(), c.run_backward()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        res = (c.run_forward(), c.run_backward(return_dlog_decay=True))
+    for x in lens:
+        c.lens = x
+        c.cu.copy_(torch.tensor(np.concatenate([[0], np.cumsum(x)]), dtype=torch.int32))
+        for t in (c.q, c.k, c.v, c.do):
+            t.normal_()
+        g.replay()
+        torch.cuda.synchronize()
+        c.check_forward(*res[0])
+        c.check_backward(res[1])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("bounds", [[0, 900, 300, 700], [5, -7, 2000, 640], [700, 700, 0, 700], [0, 2 ** 31 - 1, -2 ** 31, 9]],
+                         ids=str)
+def test_bounds_that_do_not_ascend_stay_inside(dt, bounds):
+    """Unspecified results, but nothing outside the tensors is written, and the
+    device stays usable."""
+    t, pad = 700, 64
+    c = Case(dt, [300, 300, 100], 2, 1, 64, 64)
+    c.cu = torch.tensor(bounds, dtype=torch.int32).cuda()
+    whole = torch.full((t + 2 * pad, 2, 64), 7.0, dtype=DT[dt], device="cuda")
+    out = whole[pad:pad + t]
+    X.linattn(c.q, c.k, c.v, c.lam, cu_seqlens=c.cu, state=c.s0, return_state=True, out=out)
+    c.run_backward(return_dlog_decay=True)
+    torch.cuda.synchronize()
+    assert bool((whole[:pad] == 7).all()) and bool((whole[pad + t:] == 7).all())
+    X.device_status()
+    d = Case(dt, [300, 300, 100], 2, 1, 64, 64)
+    d.check_forward(*d.run_forward())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
+def test_nan_decay_stays_in_its_head(dt):
+    c = Case(dt, [200], 2, 2, 64, 64, lam=[-0.1, float("nan")])
+    o, end = c.run_forward()
+    d = Case(dt, [200], 2, 2, 64, 64, lam=[-0.1, -0.1])
+    o2, end2 = d.run_forward()
+    assert torch.equal(o[:, 0], o2[:, 0]) and torch.equal(end[:, 0], end2[:, 0])
+    assert bool(torch.isnan(end[:, 1]).all())
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp64"])
+def test_differences(dt):
+    """The gradients against central differences of the fp64 forward call on the
+    same values, along one direction of each input, over several segments."""
+    c = Case(dt, [1200, 40], 2, 1, 16, 24)
+    w = Case("fp64", [1200, 40], 2, 1, 16, 24)
+    w.q, w.k, w.v, w.do = (x.double() for x in (c.q, c.k, c.v, c.do))
+    w.lam, w.s0, w.ds = c.lam.double(), c.s0.double(), c.ds.double()
+    g = c.run_backward(return_dlog_decay=True)
+
+    def loss():
+        o, end = w.run_forward()
+        return float((o * w.do).sum() + (end * w.ds).sum())
+
+    _, n = w.backward_ref()
+    for x, grad, name in ((w.q, g.dq, "dq"), (w.k, g.dk, "dk"), (w.v, g.dv, "dv"), (w.s0, g.dstate, "dstate"),
+                          (w.lam, g.dlog_decay, "dlam")):
+        step = torch.randn(x.shape, dtype=torch.float64, generator=torch.Generator().manual_seed(5)).cuda()
+        h = 1e-4 if name == "dlam" else 1e-2
+        keep = x.clone()
+        x.copy_(keep + h * step)
+        up = loss()
+        x.copy_(keep - h * step)
+        down = loss()
+        x.copy_(keep)
+        mine = float((grad.double() * step).sum())
+        size = float((torch.from_numpy(n[name]).cuda() * step.abs()).sum())
+        # The loss is linear in all but lam: the difference is exact up to fp64's rounding.  In lam it is off by
+        # (h step)^2 / 6 of the third derivative, whose terms are d^2 times the first's: with e^{-d / 2}
+        # sum d^3 / sum d = 24, so 4 (h step)^2, and |step| <= 2.
+        assert float(step.abs().max()) <= 2 or name != "dlam"
+        tol = (tol_rows(dt) if name in ("dq", "dk", "dv") else tol_acc(dt)) + (16 * h * h if name == "dlam" else 1e-9)
+        assert abs((up - down) / (2 * h) - mine) <= tol * size, (name, (up - down) / (2 * h), mine, size)
