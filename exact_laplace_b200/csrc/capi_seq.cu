@@ -156,13 +156,22 @@ lx::LinRole role(lx::LinRows q, lx::LinRows k, lx::LinRows v, int nq, int nk, in
     return R;
 }
 
-// The products of roles[0 .. count), or the segments' own states alone.
-cudaError_t run(const laplex_linattn_shape& s, const lx::LinRole* roles, int count, const lx::LinSeqs& S,
-                bool state_only, uint32_t* status, cudaStream_t st) {
-    if (tensor_cores(s)) return lx::tc_run(s.dtype, roles, count, S, s.hkv, s.log_decay, state_only, status, st);
+// The products of roles[0 .. count).  `last`: also the states behind the last tokens, by their own pass.
+cudaError_t run(const laplex_linattn_shape& s, const lx::LinRole* roles, int count, const lx::LinRole* last,
+                const lx::LinSeqs& S, uint32_t* status, cudaStream_t st) {
+    if (tensor_cores(s)) return lx::tc_run(s.dtype, roles, count, last, S, s.hkv, s.log_decay, status, st);
     cudaError_t e = cudaSuccess;
-    for (int i = 0; i < count && e == cudaSuccess; ++i)
-        e = lx::rec_run(s.dtype, roles[i], S, s.hkv, s.log_decay, state_only, st);
+    for (int i = 0; i < count && e == cudaSuccess; ++i) e = lx::rec_run(s.dtype, roles[i], S, s.hkv, s.log_decay, false, st);
+    if (e == cudaSuccess && last) e = lx::rec_run(s.dtype, *last, S, s.hkv, s.log_decay, true, st);
+    return e;
+}
+
+// The segments' own states alone.
+cudaError_t run_states(const laplex_linattn_shape& s, const lx::LinRole* roles, int count, const lx::LinSeqs& S,
+                       uint32_t* status, cudaStream_t st) {
+    if (tensor_cores(s)) return lx::tc_states(s.dtype, roles, count, S, s.hkv, s.log_decay, status, st);
+    cudaError_t e = cudaSuccess;
+    for (int i = 0; i < count && e == cudaSuccess; ++i) e = lx::rec_run(s.dtype, roles[i], S, s.hkv, s.log_decay, true, st);
     return e;
 }
 
@@ -184,7 +193,7 @@ cudaError_t segment_states(const laplex_linattn_shape& s, Direction* D, int coun
         R[i].skip_last = D[i].last == nullptr;
         R[i].o = nullptr;
     }
-    cudaError_t e = run(s, R, count, S, true, status, st);
+    cudaError_t e = run_states(s, R, count, S, status, st);
     lx::LinCarry C[2] = {};
     for (int i = 0; i < count; ++i) {
         C[i].S = S;
@@ -248,8 +257,7 @@ laplex_status laplex_linattn(const laplex_linattn_shape* shape, const laplex_row
     const bool apart = tensor_cores(s) && R.state_out;
     lx::LinRole P = R;
     if (apart) P.state_out = nullptr;
-    if (e == cudaSuccess) e = run(s, &P, 1, S, false, status, st);
-    if (e == cudaSuccess && apart) e = run(s, &R, 1, S, true, status, st);
+    if (e == cudaSuccess) e = run(s, &P, 1, apart ? &R : nullptr, S, status, st);
     return done(e, "laplex_linattn");
 }
 
@@ -328,11 +336,8 @@ laplex_status laplex_linattn_backward(const laplex_linattn_shape* shape, const l
         out(&Rv, rdv);
         roles[count++] = Rv;
     }
-    e = run(s, roles, count, S, false, status, st);
-    if (e == cudaSuccess && apart) {
-        Rv.state_out = dstate_in;
-        e = run(s, &Rv, 1, S, true, status, st);
-    }
+    Rv.state_out = dstate_in;
+    e = run(s, roles, count, apart ? &Rv : nullptr, S, status, st);
     return done(e, "laplex_linattn_backward");
 }
 

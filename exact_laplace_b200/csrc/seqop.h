@@ -100,10 +100,13 @@ size_t dlam_ws_bytes(laplex_dtype dt, int64_t T, int N, int Hkv, int dk, int dv,
 cudaError_t dlam_run(laplex_dtype dt, LinRole fwd, LinRows dout, LinSeqs S, int H, const void* lam,
                      const void* state, const void* dstate, void* dlam, void* ws, size_t ws_bytes, cudaStream_t st);
 
-// ---- 16-bit rows on the tensor cores (linattn_tc.cu): up to three products at a time
+// ---- 16-bit rows on the tensor cores (linattn_tc.cu): up to three products at a time and, with
+// them, the states behind the last tokens (`last`, or NULL); states of segments, two directions at a time
 int tc_segment(int64_t T, int N, int H, int roles, bool equal);
-cudaError_t tc_run(laplex_dtype dt, const LinRole* roles, int count, const LinSeqs& S, int H, const void* lam,
-                   bool state_only, uint32_t* status, cudaStream_t st);
+cudaError_t tc_run(laplex_dtype dt, const LinRole* roles, int count, const LinRole* last, const LinSeqs& S, int H,
+                   const void* lam, uint32_t* status, cudaStream_t st);
+cudaError_t tc_states(laplex_dtype dt, const LinRole* roles, int count, const LinSeqs& S, int H, const void* lam,
+                      uint32_t* status, cudaStream_t st);
 
 // ---- single tokens (linattn_step.cu)
 struct LinStep {

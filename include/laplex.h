@@ -403,7 +403,11 @@ laplex_status laplex_matvec_sym_noalloc(const float* sorted, const int32_t* perm
  *    gradients are float, double for LAPLEX_F64, contiguous; a state is [dk, dv].
  *    16-bit rows: products of 16-bit values summed in fp32; inside a block of
  *    tokens the weights e^{lam (t - s)} <q_t, k_s> and the state that q_t reads
- *    are rounded once to the rows' type, the states are not.
+ *    are rounded once to the rows' type (fp16: times a power of two that keeps
+ *    them in its range); the states that go on and leave are fp32.  Long
+ *    sequences are cut into segments by a rule on the sizes and on whether
+ *    cu_seqlens is NULL, so the last bits of a result may differ between the two
+ *    ways to pass the same lengths.  The same call gives the same bits.
  *  - Tokens are packed: sequence n owns rows cu_seqlens[n] .. cu_seqlens[n+1]-1
  *    (int32 on the device, ascending, cu_seqlens[0] = 0, at most `tokens`);
  *    cu_seqlens NULL: `seqs` sequences of tokens / seqs rows each.  A sequence
@@ -415,8 +419,13 @@ laplex_status laplex_matvec_sym_noalloc(const float* sorted, const int32_t* perm
  *  - Strides are in elements and at least dim; rows start on 16 bytes.  Integer
  *    arrays need only the alignment of their elements.
  *  - A token never reaches an earlier output: NaN and Inf in row s of k or v
- *    leave the rows t < s of o as they are.
- *  - log_decay = -Inf keeps no past (S_t = k_t v_t^T).
+ *    leave the rows t < s of o as they are.  Of the rows t >= s they may make
+ *    any NaN (with 16-bit rows also where the definition gives Inf).
+ *  - log_decay = -Inf keeps no past (S_t = k_t v_t^T).  A positive log decay
+ *    lets states grow; e^{lam L} over a sequence of L tokens, and 128 lam, must
+ *    stay in the range of the accumulators (fp16 rows: lam at most 0.1).
+ *  - Outputs overlap neither inputs nor other outputs, except where a call says
+ *    so.
  * ------------------------------------------------------------------------ */
 
 /* Rows ptr + token * token_stride + head * head_stride (elements). */
@@ -470,6 +479,7 @@ laplex_status laplex_linattn(const laplex_linattn_shape* shape, const laplex_row
  *   state_in, dstate_out: NULL means 0.
  *   dq, dk, dv, dstate_in, dlog_decay: out, each may be NULL (not computed).
  * The gradient of the decay runs as a recurrence in fp32 (fp64) for every type.
+ * dstate_in is neither state_in nor dstate_out (refused).
  */
 laplex_status laplex_linattn_backward(const laplex_linattn_shape* shape, const laplex_rows* q, const laplex_rows* k,
                                       const laplex_rows* v, const laplex_rows* dout, const void* state_in,
@@ -495,7 +505,7 @@ laplex_status laplex_linattn_step(const laplex_linattn_shape* shape, const laple
  * Embedding lookup: the product with the routing [a_i == b_j], the kernel's
  * limit of small temperature (summary §2.1), b the rows' numbers.
  *   out_i = scale table[tokens_i] (computed in fp32, rounded once), a row of
- *   zeros for a token outside [0, rows) (padding).
+ *   zeros for a token outside [0, rows) (padding), any int64 among them.
  *   tokens [n]: int32 or int64 (token_bytes 4 or 8).  table [rows, ld], out [n, out_ld].
  */
 laplex_status laplex_embed(const void* table, int64_t ld, int64_t rows, int64_t dim, const void* tokens,
@@ -507,11 +517,11 @@ laplex_status laplex_embed_backward_workspace_size(int64_t n, int64_t rows, int6
                                                    size_t* bytes);
 
 /*
- * Its gradient, by sorting the tokens (the stable digit passes of
- * laplex_sort_anchors) and summing runs:
+ * Its gradient, by sorting the tokens (up to 65536 by one thread-block cluster,
+ * more by the stable digit passes of laplex_sort_anchors) and summing runs:
  *   dtable_r = scale sum over {i : tokens_i = r} of g_i
- * summed in fp32 (fp64) in a fixed order of ascending i: the result does not
- * vary from run to run.  Every row of dtable is written (0 where no token
+ * summed in fp32 (fp64) in a fixed order (ascending i; long runs in parts): the
+ * result does not vary from run to run.  Every row of dtable is written (0 where no token
  * names it); with accumulate != 0 the sums are added to dtable instead, and
  * rows without a token are left as they are.
  *   g [n, g_ld] of dtype; dtable [rows, ld] of out_dtype, dtype itself or LAPLEX_F32.
