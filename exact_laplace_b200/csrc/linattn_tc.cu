@@ -100,6 +100,7 @@ struct TcShared {
     uint64_t v_ready[2], k_ready[2], s_ready;          // from the state warps
     uint64_t p_ready, o_read;                          // from the rows warps
     uint64_t k_max, s_max, p_max[4];                   // fp16: maxima exchanged among the state warps, in a pair of rows warps
+    uint64_t drain;      // after a wait that ran out
     uint32_t tmem;
     uint32_t dead;       // a wait ran out
     alignas(16) float grow[16];  // e^{lam j}, 16 columns of P towards the row's end
@@ -1021,7 +1022,7 @@ __device__ __forceinline__ void lin_block(const TcArgs& A, int block, unsigned c
     }
     constexpr int ISSUE = (OUT ? 2 : 1) * TC_GROUP / 32;  // the issuing warp
     if (tid == 0) {
-        for (uint64_t* b : {&sh.kv_full[0], &sh.kv_full[1], &sh.q_full, &sh.p_done, &sh.k_free, &sh.o2_done, &sh.o_done, &sh.u_done[0], &sh.u_done[1]})
+        for (uint64_t* b : {&sh.kv_full[0], &sh.kv_full[1], &sh.q_full, &sh.p_done, &sh.k_free, &sh.o2_done, &sh.o_done, &sh.u_done[0], &sh.u_done[1], &sh.drain})
             mbar_init(b, 1);
         for (uint64_t* b : {&sh.v_ready[0], &sh.v_ready[1], &sh.k_ready[0], &sh.k_ready[1], &sh.s_ready, &sh.p_ready, &sh.o_read, &sh.k_max, &sh.s_max})
             mbar_init(b, TC_GROUP / 32);
@@ -1079,11 +1080,17 @@ __device__ __forceinline__ void lin_block(const TcArgs& A, int block, unsigned c
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (sh.dead && tid == 0) {
-        // a copy or a product did not come: report it, and let the copies in flight land
-        set_status(A.status, ST_TIMEOUT);
-        for (uint64_t& b : sh.kv_full) mbar_wait(&b, 0);
-        mbar_wait(&sh.q_full, 0);
+    if (sh.dead) {
+        // a copy or a product did not come: report it, and let those in flight end (within a bound; a phase is
+        // named by its parity, so both are waited for, and one of them may not come)
+        if (tid / 32 == ISSUE) B.commit(&sh.drain);
+        if (tid == 0) {
+            set_status(A.status, ST_TIMEOUT);
+            for (uint64_t* b : {&sh.kv_full[0], &sh.kv_full[1], &sh.q_full})
+                for (uint32_t parity = 0; parity < 2; ++parity) mbar_wait(b, parity);
+            mbar_wait(&sh.drain, 0);
+        }
+        __syncthreads();
     }
     if (tid / 32 == ISSUE) {
         tc_fence_after();
