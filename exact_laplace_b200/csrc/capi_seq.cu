@@ -158,11 +158,12 @@ lx::LinRole role(lx::LinRows q, lx::LinRows k, lx::LinRows v, int nq, int nk, in
 
 // The products of roles[0 .. count).  `last`: also the states behind the last tokens, by their own pass.
 cudaError_t run(const laplex_linattn_shape& s, const lx::LinRole* roles, int count, const lx::LinRole* last,
-                const lx::LinSeqs& S, uint32_t* status, cudaStream_t st) {
-    if (tensor_cores(s)) return lx::tc_run(s.dtype, roles, count, last, S, s.hkv, s.log_decay, status, st);
+                const lx::LinSeqs& S, uint32_t* status, bool next, cudaStream_t st) {
+    if (tensor_cores(s)) return lx::tc_run(s.dtype, roles, count, last, S, s.hkv, s.log_decay, status, next, st);
     cudaError_t e = cudaSuccess;
-    for (int i = 0; i < count && e == cudaSuccess; ++i) e = lx::rec_run(s.dtype, roles[i], S, s.hkv, s.log_decay, false, st);
-    if (e == cudaSuccess && last) e = lx::rec_run(s.dtype, *last, S, s.hkv, s.log_decay, true, st);
+    for (int i = 0; i < count && e == cudaSuccess; ++i)
+        e = lx::rec_run(s.dtype, roles[i], S, s.hkv, s.log_decay, false, next || i > 0, st);
+    if (e == cudaSuccess && last) e = lx::rec_run(s.dtype, *last, S, s.hkv, s.log_decay, true, next || count > 0, st);
     return e;
 }
 
@@ -171,7 +172,7 @@ cudaError_t run_states(const laplex_linattn_shape& s, const lx::LinRole* roles, 
                        uint32_t* status, cudaStream_t st) {
     if (tensor_cores(s)) return lx::tc_states(s.dtype, roles, count, S, s.hkv, s.log_decay, status, st);
     cudaError_t e = cudaSuccess;
-    for (int i = 0; i < count && e == cudaSuccess; ++i) e = lx::rec_run(s.dtype, roles[i], S, s.hkv, s.log_decay, true, st);
+    for (int i = 0; i < count && e == cudaSuccess; ++i) e = lx::rec_run(s.dtype, roles[i], S, s.hkv, s.log_decay, true, i > 0, st);
     return e;
 }
 
@@ -257,7 +258,7 @@ laplex_status laplex_linattn(const laplex_linattn_shape* shape, const laplex_row
     const bool apart = tensor_cores(s) && R.state_out;
     lx::LinRole P = R;
     if (apart) P.state_out = nullptr;
-    if (e == cudaSuccess) e = run(s, &P, 1, apart ? &R : nullptr, S, status, st);
+    if (e == cudaSuccess) e = run(s, &P, 1, apart ? &R : nullptr, S, status, R.in_by_slot, st);
     return done(e, "laplex_linattn");
 }
 
@@ -337,7 +338,7 @@ laplex_status laplex_linattn_backward(const laplex_linattn_shape* shape, const l
         roles[count++] = Rv;
     }
     Rv.state_out = dstate_in;
-    e = run(s, roles, count, apart ? &Rv : nullptr, S, status, st);
+    e = run(s, roles, count, apart ? &Rv : nullptr, S, status, cut, st);
     return done(e, "laplex_linattn_backward");
 }
 

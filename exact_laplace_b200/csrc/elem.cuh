@@ -26,6 +26,15 @@ template <typename T> struct VecOf { static constexpr int N = 16 / (int)sizeof(T
 // N elements of T, moved in accesses of at most 16 bytes
 template <typename T, int N> struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack { T v[N]; };
 
+// The kernels of one call follow one another by programmatic launches (launch_next):
+// a kernel is placed on the SMs while the last blocks of the one before still run.
+// Its first statement waits for that kernel's end and its writes; then the next one
+// may be placed.  (Without such a launch before or after, both do nothing.)
+__device__ __forceinline__ void after_previous() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // e^(lam d): lam is a log decay; -inf (no memory) acts as a decay that no d >= 1
 // survives, without the NaN of -inf * 0.  fp32: what the product lam d rounds off
 // (2^-24 of it, so 1e-6 of the result at lam d = 16) is put back.

@@ -164,6 +164,7 @@ __device__ __forceinline__ void st_remote(uint32_t a, uint2 v) {
 __global__ void __launch_bounds__(TS_NT) k_token_sort(const __grid_constant__ TokenSort P) {
     extern __shared__ __align__(16) unsigned char raw[];
     TokenSortShared& sh = *reinterpret_cast<TokenSortShared*>(raw);
+    after_previous();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int me = blockIdx.x, blocks = gridDim.x;  // the grid is one cluster
     const int lo = me << P.shift, count = max(0, min(1 << P.shift, P.n - lo));
@@ -392,6 +393,7 @@ __global__ void __launch_bounds__(SUM_NT) k_embed_sum(const __grid_constant__ Em
     constexpr bool RING = VN > 1;
     constexpr int NW = SUM_NT / 32;
     extern __shared__ __align__(16) unsigned char raw[];
+    after_previous();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const EmbedArgs& E = P.A;
     // the zeroing blocks lie evenly between the others: block b is the (b zero / all)-th of them
@@ -508,6 +510,7 @@ __global__ void __launch_bounds__(EMB_NT) k_embed_join(const __grid_constant__ E
     using A = typename AccOf<T>::A;
     constexpr int NW = EMB_NT / 32;
     __shared__ __align__(16) A red[NW][32 * VN];
+    after_previous();
     const EmbedArgs& E = P.A;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // this block's tiles: those of blockIdx.x + t gridDim.x that a long run leaves which began in them
@@ -606,7 +609,7 @@ size_t embed_bwd_ws_bytes(int64_t n, int64_t rows, int64_t dim, laplex_dtype dt)
 }
 
 template <typename T, typename W>
-static cudaError_t embed_sum_launch(EmbedSum S, int sms, cudaStream_t st) {
+static cudaError_t embed_sum_launch(EmbedSum S, int sms, bool sorted, cudaStream_t st) {
     constexpr int VN = VecOf<T>::N;
     const bool vec = vec_ok(S.A, VN, sizeof(T), sizeof(W), std::min<int>(16, VN * sizeof(W)));
     const int64_t cols = (S.A.dim + 32 * (vec ? VN : 1) - 1) / (32 * (vec ? VN : 1));
@@ -620,18 +623,19 @@ static cudaError_t embed_sum_launch(EmbedSum S, int sms, cudaStream_t st) {
         cudaError_t e = current_device_sms(&dev, &n);
         if (e == cudaSuccess) e = blocks_per_sm<&k_embed_sum<T, W, VN>>(dev, SUM_NT, ring, &per);
         if (e != cudaSuccess) return e;
-        if (vec) k_embed_sum<T, W, VN><<<(unsigned)grid, SUM_NT, ring, st>>>(S);
-        else k_embed_sum<T, W, 1><<<(unsigned)grid, SUM_NT, 0, st>>>(S);
+        e = vec ? launch(sorted, k_embed_sum<T, W, VN>, (unsigned)grid, SUM_NT, ring, st, S)
+                : launch(sorted, k_embed_sum<T, W, 1>, (unsigned)grid, SUM_NT, 0, st, S);
+        if (e != cudaSuccess) return e;
     }
     if (S.tiles > 1) {
         constexpr int JN = 16 / (int)sizeof(typename AccOf<T>::A);
         const bool jvec = S.A.dim % JN == 0;
         const int64_t jcols = (S.A.dim + 32 * (jvec ? JN : 1) - 1) / (32 * (jvec ? JN : 1));
         const dim3 jg((unsigned)std::min<int64_t>(S.tiles - 1, 2 * (int64_t)sms), (unsigned)std::min<int64_t>(jcols, 8));
-        if (jvec) k_embed_join<T, W, JN><<<jg, EMB_NT, 0, st>>>(S);
-        else k_embed_join<T, W, 1><<<jg, EMB_NT, 0, st>>>(S);
+        return jvec ? launch(true, k_embed_join<T, W, JN>, jg, EMB_NT, 0, st, S)
+                    : launch(true, k_embed_join<T, W, 1>, jg, EMB_NT, 0, st, S);
     }
-    return cudaGetLastError();
+    return cudaSuccess;
 }
 
 cudaError_t embed_bwd_run(laplex_dtype dt, laplex_dtype out_dt, const EmbedArgs& A, void* ws, size_t ws_bytes,
@@ -650,7 +654,8 @@ cudaError_t embed_bwd_run(laplex_dtype dt, laplex_dtype out_dt, const EmbedArgs&
     void* part = p += Z.seen;
     void* sort = p += Z.part;
     uint32_t* bits = A.accumulate ? nullptr : seen;
-    if (A.n > 0 && A.n <= TS_MAX) {
+    const bool sorted = A.n > 0 && A.n <= TS_MAX;  // by a kernel of this call
+    if (sorted) {
         e = token_sort(A, skeys, perm, bits, st);
         if (e != cudaSuccess) return e;
     } else {
@@ -674,12 +679,12 @@ cudaError_t embed_bwd_run(laplex_dtype dt, laplex_dtype out_dt, const EmbedArgs&
     S.sum_blocks = S.zero_blocks = 0;
     const bool f32 = out_dt == LAPLEX_F32;
     switch (dt) {
-        case LAPLEX_F32: return embed_sum_launch<float, float>(S, sms, st);
-        case LAPLEX_F64: return embed_sum_launch<double, double>(S, sms, st);
-        case LAPLEX_F16: return f32 ? embed_sum_launch<__half, float>(S, sms, st) : embed_sum_launch<__half, __half>(S, sms, st);
+        case LAPLEX_F32: return embed_sum_launch<float, float>(S, sms, sorted, st);
+        case LAPLEX_F64: return embed_sum_launch<double, double>(S, sms, sorted, st);
+        case LAPLEX_F16: return f32 ? embed_sum_launch<__half, float>(S, sms, sorted, st) : embed_sum_launch<__half, __half>(S, sms, sorted, st);
         case LAPLEX_BF16:
-            return f32 ? embed_sum_launch<__nv_bfloat16, float>(S, sms, st)
-                       : embed_sum_launch<__nv_bfloat16, __nv_bfloat16>(S, sms, st);
+            return f32 ? embed_sum_launch<__nv_bfloat16, float>(S, sms, sorted, st)
+                       : embed_sum_launch<__nv_bfloat16, __nv_bfloat16>(S, sms, sorted, st);
     }
     return cudaErrorInvalidValue;
 }

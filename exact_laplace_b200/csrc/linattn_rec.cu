@@ -192,6 +192,7 @@ __device__ __forceinline__ void rec_reduce(const A (&p)[U][4], const A* wq, A* o
 template <typename T, int RPT, int READ, bool DER, bool ONE>
 __global__ void __launch_bounds__(REC_NT) k_rec(const __grid_constant__ RecArgs P) {
     using A = typename AccOf<T>::A;
+    after_previous();
     constexpr int DKP = RPT * 8;
     extern __shared__ __align__(16) unsigned char smem_raw[];
     constexpr int STAGE = DKP * (READ ? 2 : 1) + REC_COLS * (READ == 2 ? 2 : 1);  // values of a row in all operands
@@ -429,6 +430,7 @@ template <typename A>
 __global__ void __launch_bounds__(256) k_dlam_join(const double* __restrict__ part, int64_t slots, int H, int cb,
                                                    A* __restrict__ dlam) {
     __shared__ double red[256];
+    after_previous();
     const int h = blockIdx.x;
     double s = 0;
     for (int64_t i = threadIdx.x; i < slots * cb; i += 256) s += part[(i / cb * H + h) * cb + i % cb];
@@ -459,6 +461,7 @@ struct CarryArgs {
 
 template <typename A, bool DER>
 __global__ void __launch_bounds__(128) k_carry(const __grid_constant__ CarryArgs args) {
+    after_previous();
     const LinCarry& C = args.dir[args.count > 1 && blockIdx.x >= gridDim.x / 2];
     const unsigned bx = args.count > 1 ? blockIdx.x % (gridDim.x / 2) : blockIdx.x;
     constexpr int VN = 16 / (int)sizeof(A), U = DER ? 2 : 4;
@@ -539,7 +542,7 @@ int rec_segment(int64_t T, int N, int H, int dv, bool equal) {
 }
 
 template <typename T, int RPT, int READ, bool DER, bool ONE>
-static cudaError_t rec_launch(const RecArgs& P, cudaStream_t st) {
+static cudaError_t rec_launch(const RecArgs& P, bool next, cudaStream_t st) {
     using A = typename AccOf<T>::A;
     constexpr auto kern = k_rec<T, RPT, READ, DER, ONE>;
     constexpr size_t row = sizeof(A) * (2 * (RPT * 8 * (READ ? 2 : 1) + REC_COLS * (READ == 2 ? 2 : 1)) + (READ == 1 ? REC_OUT : 0));
@@ -551,16 +554,15 @@ static cudaError_t rec_launch(const RecArgs& P, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)P.S.slots, (unsigned)P.H, (unsigned)((P.R.dv + REC_COLS - 1) / REC_COLS));
     if (grid.x == 0) return cudaSuccess;
-    kern<<<grid, REC_NT, smem, st>>>(P);
-    return cudaGetLastError();
+    return launch(next, kern, grid, REC_NT, smem, st, P);
 }
 
 template <typename T, int READ, bool DER, bool ONE = false>
-static cudaError_t rec_dim(RecArgs P, cudaStream_t st) {
+static cudaError_t rec_dim(RecArgs P, bool next, cudaStream_t st) {
     P.rows = std::max(P.R.nq, P.R.nk) > 16 ? 32 : 16;
-    return P.R.dk <= 64   ? rec_launch<T, 8, READ, DER, ONE>(P, st)
-           : P.R.dk <= 96 ? rec_launch<T, 12, READ, DER, ONE>(P, st)
-                          : rec_launch<T, 16, READ, DER, ONE>(P, st);
+    return P.R.dk <= 64   ? rec_launch<T, 8, READ, DER, ONE>(P, next, st)
+           : P.R.dk <= 96 ? rec_launch<T, 12, READ, DER, ONE>(P, next, st)
+                          : rec_launch<T, 16, READ, DER, ONE>(P, next, st);
 }
 
 template <typename F>
@@ -575,7 +577,7 @@ static cudaError_t with_type(laplex_dtype dt, F f) {
 }
 
 cudaError_t rec_run(laplex_dtype dt, const LinRole& R, const LinSeqs& S, int H, const void* lam, bool state_only,
-                    cudaStream_t st) {
+                    bool next, cudaStream_t st) {
     RecArgs P = {};
     P.R = R;
     P.S = S;
@@ -583,8 +585,8 @@ cudaError_t rec_run(laplex_dtype dt, const LinRole& R, const LinSeqs& S, int H, 
     P.lam = lam;
     const auto go = [&](auto t) {
         using T = decltype(t);
-        if (R.nq == 1 && R.nk == 1) return state_only ? rec_dim<T, 0, false, true>(P, st) : rec_dim<T, 1, false, true>(P, st);
-        return state_only ? rec_dim<T, 0, false>(P, st) : rec_dim<T, 1, false>(P, st);
+        if (R.nq == 1 && R.nk == 1) return state_only ? rec_dim<T, 0, false, true>(P, next, st) : rec_dim<T, 1, false, true>(P, next, st);
+        return state_only ? rec_dim<T, 0, false>(P, next, st) : rec_dim<T, 1, false>(P, next, st);
     };
     return dt == LAPLEX_F64 ? go(double()) : go(float());
 }
@@ -598,13 +600,11 @@ cudaError_t carry_run(laplex_dtype dt, const LinCarry* C, int count, cudaStream_
     args.count = count;
     for (int i = 0; i < count; ++i) args.dir[i] = C[i];
     if (dt == LAPLEX_F64) {
-        if (C->w) k_carry<double, true><<<grid, 128, 0, st>>>(args);
-        else k_carry<double, false><<<grid, 128, 0, st>>>(args);
-    } else {
-        if (C->w) k_carry<float, true><<<grid, 128, 0, st>>>(args);
-        else k_carry<float, false><<<grid, 128, 0, st>>>(args);
+        return C->w ? launch(true, k_carry<double, true>, grid, 128, 0, st, args)
+                    : launch(true, k_carry<double, false>, grid, 128, 0, st, args);
     }
-    return cudaGetLastError();
+    return C->w ? launch(true, k_carry<float, true>, grid, 128, 0, st, args)
+                : launch(true, k_carry<float, false>, grid, 128, 0, st, args);
 }
 
 static LinSeqs dlam_seqs(int64_t T, int N, const int32_t* cu, int Hkv, int dv) {
@@ -651,7 +651,7 @@ cudaError_t dlam_run(laplex_dtype dt, LinRole fwd, LinRows dout, LinSeqs S0, int
         Q.R.state_out = base;
         Q.R.out_by_slot = 1;
         Q.R.w_out = base + sb;
-        e = with_type(dt, [&](auto t) { return rec_dim<decltype(t), 0, true>(Q, st); });
+        e = with_type(dt, [&](auto t) { return rec_dim<decltype(t), 0, true>(Q, false, st); });
         if (e != cudaSuccess) return e;
         LinCarry C = {};
         C.S = S;
@@ -668,11 +668,11 @@ cudaError_t dlam_run(laplex_dtype dt, LinRole fwd, LinRows dout, LinSeqs S0, int
     }
     P.dout = dout;
     P.dstate = dstate;
-    e = with_type(dt, [&](auto t) { return rec_dim<decltype(t), 2, true>(P, st); });
+    e = with_type(dt, [&](auto t) { return rec_dim<decltype(t), 2, true>(P, S.seg <= S.T, st); });
     if (e != cudaSuccess) return e;
-    if (dt == LAPLEX_F64) k_dlam_join<double><<<H, 256, 0, st>>>(P.part, S.slots, H, cb, (double*)dlam);
-    else k_dlam_join<float><<<H, 256, 0, st>>>(P.part, S.slots, H, cb, (float*)dlam);
-    return cudaGetLastError();
+    const bool next = S.slots > 0;  // (without a sequence no kernel ran)
+    return dt == LAPLEX_F64 ? launch(next, k_dlam_join<double>, H, 256, 0, st, P.part, (int64_t)S.slots, H, cb, (double*)dlam)
+                            : launch(next, k_dlam_join<float>, H, 256, 0, st, P.part, (int64_t)S.slots, H, cb, (float*)dlam);
 }
 
 }  // namespace lx

@@ -1007,6 +1007,7 @@ struct TcBlock {
 // block: its segment and role
 template <typename T, int DK, int DV, bool OUT>
 __device__ __forceinline__ void lin_block(const TcArgs& A, int block, unsigned char* sm) {
+    after_previous();
     using Z = TcSize<DK, DV, OUT>;
     TcShared& sh = *reinterpret_cast<TcShared*>(sm + Z::TILES);
     const TcRole& R = A.role[block % A.nroles];
@@ -1198,7 +1199,7 @@ template <auto kern> static cudaError_t registers_suffice(int threads) {
 }
 
 template <typename T, int DK, int DV, bool OUT>
-static cudaError_t tc_launch(const TcArgs& A, cudaStream_t st) {
+static cudaError_t tc_launch(const TcArgs& A, bool next, cudaStream_t st) {
     constexpr auto kern = k_lin_tc<T, DK, DV, OUT>;
     using Z = TcSize<DK, DV, OUT>;
     constexpr size_t smem = Z::BYTES;
@@ -1209,12 +1210,11 @@ static cudaError_t tc_launch(const TcArgs& A, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(A.S.slots * A.nroles), (unsigned)A.H);
     if (grid.x == 0) return cudaSuccess;
-    kern<<<grid, Z::NT, smem, st>>>(A);
-    return cudaGetLastError();
+    return launch(next, kern, grid, Z::NT, smem, st, A);
 }
 
 template <typename T, int DK, int DV, int DK2, int DV2, bool OUT2>
-static cudaError_t pair_launch(const TcArgs& A, const TcArgs& B, cudaStream_t st) {
+static cudaError_t pair_launch(const TcArgs& A, const TcArgs& B, bool next, cudaStream_t st) {
     constexpr auto kern = k_lin_pair<T, DK, DV, DK2, DV2, OUT2>;
     using Z = TcSize<DK, DV, true>;
     constexpr size_t smem = std::max(Z::BYTES, TcSize<DK2, DV2, OUT2>::BYTES);
@@ -1226,17 +1226,16 @@ static cudaError_t pair_launch(const TcArgs& A, const TcArgs& B, cudaStream_t st
     const int first = A.S.slots * A.nroles;
     const dim3 grid((unsigned)(first + B.S.slots * B.nroles), (unsigned)A.H);
     if (grid.x == 0) return cudaSuccess;
-    kern<<<grid, Z::NT, smem, st>>>(A, B, first);
-    return cudaGetLastError();
+    return launch(next, kern, grid, Z::NT, smem, st, A, B, first);
 }
 
 static_assert(TcSize<128, 128, true>::BYTES <= 232448 && TcSize<128, 128, false>::BYTES <= 232448 / 2 - 1024,
               "shared memory of a block");
 
 template <typename T, bool OUT>
-static cudaError_t tc_dims(const TcArgs& A, int dk, int dv, cudaStream_t st) {
-    if (dk <= 64) return dv <= 64 ? tc_launch<T, 64, 64, OUT>(A, st) : tc_launch<T, 64, 128, OUT>(A, st);
-    return dv <= 64 ? tc_launch<T, 128, 64, OUT>(A, st) : tc_launch<T, 128, 128, OUT>(A, st);
+static cudaError_t tc_dims(const TcArgs& A, int dk, int dv, bool next, cudaStream_t st) {
+    if (dk <= 64) return dv <= 64 ? tc_launch<T, 64, 64, OUT>(A, next, st) : tc_launch<T, 64, 128, OUT>(A, next, st);
+    return dv <= 64 ? tc_launch<T, 128, 64, OUT>(A, next, st) : tc_launch<T, 128, 128, OUT>(A, next, st);
 }
 
 static int tc_pad(int d) { return d <= 64 ? 64 : 128; }
@@ -1304,12 +1303,12 @@ static cudaError_t tc_args(laplex_dtype dt, const LinRole* roles, int count, boo
 }
 
 template <typename T>
-static cudaError_t tc_both(const TcArgs& A, const TcArgs& B, bool out2, cudaStream_t st) {
+static cudaError_t tc_both(const TcArgs& A, const TcArgs& B, bool out2, bool next, cudaStream_t st) {
     const int dk = tc_pad(A.role[0].dk), dv = tc_pad(A.role[0].dv);
     if (out2)  // of two shapes: one is the other transposed
-        return dk < dv ? pair_launch<T, 64, 128, 128, 64, true>(A, B, st) : pair_launch<T, 64, 128, 128, 64, true>(B, A, st);
-    if (dk <= 64) return dv <= 64 ? pair_launch<T, 64, 64, 64, 64, false>(A, B, st) : pair_launch<T, 64, 128, 64, 128, false>(A, B, st);
-    return dv <= 64 ? pair_launch<T, 128, 64, 128, 64, false>(A, B, st) : pair_launch<T, 128, 128, 128, 128, false>(A, B, st);
+        return dk < dv ? pair_launch<T, 64, 128, 128, 64, true>(A, B, next, st) : pair_launch<T, 64, 128, 128, 64, true>(B, A, next, st);
+    if (dk <= 64) return dv <= 64 ? pair_launch<T, 64, 64, 64, 64, false>(A, B, next, st) : pair_launch<T, 64, 128, 64, 128, false>(A, B, next, st);
+    return dv <= 64 ? pair_launch<T, 128, 64, 128, 64, false>(A, B, next, st) : pair_launch<T, 128, 128, 128, 128, false>(A, B, next, st);
 }
 
 // The products of roles[0 .. count), and the states of `last` if there is one.  Two launches that fit on the GPU
@@ -1317,7 +1316,7 @@ static cudaError_t tc_both(const TcArgs& A, const TcArgs& B, bool out2, cudaStre
 // of 64 x 64 with their last state: 10.5 us against 19 in turn; the gradients of 1500 tokens of 4 heads of 64 x 96: 17
 // against 30.  More blocks than SMs: the state pass does better by itself, two blocks on an SM.)
 cudaError_t tc_run(laplex_dtype dt, const LinRole* roles, int count, const LinRole* last, const LinSeqs& S, int H,
-                   const void* lam, uint32_t* status, cudaStream_t st) {
+                   const void* lam, uint32_t* status, bool next, cudaStream_t st) {
     TcArgs A[3];
     int n = 0;
     bool done[3] = {false, false, false}, state[3] = {false, false, false};
@@ -1342,16 +1341,18 @@ cudaError_t tc_run(laplex_dtype dt, const LinRole* roles, int count, const LinRo
         if (!state[at] && at + 1 < n && (int64_t)S.slots * H * (X.nroles + A[at + 1].nroles) <= sms &&
             (!state[at + 1] || (tc_pad(A[at + 1].role[0].dk) == dk && tc_pad(A[at + 1].role[0].dv) == dv &&
                                 A[at + 1].role[0].state_out != X.role[0].state_in))) {
-            e = dt == LAPLEX_BF16 ? tc_both<__nv_bfloat16>(X, A[at + 1], !state[at + 1], st)
-                                  : tc_both<__half>(X, A[at + 1], !state[at + 1], st);
+            e = dt == LAPLEX_BF16 ? tc_both<__nv_bfloat16>(X, A[at + 1], !state[at + 1], next, st)
+                                  : tc_both<__half>(X, A[at + 1], !state[at + 1], next, st);
             at += 2;
+            next = true;
             continue;
         }
         if (dt == LAPLEX_BF16)
-            e = state[at] ? tc_dims<__nv_bfloat16, false>(X, dk, dv, st) : tc_dims<__nv_bfloat16, true>(X, dk, dv, st);
+            e = state[at] ? tc_dims<__nv_bfloat16, false>(X, dk, dv, next, st) : tc_dims<__nv_bfloat16, true>(X, dk, dv, next, st);
         else
-            e = state[at] ? tc_dims<__half, false>(X, dk, dv, st) : tc_dims<__half, true>(X, dk, dv, st);
+            e = state[at] ? tc_dims<__half, false>(X, dk, dv, next, st) : tc_dims<__half, true>(X, dk, dv, next, st);
         ++at;
+        next = true;
     }
     return e;
 }
@@ -1366,7 +1367,7 @@ cudaError_t tc_states(laplex_dtype dt, const LinRole* roles, int count, const Li
         e = tc_args(dt, roles, count, done, S, H, lam, true, status, &A);
         if (e != cudaSuccess) return e;
         const int dk = tc_pad(A.role[0].dk), dv = tc_pad(A.role[0].dv);
-        e = dt == LAPLEX_BF16 ? tc_dims<__nv_bfloat16, false>(A, dk, dv, st) : tc_dims<__half, false>(A, dk, dv, st);
+        e = dt == LAPLEX_BF16 ? tc_dims<__nv_bfloat16, false>(A, dk, dv, i > 0, st) : tc_dims<__half, false>(A, dk, dv, i > 0, st);
     }
     return e;
 }

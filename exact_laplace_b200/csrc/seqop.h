@@ -90,10 +90,11 @@ struct LinCarry {
     void* last;               // per sequence: the state behind the last segment, or NULL
 };
 
+// (next: the call has launched a kernel before)
 // ---- recurrent kernels (every type; linattn_rec.cu)
 int rec_segment(int64_t T, int N, int H, int dv, bool equal);
 cudaError_t rec_run(laplex_dtype dt, const LinRole& R, const LinSeqs& S, int H, const void* lam, bool state_only,
-                    cudaStream_t st);
+                    bool next, cudaStream_t st);
 cudaError_t carry_run(laplex_dtype dt, const LinCarry* C, int count, cudaStream_t st);  // up to two directions
 // dlam[h] = sum over the sequences of scale <do_t, W_t^T q_t> (+ <dstate, W_last>)
 size_t dlam_ws_bytes(laplex_dtype dt, int64_t T, int N, int Hkv, int dk, int dv, bool equal);
@@ -104,7 +105,7 @@ cudaError_t dlam_run(laplex_dtype dt, LinRole fwd, LinRows dout, LinSeqs S, int 
 // them, the states behind the last tokens (`last`, or NULL); states of segments, two directions at a time
 int tc_segment(int64_t T, int N, int H, int roles, bool equal);
 cudaError_t tc_run(laplex_dtype dt, const LinRole* roles, int count, const LinRole* last, const LinSeqs& S, int H,
-                   const void* lam, uint32_t* status, cudaStream_t st);
+                   const void* lam, uint32_t* status, bool next, cudaStream_t st);
 cudaError_t tc_states(laplex_dtype dt, const LinRole* roles, int count, const LinSeqs& S, int H, const void* lam,
                       uint32_t* status, cudaStream_t st);
 
@@ -144,6 +145,22 @@ cudaError_t embed_bwd_run(laplex_dtype dt, laplex_dtype out_dt, const EmbedArgs&
 size_t sort_keys_ws_bytes(int64_t n);
 cudaError_t sort_keys_run(const uint32_t* keys, int64_t n, uint32_t top, uint32_t* skeys, int32_t* perm, void* ws,
                           size_t ws_bytes, uint32_t* status, cudaStream_t st);
+
+// A launch; `next`: behind another kernel of the same call, on whose end it waits by itself (after_previous).
+template <typename... P, typename... A>
+cudaError_t launch(bool next, void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const A&... args) {
+    cudaLaunchAttribute at = {};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &at;
+    cfg.numAttrs = next ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 
 inline size_t elem_bytes(laplex_dtype dt) { return dt == LAPLEX_F64 ? 8 : dt == LAPLEX_F32 ? 4 : 2; }
 inline size_t acc_bytes(laplex_dtype dt) { return dt == LAPLEX_F64 ? 8 : 4; }
