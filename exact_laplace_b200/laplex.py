@@ -552,13 +552,13 @@ def _addr(x):
     return None if x is None else x.data_ptr()
 
 
-def _like(x):
-    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+def _new(shape, dtype, dev):
+    return torch.empty(*shape, dtype=dtype, device=dev)  # (sizes one by one: 0.8 us less than as a tuple)
 
 
 def _state(name, x, shape, dtype):
     if x is not None:
-        if tuple(x.shape) != tuple(shape) or x.dtype != dtype or not x.is_contiguous():
+        if x.shape != shape or x.dtype != dtype or not x.is_contiguous():
             raise LaplexError(EINVAL, f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     return x
 
@@ -570,7 +570,7 @@ def _shape(q3, k3, v3, seqs, cu, log_decay, scale, dt):
     if k3.shape != (t, hkv, dk) or v3.shape != (t, hkv, dv):
         raise LaplexError(EINVAL, f"shapes of q {tuple(q3.shape)}, k {tuple(k3.shape)} and v {tuple(v3.shape)}")
     acc = torch.float64 if dt == F64 else torch.float32
-    if tuple(log_decay.shape) != (hkv,) or log_decay.dtype != acc or not log_decay.is_contiguous():
+    if log_decay.shape != (hkv,) or log_decay.dtype != acc or not log_decay.is_contiguous():
         raise LaplexError(EINVAL, f"log_decay must be a contiguous {acc} tensor of {hkv} heads")
     s = _LinattnShape(t, seqs, None if cu is None else cu.data_ptr(), hq, hkv, dk, dv, log_decay.data_ptr(),
                       float(dk ** -0.5 if scale is None else scale), dt)
@@ -638,11 +638,11 @@ def linattn(q, k, v, log_decay, scale=None, cu_seqlens=None, state=None, return_
     _state("state_out", state_out, shape, acc)
     with _on(dev):
         if out is None:
-            out = torch.empty(tuple(q.shape[:-1]) + (s.dv,), dtype=q.dtype, device=dev)
-        elif tuple(out.shape) != tuple(q.shape[:-1]) + (s.dv,):
+            out = _new(q.shape[:-1] + (s.dv,), q.dtype, dev)
+        elif out.shape != q.shape[:-1] + (s.dv,):
             raise LaplexError(EINVAL, f"out must have the shape {tuple(q.shape[:-1]) + (s.dv,)}")
         if return_state and state_out is None:
-            state_out = torch.empty(shape, dtype=acc, device=dev)
+            state_out = _new(shape, acc, dev)
         raw = _raw_stream(dev)
         ws = _linattn_ws(s, LINATTN_FORWARD, dev, raw)
         _check(lib().laplex_linattn(ctypes.byref(s), _rows(q3), _rows(k3), _rows(v3), _addr(state),
@@ -663,20 +663,20 @@ def linattn_backward(q, k, v, log_decay, dout, scale=None, cu_seqlens=None, stat
     seqs = _seqs(q, cu_seqlens)
     q3, k3, v3, do3 = _packed("q", q), _packed("k", k), _packed("v", v), _packed("dout", dout)
     s, acc = _shape(q3, k3, v3, seqs, cu_seqlens, log_decay, scale, _seq_dt(q, k, v, dout, *(out or ())))
-    if tuple(do3.shape) != (s.tokens, s.hq, s.dv):
+    if do3.shape != (s.tokens, s.hq, s.dv):
         raise LaplexError(EINVAL, f"dout must have the shape {(s.tokens, s.hq, s.dv)}")
     shape = (seqs, s.hkv, s.dk, s.dv)
     _state("state", state, shape, acc)
     _state("dstate", dstate, shape, acc)
     with _on(dev):
         if out is None:
-            out = (_like(q), _like(k), _like(v))
+            out = tuple(_new(x.shape, x.dtype, dev) for x in (q, k, v))
         elif any(a.shape != b.shape for a, b in zip(out, (q, k, v))):
             raise LaplexError(EINVAL, "out must have the shapes of q, k and v")
         dq, dk, dv = out
         ds = None
         if return_dstate or (return_dstate is None and state is not None):
-            ds = torch.empty(shape, dtype=acc, device=dev)
+            ds = _new(shape, acc, dev)
         dl = torch.empty(s.hkv, dtype=acc, device=dev) if return_dlog_decay else None
         raw = _raw_stream(dev)
         ws = _linattn_ws(s, LINATTN_BACKWARD_DECAY if return_dlog_decay else LINATTN_BACKWARD, dev, raw)
@@ -703,12 +703,12 @@ def linattn_step(q, k, v, log_decay, states, slots=None, scale=None, out=None):
     if states.dim() != 4:
         raise LaplexError(EINVAL, "states must be [num_slots, hkv, dk, dv]")
     _state("states", states, (states.shape[0], s.hkv, s.dk, s.dv), acc)
-    if slots is not None and (slots.dtype != torch.int32 or tuple(slots.shape) != (s.tokens,) or not slots.is_contiguous()):
+    if slots is not None and (slots.dtype != torch.int32 or slots.shape != (s.tokens,) or not slots.is_contiguous()):
         raise LaplexError(EINVAL, "slots must be a contiguous int32 tensor [rows]")
     with _on(dev):
         if out is None:
-            out = torch.empty((s.tokens, s.hq, s.dv), dtype=q.dtype, device=dev)
-        elif tuple(out.shape) != (s.tokens, s.hq, s.dv):
+            out = _new((s.tokens, s.hq, s.dv), q.dtype, dev)
+        elif out.shape != (s.tokens, s.hq, s.dv):
             raise LaplexError(EINVAL, f"out must have the shape {(s.tokens, s.hq, s.dv)}")
         _check(lib().laplex_linattn_step(ctypes.byref(s), _rows(q3), _rows(k3), _rows(v3), states.data_ptr(),
                                          states.shape[0], _addr(slots), _rows(_packed("out", out)), _raw_stream(dev)))
@@ -733,11 +733,11 @@ def embed(table, tokens, scale=1.0, out=None):
     float32 or float64; tokens int32 or int64."""
     dev = _seq_dev(table, tokens, out)
     dt, tb, ld = _seq_dt(table, out), _tokens(tokens), _table("table", table)
-    shape = tuple(tokens.shape) + (table.shape[1],)
+    shape = tokens.shape + (table.shape[1],)
     with _on(dev):
         if out is None:
-            out = torch.empty(shape, dtype=table.dtype, device=dev)
-        elif tuple(out.shape) != shape or (out.dim() != 2 and not out.is_contiguous()):
+            out = _new(shape, table.dtype, dev)
+        elif out.shape != shape or (out.dim() != 2 and not out.is_contiguous()):
             raise LaplexError(EINVAL, f"out must have the shape {shape}")
         o2 = out if out.dim() == 2 else out.view(-1, table.shape[1])
         _check(lib().laplex_embed(table.data_ptr(), ld, table.shape[0], table.shape[1], tokens.data_ptr(), tb,
@@ -765,7 +765,7 @@ def embed_backward(tokens, g, rows, scale=1.0, out=None, accumulate=False, dtype
         raise LaplexError(EINVAL, "accumulate needs out")
     with _on(dev):
         if out is None:
-            out = torch.empty((rows, dim), dtype=dtype or g.dtype, device=dev)
+            out = _new((rows, dim), dtype or g.dtype, dev)
         if out.shape[0] != rows or out.dtype not in (g.dtype, torch.float32):
             raise LaplexError(EINVAL, f"out must have {rows} rows of {g.dtype} or float32")
         key = (tokens.numel(), rows, dim, dt)
