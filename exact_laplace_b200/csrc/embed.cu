@@ -26,8 +26,8 @@
 //     zero the rows without a token, by a bitmap of the tokens that occur, lie
 //     between them, so that reads and writes overlap (write-only traffic ran at
 //     3.8 TB/s) and each row of the table is written once.
-//   k_embed_join: the partial sums of the runs that cross boundaries, in a fixed
-//     order, eight warps to a run.
+//   k_embed_join: the partial sums of the long runs, which k_embed_sum lists, in a
+//     fixed order: a warp to 32 lanes x 16 bytes of a run, eight where it has many parts.
 #include <algorithm>
 
 #include "devcache.h"
@@ -107,8 +107,10 @@ __device__ __forceinline__ int64_t token_at(const void* tokens, int tok64, int64
 }
 
 __global__ void __launch_bounds__(256) k_embed_keys(const void* tokens, int tok64, int64_t n, int64_t rows,
-                                                    uint32_t* __restrict__ keys, uint32_t* __restrict__ seen) {
+                                                    uint32_t* __restrict__ keys, uint32_t* __restrict__ seen,
+                                                    uint32_t* __restrict__ counts) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < 2) counts[i] = 0;
     if (i >= n) return;
     const int64_t tok = token_at(tokens, tok64, i);
     const bool known = tok >= 0 && tok < rows;
@@ -129,6 +131,7 @@ struct TokenSort {
     int32_t* perm;
     uint32_t* seen;    // or NULL
     int64_t words;     // of seen
+    uint32_t* counts;  // two, set to 0 for k_embed_sum
 };
 
 struct TokenSortShared {
@@ -171,6 +174,7 @@ __global__ void __launch_bounds__(TS_NT) k_token_sort(const __grid_constant__ To
     const int bins = 1 << P.bits;
     if (P.seen)
         for (int64_t i = (int64_t)me * TS_NT + tid; i < P.words; i += (int64_t)blocks * TS_NT) P.seen[i] = 0;
+    if (me == 0 && tid < 2) P.counts[tid] = 0;
     cluster_sync();  // the bitmap is clear (and every block of the cluster runs)
     for (int i = tid; i < count; i += TS_NT) {
         const int64_t tok = token_at(P.tokens, P.tok64, lo + i);
@@ -298,7 +302,8 @@ __global__ void __launch_bounds__(TS_NT) k_token_sort(const __grid_constant__ To
     }
 }
 
-static cudaError_t token_sort(const EmbedArgs& A, uint32_t* skeys, int32_t* perm, uint32_t* seen, cudaStream_t st) {
+static cudaError_t token_sort(const EmbedArgs& A, uint32_t* skeys, int32_t* perm, uint32_t* seen, uint32_t* counts,
+                              cudaStream_t st) {
     TokenSort P;
     P.tokens = A.tokens;
     P.tok64 = A.tok64;
@@ -308,6 +313,7 @@ static cudaError_t token_sort(const EmbedArgs& A, uint32_t* skeys, int32_t* perm
     P.perm = perm;
     P.seen = seen;
     P.words = (A.rows + 31) / 32;
+    P.counts = counts;
     int bits = 1;
     while (bits < 31 && (A.rows >> bits) != 0) ++bits;
     P.passes = (bits + 9) / 10;  // as few as 1024 digits allow
@@ -342,6 +348,8 @@ struct EmbedSum {
     void* part;             // [tiles][2][dim]: sums of the runs that enter / leave a tile
     int64_t tiles;
     int R;                  // sorted positions per tile
+    int32_t* list;          // [2][tiles]: tiles in which a long run begins; those of many parts
+    uint32_t* counts;       // of both
     int64_t sum_blocks, zero_blocks;  // blocks of the sums, and those that zero the rows without a token
 };
 
@@ -379,6 +387,7 @@ __device__ __forceinline__ bool border(const uint32_t* keys, int64_t p, int64_t 
 }
 
 constexpr int SUM_NT = 128;
+constexpr int MANY = 16;  // parts of a run that one warp joins
 
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
@@ -499,12 +508,20 @@ __global__ void __launch_bounds__(SUM_NT) k_embed_sum(const __grid_constant__ Em
     } else if (leaves) {
 #pragma unroll
         for (int e = 0; e < VN; ++e) part[E.dim + e] = s[e];
+        if (c == 0) {  // for the join, in any order: each run has its own row
+            const int64_t far = p1 + (int64_t)(MANY - 1) * P.R + SUM_H;
+            const int many = far < E.n && P.keys[far] == cur;
+            P.list[many * P.tiles + atomicAdd(P.counts + many, 1u)] = (int32_t)tile;
+        }
     } else embed_write<T, W, VN>(E, cur, c, s);
 }
 
-// The runs that cross tile boundaries, by the tile that a run leaves: eight warps
-// sum an eighth of its parts each, in order, and the eight are joined in order.
-// VN columns a lane.
+// The long runs: part 0 is the one of the end of the tile where the run begins, part
+// i > 0 the one of the start of the i-th tile after it.  Runs of up to MANY parts take
+// a warp for each 32 VN columns; longer ones a block, whose warps sum an eighth of
+// the parts each, in order, and are joined in order.  (Found by a search over all
+// tiles' borders, a block to a run: 210 us for the gradient of 65536 Zipf tokens, 2048
+// columns, 170 such runs; so 197.)
 template <typename T, typename W, int VN>
 __global__ void __launch_bounds__(EMB_NT) k_embed_join(const __grid_constant__ EmbedSum P) {
     using A = typename AccOf<T>::A;
@@ -513,69 +530,69 @@ __global__ void __launch_bounds__(EMB_NT) k_embed_join(const __grid_constant__ E
     after_previous();
     const EmbedArgs& E = P.A;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // this block's tiles: those of blockIdx.x + t gridDim.x that a long run leaves which began in them
-    __shared__ int64_t todo[EMB_NT];
-    __shared__ int found, past;
-    const auto join = [&](int64_t tile) {
-        const uint32_t key = P.keys[(tile + 1) * P.R - 1];
-        // the first tile past the run: it enters a tile as long as it is long at its start
-        int64_t lo = tile + 1;
-        for (;; lo += EMB_NT) {
-            if (threadIdx.x == 0) past = EMB_NT;
-            __syncthreads();
-            const int64_t t = lo + threadIdx.x;
-            if (!(t < P.tiles && P.keys[t * P.R] == key && long_run(P.keys, t * P.R, E.n))) atomicMin(&past, (int)threadIdx.x);
-            __syncthreads();
-            const int p = past;
-            __syncthreads();
-            if (p < EMB_NT) {
-                lo += p;
+    const int64_t pieces = (E.dim + 32 * VN - 1) / (32 * VN);
+    const int64_t few = P.counts[0] * pieces, many = P.counts[1] * pieces;
+    // the run that begins in `tile`: its key and parts (by a whole warp)
+    const auto find = [&](int64_t tile, uint32_t* key) -> int64_t {
+        const uint32_t k = P.keys[(tile + 1) * P.R - 1];
+        *key = k;
+        const auto enters = [&](int64_t t) {  // (long at its start; ascending keys: true up to the last such tile)
+            const int64_t p = t * P.R + SUM_H;
+            return p < E.n && P.keys[p] == k;
+        };
+        int64_t end = tile + 1;  // all tiles between are entered
+        for (;;) {
+            const int n = __popc(__ballot_sync(FULL, enters(end + lane * 32)));
+            if (n == 0) break;
+            end += (n - 1) * 32 + 1;
+            if (n < 32) {
+                end += __popc(__ballot_sync(FULL, enters(end + lane)));
                 break;
             }
         }
-        // part 0 is the one of this tile's end, part i > 0 the one of tile + i's start
-        const int64_t parts = lo - tile, a0 = parts * warp / NW, a1 = parts * (warp + 1) / NW;
-        const A* part = static_cast<const A*>(P.part) + tile * 2 * E.dim;
-        for (int64_t cb = (int64_t)blockIdx.y * 32 * VN; cb < E.dim; cb += (int64_t)gridDim.y * 32 * VN) {
-            const int64_t c = cb + lane * VN;
-            A s[VN];
+        return end - tile;
+    };
+    const auto sum = [&](int64_t tile, int64_t a0, int64_t a1, int64_t c, A(&s)[VN]) {
+        const A* part = static_cast<const A*>(P.part) + tile * 2 * E.dim + c;
 #pragma unroll
-            for (int e = 0; e < VN; ++e) s[e] = 0;
-            if (c < E.dim) {
+        for (int e = 0; e < VN; ++e) s[e] = 0;
 #pragma unroll 8
-                for (int64_t i = a0; i < a1; ++i) {
-                    const Pack<A, VN> v = *reinterpret_cast<const Pack<A, VN>*>(part + (i == 0 ? E.dim : i * 2 * E.dim) + c);
+        for (int64_t i = a0; i < a1; ++i) {
+            const Pack<A, VN> v = *reinterpret_cast<const Pack<A, VN>*>(part + (i == 0 ? E.dim : i * 2 * E.dim));
 #pragma unroll
-                    for (int e = 0; e < VN; ++e) s[e] += v.v[e];
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < VN; ++e) red[warp][lane * VN + e] = s[e];
-            __syncthreads();
-            for (int x = threadIdx.x; x < 32 * VN; x += EMB_NT) {
-                A t = 0;
-#pragma unroll
-                for (int w = 0; w < NW; ++w) t += red[w][x];
-                if (cb + x < E.dim) embed_write<T, W, 1>(E, key, cb + x, &t);
-            }
-            __syncthreads();
+            for (int e = 0; e < VN; ++e) s[e] += v.v[e];
         }
     };
-    for (int64_t t0 = blockIdx.x; t0 < P.tiles - 1; t0 += (int64_t)gridDim.x * EMB_NT) {
-        if (threadIdx.x == 0) found = 0;
-        __syncthreads();
-        {
-            const int64_t t = t0 + (int64_t)threadIdx.x * gridDim.x;
-            if (t < P.tiles - 1) {  // (the last tile leaves nothing)
-                const int64_t a = t * P.R, b = a + P.R;
-                const uint32_t k = P.keys[b - 1];
-                if (k != (uint32_t)E.rows && long_run(P.keys, b, E.n) && !(P.keys[a] == k && long_run(P.keys, a, E.n)))
-                    todo[atomicAdd(&found, 1)] = t;  // (in any order: each has its own row)
-            }
+    for (int64_t x = blockIdx.x; x < many; x += gridDim.x) {
+        const int64_t tile = P.list[P.tiles + x / pieces], cb = x % pieces * 32 * VN, c = cb + lane * VN;
+        uint32_t key;
+        const int64_t parts = find(tile, &key);
+        A s[VN];
+        if (c < E.dim) {
+            sum(tile, parts * warp / NW, parts * (warp + 1) / NW, c, s);
+#pragma unroll
+            for (int e = 0; e < VN; ++e) red[warp][lane * VN + e] = s[e];
         }
         __syncthreads();
-        for (int f = 0; f < found; ++f) join(todo[f]);
-        __syncthreads();  // `found` has been read
+        for (int i = threadIdx.x; i < 32 * VN; i += EMB_NT) {
+            if (cb + i >= E.dim) break;
+            A t = 0;
+#pragma unroll
+            for (int w = 0; w < NW; ++w) t += red[w][i];
+            embed_write<T, W, 1>(E, key, cb + i, &t);
+        }
+        __syncthreads();
+    }
+    // (from the last block on: the first ones have the long runs)
+    for (int64_t x = (int64_t)(gridDim.x - 1 - blockIdx.x) * NW + warp; x < few; x += (int64_t)gridDim.x * NW) {
+        const int64_t tile = P.list[x / pieces], c = x % pieces * 32 * VN + lane * VN;
+        uint32_t key;
+        const int64_t parts = find(tile, &key);
+        if (c >= E.dim) continue;
+        A s[VN];
+        sum(tile, 0, parts, c, s);
+#pragma unroll
+        for (int e = 0; e < VN; ++e) embed_write<T, W, 1>(E, key, c + e, &s[e]);
     }
 }
 
@@ -589,7 +606,8 @@ static int embed_tile(int64_t n, int64_t dim, int es) {
 }
 
 struct EmbedWs {
-    size_t keys, skeys, perm, seen, part, sort;
+    size_t keys, skeys, perm, seen, part, list, sort;
+    size_t all() const { return keys + skeys + perm + seen + part + list + sort; }
 };
 static EmbedWs embed_ws(int64_t n, int64_t rows, int64_t dim, laplex_dtype dt) {
     EmbedWs W;
@@ -599,13 +617,13 @@ static EmbedWs embed_ws(int64_t n, int64_t rows, int64_t dim, laplex_dtype dt) {
     W.perm = Carve::need((size_t)n, 4);
     W.seen = Carve::need((size_t)((rows + 31) / 32), 4);
     W.part = Carve::need((size_t)(tiles * 2 * dim), acc_bytes(dt));
+    W.list = Carve::need((size_t)(2 * tiles + 2), 4);
     W.sort = n <= TS_MAX ? 0 : sort_keys_ws_bytes(n);
     return W;
 }
 
 size_t embed_bwd_ws_bytes(int64_t n, int64_t rows, int64_t dim, laplex_dtype dt) {
-    const EmbedWs W = embed_ws(n, rows, dim, dt);
-    return W.keys + W.skeys + W.perm + W.seen + W.part + W.sort;
+    return embed_ws(n, rows, dim, dt).all();
 }
 
 template <typename T, typename W>
@@ -631,7 +649,7 @@ static cudaError_t embed_sum_launch(EmbedSum S, int sms, bool sorted, cudaStream
         constexpr int JN = 16 / (int)sizeof(typename AccOf<T>::A);
         const bool jvec = S.A.dim % JN == 0;
         const int64_t jcols = (S.A.dim + 32 * (jvec ? JN : 1) - 1) / (32 * (jvec ? JN : 1));
-        const dim3 jg((unsigned)std::min<int64_t>(S.tiles - 1, 2 * (int64_t)sms), (unsigned)std::min<int64_t>(jcols, 8));
+        const unsigned jg = (unsigned)std::min<int64_t>((S.tiles * jcols + EMB_NT / 32 - 1) / (EMB_NT / 32), 4 * (int64_t)sms);
         return jvec ? launch(true, k_embed_join<T, W, JN>, jg, EMB_NT, 0, st, S)
                     : launch(true, k_embed_join<T, W, 1>, jg, EMB_NT, 0, st, S);
     }
@@ -645,23 +663,27 @@ cudaError_t embed_bwd_run(laplex_dtype dt, laplex_dtype out_dt, const EmbedArgs&
     cudaError_t e = current_device_sms(&dev, &sms);
     if (e != cudaSuccess) return e;
     const EmbedWs Z = embed_ws(A.n, A.rows, A.dim, dt);
-    if (ws_bytes < Z.keys + Z.skeys + Z.perm + Z.seen + Z.part + Z.sort) return cudaErrorInvalidValue;
+    if (ws_bytes < Z.all()) return cudaErrorInvalidValue;
     char* p = static_cast<char*>(ws);
     uint32_t* keys = (uint32_t*)p;
     uint32_t* skeys = (uint32_t*)(p += Z.keys);
     int32_t* perm = (int32_t*)(p += Z.skeys);
     uint32_t* seen = (uint32_t*)(p += Z.perm);
     void* part = p += Z.seen;
-    void* sort = p += Z.part;
+    int32_t* list = (int32_t*)(p += Z.part);
+    void* sort = p += Z.list;
     uint32_t* bits = A.accumulate ? nullptr : seen;
+    const int R = embed_tile(A.n, A.dim, (int)elem_bytes(dt));
+    const int64_t tiles = (A.n + R - 1) / R;
+    uint32_t* counts = (uint32_t*)list + 2 * tiles;
     const bool sorted = A.n > 0 && A.n <= TS_MAX;  // by a kernel of this call
     if (sorted) {
-        e = token_sort(A, skeys, perm, bits, st);
+        e = token_sort(A, skeys, perm, bits, counts, st);
         if (e != cudaSuccess) return e;
     } else {
         if (bits) e = cudaMemsetAsync(seen, 0, (size_t)((A.rows + 31) / 32) * 4, st);
         if (e == cudaSuccess && A.n > 0) {
-            k_embed_keys<<<(unsigned)((A.n + 255) / 256), 256, 0, st>>>(A.tokens, A.tok64, A.n, A.rows, keys, bits);
+            k_embed_keys<<<(unsigned)((A.n + 255) / 256), 256, 0, st>>>(A.tokens, A.tok64, A.n, A.rows, keys, bits, counts);
             e = cudaGetLastError();
             if (e == cudaSuccess)
                 e = sort_keys_run(keys, A.n, (uint32_t)A.rows, skeys, perm, sort, Z.sort, status, st);
@@ -674,8 +696,10 @@ cudaError_t embed_bwd_run(laplex_dtype dt, laplex_dtype out_dt, const EmbedArgs&
     S.perm = perm;
     S.seen = seen;
     S.part = part;
-    S.R = embed_tile(A.n, A.dim, (int)elem_bytes(dt));
-    S.tiles = (A.n + S.R - 1) / S.R;
+    S.R = R;
+    S.tiles = tiles;
+    S.list = list;
+    S.counts = counts;
     S.sum_blocks = S.zero_blocks = 0;
     const bool f32 = out_dt == LAPLEX_F32;
     switch (dt) {

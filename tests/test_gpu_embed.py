@@ -112,6 +112,20 @@ def test_gradient_sizes(n, rows, dim):
     assert torch.equal(got, X.embed_backward(torch.from_numpy(t).cuda(), g, rows, dtype=torch.float32))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32", "fp64"])
+@pytest.mark.parametrize("dim", [8, 130, 264])
+def test_gradient_of_runs_around_the_tiles(dt, dim):
+    # runs that begin and end around multiples of 16 positions, with 1 to 1300 tiles between
+    lens = [16 * k + d for k in (1, 2, 15, 16, 17, 18, 33) for d in (-1, 0, 1, 15)] + [20800]
+    rng = np.random.default_rng(7)
+    n, rows = sum(lens), 3 * len(lens)
+    t = np.repeat(3 * rng.permutation(len(lens)), lens)[rng.permutation(n)]
+    g = values((n, dim), DT[dt], 8)
+    got = X.embed_backward(torch.from_numpy(t).cuda(), g, rows, scale=0.5)
+    check_gradient(got, t, g, rows, 0.5, DT[dt], DT[dt])
+    assert torch.equal(got, X.embed_backward(torch.from_numpy(t).cuda(), g, rows, scale=0.5))
+
+
 @pytest.mark.parametrize("dt,out_dt", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp32"), ("fp32", "fp32"), ("fp64", "fp64")])
 def test_gradient_accumulates(dt, out_dt):
     n, rows, dim = 700, 90, 40
