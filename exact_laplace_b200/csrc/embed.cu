@@ -16,16 +16,17 @@
 // from run to run.
 //   k_token_sort (up to 65536 tokens): one cluster of up to 8 blocks keeps the
 //     tokens in its shared memory through the stable digit passes and scatters
-//     through distributed shared memory; one launch in place of seven to ten.  More
-//     tokens take the digit passes of sort.cu.
+//     through distributed shared memory; one launch in place of seven to ten.  The
+//     other SMs zero a part of the table meanwhile.  More tokens take the digit passes
+//     of sort.cu.
 //   k_embed_sum: a warp takes R consecutive sorted positions and 32 lanes x 16
 //     bytes of columns, reads the rows of g (16 to 32 in flight), sums in fp32 in
 //     position order, and writes the rows whose run lies inside its R positions.
 //     A run that crosses a boundary by up to 16 positions belongs to the warp before
 //     it; a longer one leaves one partial sum per side.  Blocks that
-//     zero the rows without a token, by a bitmap of the tokens that occur, lie
+//     zero the other rows without a token, by a bitmap of the tokens that occur, lie
 //     between them, so that reads and writes overlap (write-only traffic ran at
-//     3.8 TB/s) and each row of the table is written once.
+//     3.8 TB/s).
 //   k_embed_join: the partial sums of the long runs, which k_embed_sum lists, in a
 //     fixed order: a warp to 32 lanes x 16 bytes of a run, eight where it has many parts.
 #include <algorithm>
@@ -132,6 +133,9 @@ struct TokenSort {
     uint32_t* seen;    // or NULL
     int64_t words;     // of seen
     uint32_t* counts;  // two, set to 0 for k_embed_sum
+    int blocks;        // of the sort; the others zero rows of the table
+    unsigned char* zero;
+    int64_t zero_rows, zero_bytes, zero_ld;  // bytes of a row, and from row to row: multiples of 16
 };
 
 struct TokenSortShared {
@@ -169,7 +173,14 @@ __global__ void __launch_bounds__(TS_NT) k_token_sort(const __grid_constant__ To
     TokenSortShared& sh = *reinterpret_cast<TokenSortShared*>(raw);
     after_previous();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int me = blockIdx.x, blocks = gridDim.x;  // the grid is one cluster
+    const int me = blockIdx.x, blocks = P.blocks;  // the first cluster
+    if (me >= blocks) {
+        const int64_t w = (int64_t)(me - blocks) * TS_NW + warp, all = (int64_t)(gridDim.x - blocks) * TS_NW;
+        for (int64_t r = w; r < P.zero_rows; r += all)
+            for (int64_t c = lane * 16; c < P.zero_bytes; c += 512)
+                *reinterpret_cast<uint4*>(P.zero + r * P.zero_ld + c) = make_uint4(0, 0, 0, 0);
+        return;
+    }
     const int lo = me << P.shift, count = max(0, min(1 << P.shift, P.n - lo));
     const int bins = 1 << P.bits;
     if (P.seen)
@@ -302,8 +313,20 @@ __global__ void __launch_bounds__(TS_NT) k_token_sort(const __grid_constant__ To
     }
 }
 
+// Rows of the table that the sort's launch zeroes on the SMs beside its cluster: as many as its time (9 us for
+// 4000 tokens, 31 for 65536) lets write at 3.5 TB/s.  Rows with a token are written again by the sums; the
+// others are left to k_embed_sum's blocks.  (All of them there: 197 us for 65536 tokens and 131072 rows of 2048
+// bf16 values, 26.5 for 4000 and 8192 of 520 fp32; so 189 and 24.5.)
+static int64_t zeroed_early(const EmbedArgs& A, int64_t es) {
+    const int64_t bytes = A.dim * es;
+    if (A.accumulate || bytes % 16 != 0 || (A.rows > 1 && A.dst_ld * es % 16 != 0)) return 0;
+    const double budget = (8.0 + 0.00035 * (double)A.n) * 3.5e6;
+    const int64_t rows = (int64_t)(budget / (double)bytes) / 32 * 32;
+    return rows >= A.rows ? A.rows : rows;
+}
+
 static cudaError_t token_sort(const EmbedArgs& A, uint32_t* skeys, int32_t* perm, uint32_t* seen, uint32_t* counts,
-                              cudaStream_t st) {
+                              int64_t zero_rows, int64_t es, cudaStream_t st) {
     TokenSort P;
     P.tokens = A.tokens;
     P.tok64 = A.tok64;
@@ -314,6 +337,10 @@ static cudaError_t token_sort(const EmbedArgs& A, uint32_t* skeys, int32_t* perm
     P.seen = seen;
     P.words = (A.rows + 31) / 32;
     P.counts = counts;
+    P.zero = static_cast<unsigned char*>(A.dst);
+    P.zero_rows = zero_rows;
+    P.zero_bytes = A.dim * es;
+    P.zero_ld = A.dst_ld * es;
     int bits = 1;
     while (bits < 31 && (A.rows >> bits) != 0) ++bits;
     P.passes = (bits + 9) / 10;  // as few as 1024 digits allow
@@ -326,7 +353,9 @@ static cudaError_t token_sort(const EmbedArgs& A, uint32_t* skeys, int32_t* perm
     if (e == cudaSuccess) e = blocks_per_sm<&k_token_sort>(dev, TS_NT, sizeof(TokenSortShared), &per);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
+    P.blocks = (int)blocks;
+    const unsigned more = zero_rows ? std::max(1u, ((unsigned)sms - blocks) / blocks) : 0;  // clusters
+    cfg.gridDim = dim3(blocks * (1 + more));
     cfg.blockDim = dim3(TS_NT);
     cfg.dynamicSmemBytes = sizeof(TokenSortShared);
     cfg.stream = st;
@@ -351,6 +380,7 @@ struct EmbedSum {
     int32_t* list;          // [2][tiles]: tiles in which a long run begins; those of many parts
     uint32_t* counts;       // of both
     int64_t sum_blocks, zero_blocks;  // blocks of the sums, and those that zero the rows without a token
+    int64_t zero_from;                // from this row on (a multiple of 8)
 };
 
 template <typename T, typename W, int VN>
@@ -413,7 +443,7 @@ __global__ void __launch_bounds__(SUM_NT) k_embed_sum(const __grid_constant__ Em
         Pack<W, VN> o;
 #pragma unroll
         for (int e = 0; e < VN; ++e) o.v[e] = from_acc<W, typename AccOf<W>::A>(0);
-        for (int64_t r = (z * NW + warp) * 8; r < E.rows; r += P.zero_blocks * NW * 8) {
+        for (int64_t r = P.zero_from + (z * NW + warp) * 8; r < E.rows; r += P.zero_blocks * NW * 8) {
             const uint32_t word = P.seen[r >> 5] >> (r & 31);
             for (int k = 0; k < 8 && r + k < E.rows; ++k) {
                 if (word >> k & 1) continue;
@@ -633,7 +663,7 @@ static cudaError_t embed_sum_launch(EmbedSum S, int sms, bool sorted, cudaStream
     const int64_t cols = (S.A.dim + 32 * (vec ? VN : 1) - 1) / (32 * (vec ? VN : 1));
     constexpr int NW = SUM_NT / 32;
     S.sum_blocks = (S.tiles * cols + NW - 1) / NW;
-    S.zero_blocks = S.A.accumulate ? 0 : std::min<int64_t>((S.A.rows + 8 * NW - 1) / (8 * NW), 16 * (int64_t)sms);
+    S.zero_blocks = S.A.accumulate ? 0 : std::min<int64_t>((S.A.rows - S.zero_from + 8 * NW - 1) / (8 * NW), 16 * (int64_t)sms);
     const int64_t grid = S.sum_blocks + S.zero_blocks;
     if (grid > 0) {
         constexpr size_t ring = (size_t)NW * 2 * SUM_H * 32 * 16;
@@ -672,13 +702,15 @@ cudaError_t embed_bwd_run(laplex_dtype dt, laplex_dtype out_dt, const EmbedArgs&
     void* part = p += Z.seen;
     int32_t* list = (int32_t*)(p += Z.part);
     void* sort = p += Z.list;
-    uint32_t* bits = A.accumulate ? nullptr : seen;
     const int R = embed_tile(A.n, A.dim, (int)elem_bytes(dt));
     const int64_t tiles = (A.n + R - 1) / R;
     uint32_t* counts = (uint32_t*)list + 2 * tiles;
     const bool sorted = A.n > 0 && A.n <= TS_MAX;  // by a kernel of this call
+    const int64_t es = out_dt == LAPLEX_F64 ? 8 : out_dt == LAPLEX_F32 ? 4 : 2;
+    const int64_t early = sorted ? zeroed_early(A, es) : 0;
+    uint32_t* bits = A.accumulate || early == A.rows ? nullptr : seen;
     if (sorted) {
-        e = token_sort(A, skeys, perm, bits, counts, st);
+        e = token_sort(A, skeys, perm, bits, counts, early, es, st);
         if (e != cudaSuccess) return e;
     } else {
         if (bits) e = cudaMemsetAsync(seen, 0, (size_t)((A.rows + 31) / 32) * 4, st);
@@ -701,6 +733,7 @@ cudaError_t embed_bwd_run(laplex_dtype dt, laplex_dtype out_dt, const EmbedArgs&
     S.list = list;
     S.counts = counts;
     S.sum_blocks = S.zero_blocks = 0;
+    S.zero_from = early;
     const bool f32 = out_dt == LAPLEX_F32;
     switch (dt) {
         case LAPLEX_F32: return embed_sum_launch<float, float>(S, sms, sorted, st);

@@ -126,6 +126,19 @@ def test_gradient_of_runs_around_the_tiles(dt, dim):
     assert torch.equal(got, X.embed_backward(torch.from_numpy(t).cuda(), g, rows, scale=0.5))
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,dim,ld", [(300, 64, 72), (300, 64, 67), (90000, 512, 520), (33, 8, 8)])
+def test_gradient_into_a_part_of_wider_rows(dt, rows, dim, ld):
+    # rows zeroed beside the sort, and those zeroed beside the sums
+    t = tokens("padded", 2000, rows)
+    g = values((2000, dim), DT[dt], 6)
+    whole = torch.full((rows + 2, ld), 7.0, dtype=DT[dt], device="cuda")
+    out = whole[:rows, :dim]
+    X.embed_backward(torch.from_numpy(t).cuda(), g, rows, out=out)
+    check_gradient(out, t, g, rows, 1.0, DT[dt], DT[dt])
+    assert bool((whole[rows:] == 7).all()) and bool((whole[:, dim:] == 7).all())
+
+
 @pytest.mark.parametrize("dt,out_dt", [("bf16", "bf16"), ("bf16", "fp32"), ("fp16", "fp32"), ("fp32", "fp32"), ("fp64", "fp64")])
 def test_gradient_accumulates(dt, out_dt):
     n, rows, dim = 700, 90, 40
