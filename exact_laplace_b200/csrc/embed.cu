@@ -354,7 +354,7 @@ static cudaError_t token_sort(const EmbedArgs& A, uint32_t* skeys, int32_t* perm
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     P.blocks = (int)blocks;
-    const unsigned more = zero_rows ? std::max(1u, ((unsigned)sms - blocks) / blocks) : 0;  // clusters
+    const unsigned more = zero_rows ? std::max(1, (sms - (int)blocks) / (int)blocks) : 0;  // clusters
     cfg.gridDim = dim3(blocks * (1 + more));
     cfg.blockDim = dim3(TS_NT);
     cfg.dynamicSmemBytes = sizeof(TokenSortShared);

@@ -461,7 +461,7 @@ struct TcBlock {
             const int d = (d0 + (x % (CH / 32)) * dd) & 127;
             const uint32_t q[4] = {w.x, w.y, w.z, w.w};
             uint32_t a0[4], a1[4];
-            if (!OUT && exact) {
+            if (!OUT && !BF && exact) {  // (bf16: weigh3)
                 // from an fp32 product, what the first part rounds off is the second (and weights below fp16's
                 // smallest still count)
                 const float f = sh.dec[d] * k_up;
