@@ -9,11 +9,15 @@ fallback: a missing or unloadable library raises ``LaplexError``.
 Host (CPU) tensors are accepted by the ``*_host`` helpers, which copy inputs to
 the device, call the same entry point and copy the result back (the end-to-end
 path a user without device buffers takes).
+
+Calls may come from several host threads, on one stream or on several: each
+enqueues its kernels as a whole.
 """
 from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -180,6 +184,21 @@ def _perm(p):
     return p
 
 
+#: held from the workspace's lookup until the call has enqueued its last kernel.  Host threads that share a
+#: stream share its workspace, and the library gives up the interpreter's lock: without this one a call's
+#: kernels could land between the passes of another's.  (One lock for all streams: what it holds up is the
+#: launches alone, some 10 us, while the rest of a call is under the interpreter's lock anyway.)
+_enqueue = threading.RLock()
+
+
+def _serial(call):
+    @functools.wraps(call)
+    def locked(*args, **kwargs):
+        with _enqueue:
+            return call(*args, **kwargs)
+    return locked
+
+
 class Workspace:
     """Device workspace cache (one growing buffer per device and stream).
 
@@ -240,6 +259,7 @@ def device_status(device=None) -> None:
 
 # ----------------------------------------------------------------------------- calls
 
+@_serial
 def sort_anchors(a: torch.Tensor, sorted_out=None, perm_out=None):
     """(sorted, perm): the anchors ascending and the int32 permutation, ties by index."""
     dev = _dev(a, sorted_out, perm_out)
@@ -252,6 +272,7 @@ def sort_anchors(a: torch.Tensor, sorted_out=None, perm_out=None):
     return s, p
 
 
+@_serial
 def sort_anchors_carry(a: torch.Tensor, x: torch.Tensor, sorted_out=None, perm_out=None, xs_out=None):
     """(sorted, perm, xs): the sort of laplex_sort_anchors with x carried along,
     xs[r] = x[perm[r]]."""
@@ -268,6 +289,7 @@ def sort_anchors_carry(a: torch.Tensor, x: torch.Tensor, sorted_out=None, perm_o
     return s, p, xs
 
 
+@_serial
 def matvec_sym_unsorted(a: torch.Tensor, x: torch.Tensor, out=None, sorted_out=None, perm_out=None):
     """(y, sorted, perm): y = K x on anchors and x in the caller's order (one
     column), in one call: the sort carrying x, the product, y back to caller order."""
@@ -284,6 +306,7 @@ def matvec_sym_unsorted(a: torch.Tensor, x: torch.Tensor, out=None, sorted_out=N
     return y, s, p
 
 
+@_serial
 def matvec_sym(sorted_anchors: torch.Tensor, x: torch.Tensor, perm=None, out=None):
     """y = K x for K_ij = exp(-|a_i - a_j|) given the sorted anchors (and perm, if x is
     in the caller's order).  x: [n] or [n, B]."""
@@ -299,6 +322,7 @@ def matvec_sym(sorted_anchors: torch.Tensor, x: torch.Tensor, perm=None, out=Non
     return y
 
 
+@_serial
 def permute(src: torch.Tensor, idx: torch.Tensor, out=None):
     """dst[idx[i]] = src[i] (4- or 8-byte elements, moved as bits); idx int32."""
     dev = _dev(src, _perm(idx), out)
@@ -312,6 +336,7 @@ def permute(src: torch.Tensor, idx: torch.Tensor, out=None):
     return dst
 
 
+@_serial
 def invert_perm(perm: torch.Tensor, out=None):
     """inv with inv[perm[r]] = r (int32)."""
     dev = _dev(_perm(perm), out)
@@ -334,6 +359,7 @@ def matvec_sym_noalloc(sorted_anchors: torch.Tensor, x: torch.Tensor, perm=None,
     return y
 
 
+@_serial
 def matvec_sym_planned(sorted_anchors: torch.Tensor, perm: torch.Tensor, inv: torch.Tensor, x: torch.Tensor,
                        out=None):
     """y = K x for x, y in the caller's order (one column), through the plan
@@ -349,6 +375,7 @@ def matvec_sym_planned(sorted_anchors: torch.Tensor, perm: torch.Tensor, inv: to
     return y
 
 
+@_serial
 def matvec_general(sa, sb, x, pa=None, pb=None, transpose=False, out=None):
     """y = K x (x on the b side) or, with transpose, y = K^T x (x on the a side)."""
     dev = _dev(sa, sb, x, _perm(pa), _perm(pb), out)
@@ -365,6 +392,7 @@ def matvec_general(sa, sb, x, pa=None, pb=None, transpose=False, out=None):
     return y
 
 
+@_serial
 def matvec_phased(sa, phi, x, pa=None, sb=None, psi=None, pb=None, transpose=False, out=None):
     """Phased product, K_ij = exp(-|a_i - b_j|) cos(phi_i - psi_j); sb=None: b = a."""
     dev = _dev(sa, phi, x, _perm(pa), sb, psi, _perm(pb), out)
@@ -380,6 +408,7 @@ def matvec_phased(sa, phi, x, pa=None, sb=None, psi=None, pb=None, transpose=Fal
     return y
 
 
+@_serial
 def gram(sa, v, pa=None, phi=None, D=None, sb=None, pb=None, psi=None, out=None):
     """z = K^T diag(D) K v (D = 1 when None); sb=None: symmetric K."""
     dev = _dev(sa, v, _perm(pa), phi, D, sb, _perm(pb), psi, out)
@@ -393,6 +422,7 @@ def gram(sa, v, pa=None, phi=None, D=None, sb=None, pb=None, psi=None, out=None)
     return z
 
 
+@_serial
 def backward(sorted_anchors, x, g, perm=None, dx_out=None, da_out=None):
     """(dx, da) of L = <g, K x>: dx = K g, da = dL/da (sign(0) = 0 at ties)."""
     dev = _dev(sorted_anchors, x, g, _perm(perm), dx_out, da_out)
@@ -405,6 +435,7 @@ def backward(sorted_anchors, x, g, perm=None, dx_out=None, da_out=None):
     return dx, da
 
 
+@_serial
 def backward_general(sa, sb, x, g, pa=None, pb=None):
     """(dx, da, db) of L = <g, K x>, K_ij = exp(-|a_i - b_j|): dx = K^T g and the
     anchor gradients (sign(0) = 0 at ties).  g, da follow pa; x, dx, db follow pb."""
@@ -420,6 +451,7 @@ def backward_general(sa, sb, x, g, pa=None, pb=None):
     return dx, da, db
 
 
+@_serial
 def backward_phased(sa, phi, x, g, pa=None, sb=None, psi=None, pb=None):
     """Gradients of L = <g, K x>, K_ij = exp(-|a_i - b_j|) cos(phi_i - psi_j).
 
@@ -443,6 +475,7 @@ def backward_phased(sa, phi, x, g, pa=None, sb=None, psi=None, pb=None):
     return (dx, dphi, da) if sym else (dx, dphi, dpsi, da, db)
 
 
+@_serial
 def gram_matrix(sa, sb, D=None, pa=None, pb=None, out=None):
     """M = A diag(D) A^T, A_ij = exp(-|a_i - b_j|), as an [n, n] tensor (rows and
     columns follow pa; sorted order without it).  D follows pb; None means 1."""
@@ -636,7 +669,7 @@ def linattn(q, k, v, log_decay, scale=None, cu_seqlens=None, state=None, return_
     shape = (seqs, s.hkv, s.dk, s.dv)
     _state("state", state, shape, acc)
     _state("state_out", state_out, shape, acc)
-    with _on(dev):
+    with _on(dev), _enqueue:
         if out is None:
             out = _new(q.shape[:-1] + (s.dv,), q.dtype, dev)
         elif out.shape != q.shape[:-1] + (s.dv,):
@@ -668,7 +701,7 @@ def linattn_backward(q, k, v, log_decay, dout, scale=None, cu_seqlens=None, stat
     shape = (seqs, s.hkv, s.dk, s.dv)
     _state("state", state, shape, acc)
     _state("dstate", dstate, shape, acc)
-    with _on(dev):
+    with _on(dev), _enqueue:
         if out is None:
             out = tuple(_new(x.shape, x.dtype, dev) for x in (q, k, v))
         elif any(a.shape != b.shape for a, b in zip(out, (q, k, v))):
@@ -763,7 +796,7 @@ def embed_backward(tokens, g, rows, scale=1.0, out=None, accumulate=False, dtype
     dim, ld = g.shape[1], _table("g", g)
     if accumulate and out is None:
         raise LaplexError(EINVAL, "accumulate needs out")
-    with _on(dev):
+    with _on(dev), _enqueue:
         if out is None:
             out = _new((rows, dim), dtype or g.dtype, dev)
         if out.shape[0] != rows or out.dtype not in (g.dtype, torch.float32):
