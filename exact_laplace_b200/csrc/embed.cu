@@ -464,12 +464,14 @@ __global__ void __launch_bounds__(SUM_NT) k_embed_sum(const __grid_constant__ Em
     if (!entered) p0 = e0;
     p1 = leaves ? p1 : e1;
     if (p0 >= p1) return;
+    // A key or position outside its range counts as no token: a sort whose wait ran out (ST_TIMEOUT) leaves
+    // what was in the workspace before.
     const uint32_t none = (uint32_t)E.rows;
     const bool in = c < E.dim;
     A s[VN];
 #pragma unroll
     for (int e = 0; e < VN; ++e) s[e] = 0;
-    uint32_t cur = P.keys[p0];
+    uint32_t cur = min(P.keys[p0], none);
     A* part = static_cast<A*>(P.part) + tile * 2 * E.dim + c;
     Pack<T, VN>* ring = reinterpret_cast<Pack<T, VN>*>(raw) + warp * 2 * SUM_H * 32 + lane;
     const T* src = static_cast<const T*>(E.src) + c;
@@ -480,8 +482,8 @@ __global__ void __launch_bounds__(SUM_NT) k_embed_sum(const __grid_constant__ Em
     const auto fetch = [&](int h, uint32_t& k, int32_t& i) {
         const int64_t p = p0 + (int64_t)h * SUM_H + lane;
         const bool has = lane < SUM_H && h < halves && p < p1;
-        k = has ? P.keys[p] : none;
         i = has ? P.perm[p] : 0;
+        k = has && (uint32_t)i < (uint32_t)E.n ? min(P.keys[p], none) : none;
     };
     const auto start = [&](int h, uint32_t k, int32_t i) {
         if constexpr (RING) {
@@ -562,7 +564,8 @@ __global__ void __launch_bounds__(EMB_NT) k_embed_join(const __grid_constant__ E
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t pieces = (E.dim + 32 * VN - 1) / (32 * VN);
     const int64_t few = P.counts[0] * pieces, many = P.counts[1] * pieces;
-    // the run that begins in `tile`: its key and parts (by a whole warp)
+    // the run that begins in `tile`: its key and parts (by a whole warp).  (k_embed_sum lists a tile only by a key
+    // of a row; keys that do not ascend give other parts, but no tile past the last.)
     const auto find = [&](int64_t tile, uint32_t* key) -> int64_t {
         const uint32_t k = P.keys[(tile + 1) * P.R - 1];
         *key = k;
