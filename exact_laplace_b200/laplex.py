@@ -202,18 +202,22 @@ def _serial(call):
 class Workspace:
     """Device workspace cache (one growing buffer per device and stream).
 
-    The header is zeroed when the buffer is (re)allocated; the library then keeps
-    its sticky status word there.  ``status()`` synchronises and reports it."""
+    The header is zeroed when a stream's first buffer is allocated, and goes along
+    into a larger one; the library keeps its sticky status word there.
+    ``status()`` synchronises and reports it."""
 
     _cache: dict = {}
 
     @classmethod
     def get(cls, device, nbytes: int) -> "torch.Tensor":
         key = (device, torch.cuda.current_stream(device).cuda_stream)
-        buf = cls._cache.get(key)
-        if buf is None or buf.numel() < nbytes:
-            buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-            cls._cache[key] = buf
+        old = cls._cache.get(key)
+        if old is not None and old.numel() >= nbytes:
+            return old
+        buf = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        if old is not None and not torch.cuda.is_current_stream_capturing():
+            buf[:256].copy_(old[:256])  # the status of the calls before, in the stream's order
+        cls._cache[key] = buf
         return buf
 
     @classmethod
