@@ -132,15 +132,18 @@ laplex_status check_ws(laplex_op op, int64_t n, int64_t k, int64_t B, laplex_dty
 }
 
 void* ws_body(void* ws) { return static_cast<char*>(ws) + lx::HEADER_BYTES; }
-uint32_t* ws_status(void* ws) { return static_cast<uint32_t*>(ws); }
+uint32_t* ws_status(void* ws) { return lx::status_word(ws); }
 
 }  // namespace
 
 namespace {
 thread_local lx::ProfileEvents g_prof = {nullptr, nullptr};
+thread_local uint32_t* g_status_word = nullptr;
 }
 
 const lx::ProfileEvents& lx::profile_events() { return g_prof; }
+
+uint32_t* lx::status_word(void* ws) { return g_status_word ? g_status_word : static_cast<uint32_t*>(ws); }
 
 void lx::set_last_error(const char* fmt, ...) {
     va_list ap;
@@ -178,6 +181,12 @@ const char* laplex_last_error(void) { return g_err; }
 laplex_status laplex_set_profile_events(void* before, void* after) {
     g_prof.before = (cudaEvent_t)before;
     g_prof.after = (cudaEvent_t)after;
+    return ok();
+}
+
+laplex_status laplex_set_status_word(void* word) {
+    REQ(aligned(word, 4), "the status word is not aligned");
+    g_status_word = static_cast<uint32_t*>(word);
     return ok();
 }
 

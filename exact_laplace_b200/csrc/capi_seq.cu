@@ -237,7 +237,7 @@ laplex_status laplex_linattn(const laplex_linattn_shape* shape, const laplex_row
     TRY(check_ws(ws, ws_bytes, linattn_body(s, LAPLEX_LINATTN_FORWARD)));
     if (s.seqs == 0) return done(cudaSuccess, "");
     cudaStream_t st = (cudaStream_t)stream;
-    uint32_t* status = static_cast<uint32_t*>(ws);
+    uint32_t* status = lx::status_word(ws);
     const lx::LinSeqs S = make_seqs(s, segment(s, false));
     lx::LinRole R = role(rq, rk, rv, s.hq / s.hkv, 1, s.dk, s.dv, false, false, s.scale, 1.0);
     R.o = const_cast<void*>(ro.p);
@@ -286,7 +286,7 @@ laplex_status laplex_linattn_backward(const laplex_linattn_shape* shape, const l
     cudaStream_t st = (cudaStream_t)stream;
     char* body = static_cast<char*>(ws) + lx::HEADER_BYTES;
     const int G = s.hq / s.hkv;
-    uint32_t* status = static_cast<uint32_t*>(ws);
+    uint32_t* status = lx::status_word(ws);
     const lx::LinSeqs S = make_seqs(s, segment(s, true));
     cudaError_t e = cudaSuccess;
     if (dlog_decay) {
@@ -450,7 +450,7 @@ laplex_status laplex_embed_backward(const void* tokens, int token_bytes, int64_t
     A.scale = scale;
     A.accumulate = accumulate != 0;
     return done(lx::embed_bwd_run(dt, out_dt, A, static_cast<char*>(ws) + lx::HEADER_BYTES, ws_bytes - lx::HEADER_BYTES,
-                                  static_cast<uint32_t*>(ws), (cudaStream_t)stream),
+                                  lx::status_word(ws), (cudaStream_t)stream),
                 "laplex_embed_backward");
 }
 

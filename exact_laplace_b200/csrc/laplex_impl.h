@@ -7,13 +7,17 @@
 
 namespace lx {
 
-// sticky device status bits, kept in the first word of the workspace header
+// sticky device status bits, kept in the first word of the workspace header (status_word)
 constexpr uint32_t ST_NONFINITE = 1u;
 constexpr uint32_t ST_TIMEOUT = 2u;
 constexpr size_t HEADER_BYTES = 256;
 
 // Sets the calling thread's message returned by laplex_last_error() (capi.cu).
 void set_last_error(const char* fmt, ...);
+
+// Where a call on workspace ws records device errors: the calling thread's word
+// (laplex_set_status_word), or the workspace's header (capi.cu).
+uint32_t* status_word(void* ws);
 
 // Optional events recorded around a call's dominant kernel (capi.cu, thread-local).
 struct ProfileEvents {

@@ -96,6 +96,7 @@ SIGNATURES = {
                            ctypes.c_int),
     "laplex_matvec_sym_noalloc": ([_P, _P, _I64, _P, _P, _P], ctypes.c_int),
     "laplex_set_profile_events": ([_P, _P], ctypes.c_int),
+    "laplex_set_status_word": ([_P], ctypes.c_int),
     "laplex_test_set_sort_wait": ([ctypes.c_uint32, ctypes.c_int], ctypes.c_int),
     "laplex_permute": ([_P, _P, _I64, ctypes.c_int, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "laplex_invert_perm": ([_P, _I64, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
@@ -188,7 +189,26 @@ def _perm(p):
 #: stream share its workspace, and the library gives up the interpreter's lock: without this one a call's
 #: kernels could land between the passes of another's.  (One lock for all streams: what it holds up is the
 #: launches alone, some 10 us, while the rest of a call is under the interpreter's lock anyway.)
-_enqueue = threading.RLock()
+class _Enqueue:
+    def __init__(self):
+        self._lock = threading.RLock()
+        self._elsewhere = False  # this call reports to a word of its own
+
+    def __enter__(self):
+        self._lock.acquire()
+
+    def report_to(self, word):
+        _check(lib().laplex_set_status_word(word.data_ptr()))
+        self._elsewhere = True
+
+    def __exit__(self, *exc):
+        if self._elsewhere:
+            self._elsewhere = False
+            lib().laplex_set_status_word(None)
+        self._lock.release()
+
+
+_enqueue = _Enqueue()
 
 
 def _serial(call):
@@ -203,10 +223,12 @@ class Workspace:
     """Device workspace cache (one growing buffer per device and stream).
 
     The header is zeroed when a stream's first buffer is allocated, and goes along
-    into a larger one; the library keeps its sticky status word there.
-    ``status()`` synchronises and reports it."""
+    into a larger one; the library keeps its sticky status word there.  Calls
+    captured into a graph in memory of the graph's own share one word per device.
+    ``status()`` synchronises and reports both."""
 
     _cache: dict = {}
+    _words: dict = {}
 
     @classmethod
     def get(cls, device, nbytes: int) -> "torch.Tensor":
@@ -221,12 +243,34 @@ class Workspace:
         return buf
 
     @classmethod
+    def captured_word(cls, device) -> "torch.Tensor":
+        """The status word of captured calls, while one is captured."""
+        word = cls._words.get(device)
+        if word is None:
+            word = torch.empty(64, dtype=torch.int32, device=device)
+            side = torch.cuda.Stream(device)  # (a memset inside the graph would run at every replay)
+            while _capturing(side):
+                side = torch.cuda.Stream(device)
+            _check(lib().laplex_workspace_init(word.data_ptr(), 256, side.cuda_stream))
+            cls._words[device] = word
+        return word
+
+    @classmethod
     def status(cls, device=None) -> None:
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
         key = (device, torch.cuda.current_stream(device).cuda_stream)
         buf = cls._cache.get(key)
         if buf is not None:
             _check(lib().laplex_get_device_status(_ptr(buf), _stream(device)))
+        word = cls._words.get(device)
+        if word is not None:
+            torch.cuda.synchronize(device)  # (replays may be on any stream)
+            _check(lib().laplex_get_device_status(_ptr(word), _stream(device)))
+
+
+def _capturing(stream) -> bool:
+    with torch.cuda.stream(stream):
+        return torch.cuda.is_current_stream_capturing()
 
 
 def workspace_size(op: int, n: int, k: int = 0, B: int = 1, dtype=torch.float32) -> int:
@@ -257,7 +301,8 @@ def test_set_sort_wait(polls: int = 0, force_expiry: bool = False) -> None:
 
 
 def device_status(device=None) -> None:
-    """Synchronise and raise if a kernel recorded a device-side error."""
+    """Synchronise and raise if a kernel recorded a device-side error: in a call on
+    the current stream, or in a captured call of a sequence operator on any stream."""
     Workspace.status(device)
 
 
@@ -625,14 +670,16 @@ def _seqs(q, cu):
 def _seq_ws(dev, raw, nbytes):
     """Workspace of a sequence operator on stream `raw`: the stream's, or while a
     graph is captured one of the graph's own memory (the stream's may be replaced
-    by a larger one while the graph lives, and two graphs may run at the same time)."""
+    by a larger one while the graph lives, and two graphs may run at the same time).
+    The graph may hand that memory to its later calls, so the call's status goes
+    to a word outside it."""
     if not torch.cuda.is_current_stream_capturing():
         buf = Workspace._cache.get((dev, raw))
         if buf is None or buf.numel() < nbytes:
             buf = Workspace.get(dev, nbytes)
     else:
         buf = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        _check(lib().laplex_workspace_init(buf.data_ptr(), nbytes, raw))
+        _enqueue.report_to(Workspace.captured_word(dev))
     return buf
 
 

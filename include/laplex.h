@@ -41,7 +41,8 @@
  *    with earlier kernels of the call possibly enqueued; laplex_last_error()
  *    then holds a message.  Errors found on the device (a non-finite anchor, an
  *    inter-block wait that ran out) are recorded in the workspace header and
- *    reported by laplex_get_device_status.  No call aborts or throws.
+ *    reported by laplex_get_device_status (laplex_set_status_word records them
+ *    elsewhere).  No call aborts or throws.
  */
 #ifndef LAPLEX_H
 #define LAPLEX_H
@@ -341,6 +342,17 @@ laplex_status laplex_gram_matrix(const void* sa, const int32_t* pa, int64_t n, c
  * Host-only bookkeeping; no synchronisation.  Returns LAPLEX_OK.
  */
 laplex_status laplex_set_profile_events(void* before, void* after);
+
+/*
+ * Where device errors go.  For the following calls on the calling thread that
+ * take a workspace: they are recorded in `word` (4 bytes of device memory,
+ * aligned to 4, zeroed by the caller) in place of the workspace's header, and
+ * laplex_get_device_status(word, stream) reports and clears them.  For calls
+ * captured into a graph whose workspace is memory of the graph, which other
+ * work may take over between replays.  The word has to outlive what was
+ * enqueued or captured.  NULL: the header again.  Host-only bookkeeping.
+ */
+laplex_status laplex_set_status_word(void* word);
 
 /*
  * Test hook for the bounded waits (no counterpart in the paper).  For the
