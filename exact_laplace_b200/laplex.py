@@ -683,7 +683,13 @@ def _seq_ws(dev, raw, nbytes):
     return buf
 
 
-_ws_sizes: dict = {}  # workspace bytes by shape
+_ws_sizes: dict = {}  # workspace bytes by shape; at most 4096 of them
+
+
+def _keep_size(key, nbytes):
+    if len(_ws_sizes) >= 4096:
+        _ws_sizes.clear()
+    _ws_sizes[key] = nbytes
 
 
 def _linattn_ws(s, call, dev, raw):
@@ -693,9 +699,7 @@ def _linattn_ws(s, call, dev, raw):
         out = ctypes.c_size_t(0)
         _check(lib().laplex_linattn_workspace_size(ctypes.byref(s), call, ctypes.byref(out)))
         nbytes = out.value
-        if len(_ws_sizes) >= 4096:
-            _ws_sizes.clear()
-        _ws_sizes[key] = nbytes
+        _keep_size(key, nbytes)
     return _seq_ws(dev, raw, nbytes)
 
 
@@ -857,7 +861,8 @@ def embed_backward(tokens, g, rows, scale=1.0, out=None, accumulate=False, dtype
         if nbytes is None:
             size = ctypes.c_size_t(0)
             _check(lib().laplex_embed_backward_workspace_size(*key, ctypes.byref(size)))
-            nbytes = _ws_sizes[key] = size.value
+            nbytes = size.value
+            _keep_size(key, nbytes)
         raw = _raw_stream(dev)
         ws = _seq_ws(dev, raw, nbytes)
         _check(lib().laplex_embed_backward(tokens.data_ptr(), tb, tokens.numel(), g.data_ptr(), ld, rows, dim,
