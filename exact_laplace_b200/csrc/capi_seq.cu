@@ -342,6 +342,11 @@ laplex_status laplex_linattn_backward(const laplex_linattn_shape* shape, const l
     return done(e, "laplex_linattn_backward");
 }
 
+laplex_status laplex_test_set_linattn_wait(uint32_t polls, int force_expiry) {
+    lx::set_linattn_wait(polls, force_expiry);
+    return done(cudaSuccess, "");
+}
+
 laplex_status laplex_linattn_step(const laplex_linattn_shape* shape, const laplex_rows* q, const laplex_rows* k,
                                   const laplex_rows* v, void* states, int64_t num_slots, const int32_t* slots,
                                   const laplex_rows* o, void* stream) {

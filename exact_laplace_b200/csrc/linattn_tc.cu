@@ -87,6 +87,8 @@ struct alignas(64) TcArgs {
     int H, nroles;
     const float* lam;
     uint32_t* status;
+    uint32_t polls;    // bound of each wait
+    int force_expiry;  // test hook: every block's first copy of K and V is never issued
     TcRole role[3];
 };
 
@@ -101,6 +103,7 @@ struct TcShared {
     uint64_t p_ready, o_read;                          // from the rows warps
     uint64_t k_max, s_max, p_max[4];                   // fp16: maxima exchanged among the state warps, in a pair of rows warps
     uint64_t drain;      // after a wait that ran out
+    int kv_phase[2], q_phase;  // the last phase of kv_full and q_full whose copies were issued, or -1
     uint32_t tmem;
     uint32_t dead;       // a wait ran out
     alignas(16) float grow[16];  // e^{lam j}, 16 columns of P towards the row's end
@@ -254,7 +257,7 @@ struct TcBlock {
     // bounded; false once any wait of the block has run out
     __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity) const {
         if (mbar_test(bar, parity & 1)) return true;
-        for (uint32_t it = 0; it < MBAR_POLLS; ++it) {
+        for (uint32_t it = 0; it < A.polls; ++it) {
             if (mbar_sleep(bar, parity & 1)) return true;
             if ((it & 15) == 15 && *(volatile uint32_t*)&sh.dead) return false;
         }
@@ -282,6 +285,7 @@ struct TcBlock {
         const int head = h * nk + i % nk;
         uint64_t* bar = &sh.kv_full[i % NS];
         if (elect()) {
+            sh.kv_phase[i % NS] = i / NS;
             mbar_expect_tx(bar, Z::KBY + Z::VBY);
             for (int b = 0; b < DK / 64; ++b)
                 tma_load3(sm + Z::K + (i % NS) * Z::KBY + b * TB, &A.map[R.mk], b * 64, head, (int)a, bar);
@@ -295,6 +299,7 @@ struct TcBlock {
         int n;
         const int64_t a = chunk_at(i / nq, &n);
         if (elect()) {
+            sh.q_phase = i;
             mbar_expect_tx(&sh.q_full, Z::KBY);
             for (int b = 0; b < DK / 64; ++b)
                 tma_load3(sm + Z::Q + b * TB, &A.map[R.mq], b * 64, h * nq + i % nq, (int)a, &sh.q_full);
@@ -311,7 +316,7 @@ struct TcBlock {
         __syncwarp();
     }
     __device__ __forceinline__ void issue() const {
-        load_kv(0);
+        if (!A.force_expiry) load_kv(0);
         if (OUT) load_q(0);
         for (int i = 1; i < NS; ++i) load_kv(i);
         bool has_state = R.state_in != nullptr;
@@ -1028,6 +1033,7 @@ __device__ __forceinline__ void lin_block(const TcArgs& A, int block, unsigned c
         for (uint64_t* b : {&sh.v_ready[0], &sh.v_ready[1], &sh.k_ready[0], &sh.k_ready[1], &sh.s_ready, &sh.p_ready, &sh.o_read, &sh.k_max, &sh.s_max})
             mbar_init(b, TC_GROUP / 32);
         for (uint64_t& b : sh.p_max) mbar_init(&b, 2);
+        sh.kv_phase[0] = sh.kv_phase[1] = sh.q_phase = -1;
         sh.dead = 0;
         fence_proxy_async();
     }
@@ -1082,15 +1088,19 @@ __device__ __forceinline__ void lin_block(const TcArgs& A, int block, unsigned c
     tc_fence_before();
     __syncthreads();
     if (sh.dead) {
-        // a copy or a product did not come: report it, and let those in flight end (within a bound; a phase is
-        // named by its parity, so both are waited for, and one of them may not come)
+        // a copy or a product did not come: report it, and let what is in flight end (within a bound): the products,
+        // the last copies issued to each buffer (those before them have been waited for), stores to tensor memory
         if (tid / 32 == ISSUE) B.commit(&sh.drain);
         if (tid == 0) {
             set_status(A.status, ST_TIMEOUT);
-            for (uint64_t* b : {&sh.kv_full[0], &sh.kv_full[1], &sh.q_full})
-                for (uint32_t parity = 0; parity < 2; ++parity) mbar_wait(b, parity);
+            for (int s = 0; s < 2; ++s)
+                if (sh.kv_phase[s] >= 0) mbar_wait(&sh.kv_full[s], sh.kv_phase[s] & 1);
+            if (sh.q_phase >= 0) mbar_wait(&sh.q_full, sh.q_phase & 1);
             mbar_wait(&sh.drain, 0);
         }
+        __syncwarp();
+        tmem_wait_st();
+        tc_fence_before();
         __syncthreads();
     }
     if (tid / 32 == ISSUE) {
@@ -1116,6 +1126,14 @@ __global__ void __launch_bounds__(TcSize<DK, DV, true>::NT, 1) k_lin_pair(const 
 }
 
 // ---------------------------------------------------------------- host side
+
+static thread_local uint32_t g_tc_polls = MBAR_POLLS;
+static thread_local int g_tc_force_expiry = 0;
+
+void set_linattn_wait(uint32_t polls, int force_expiry) {
+    g_tc_polls = polls ? polls : MBAR_POLLS;
+    g_tc_force_expiry = force_expiry;
+}
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -1250,6 +1268,8 @@ static cudaError_t tc_args(laplex_dtype dt, const LinRole* roles, int count, boo
     A.H = H;
     A.lam = static_cast<const float*>(lam);
     A.status = status;
+    A.polls = g_tc_polls;
+    A.force_expiry = g_tc_force_expiry;
     struct { LinRows x; int dim, heads; } key[4];
     int maps = 0, dk = 0, dv = 0;
     for (int j = 0; j < count; ++j) {

@@ -109,6 +109,10 @@ cudaError_t tc_run(laplex_dtype dt, const LinRole* roles, int count, const LinRo
 cudaError_t tc_states(laplex_dtype dt, const LinRole* roles, int count, const LinSeqs& S, int H, const void* lam,
                       uint32_t* status, cudaStream_t st);
 
+// bound of each wait inside the calling thread's later products and state passes (0: the default, 2^20
+// polls), and a test switch under which a block's first copy is never issued
+void set_linattn_wait(uint32_t polls, int force_expiry);
+
 // ---- single tokens (linattn_step.cu)
 struct LinStep {
     LinRows q, k, v;

@@ -110,6 +110,7 @@ SIGNATURES = {
     "laplex_linattn": ([_S, _R, _R, _R, _P, _R, _P, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "laplex_linattn_backward": ([_S, _R, _R, _R, _R, _P, _P, _R, _R, _R, _P, _P, _P, ctypes.c_size_t, _P],
                                 ctypes.c_int),
+    "laplex_test_set_linattn_wait": ([ctypes.c_uint32, ctypes.c_int], ctypes.c_int),
     "laplex_linattn_step": ([_S, _R, _R, _R, _P, _I64, _P, _R, _P], ctypes.c_int),
     "laplex_embed": ([_P, _I64, _I64, _I64, _P, ctypes.c_int, _I64, ctypes.c_double, _P, _I64, ctypes.c_int, _P],
                      ctypes.c_int),
@@ -298,6 +299,12 @@ def test_set_sort_wait(polls: int = 0, force_expiry: bool = False) -> None:
     """Test hook: bound of the sort's look-back waits on this thread (0: the
     default) and whether every wait is made to run to that bound."""
     _check(lib().laplex_test_set_sort_wait(polls, 1 if force_expiry else 0))
+
+
+def test_set_linattn_wait(polls: int = 0, force_expiry: bool = False) -> None:
+    """Test hook: bound of the waits in linattn's and linattn_backward's kernels of
+    16-bit rows on this thread (0: the default) and whether they are made to run out."""
+    _check(lib().laplex_test_set_linattn_wait(polls, 1 if force_expiry else 0))
 
 
 def device_status(device=None) -> None:

@@ -500,6 +500,17 @@ laplex_status laplex_linattn_backward(const laplex_linattn_shape* shape, const l
                                       size_t ws_bytes, void* stream);
 
 /*
+ * Test hook for the bounded waits of laplex_linattn and laplex_linattn_backward
+ * on 16-bit rows, as laplex_test_set_sort_wait for the sort's: `polls` bounds
+ * every wait inside the kernels (0 restores the default, 2^20 polls), and a
+ * non-zero `force_expiry` leaves the first copy of K and V of every block
+ * unissued, so that the waits for it run to the bound.  The device status is
+ * then LAPLEX_ETIMEOUT, the outputs are unspecified, and nothing is written
+ * outside them.  Host-only bookkeeping.  Returns LAPLEX_OK.
+ */
+laplex_status laplex_test_set_linattn_wait(uint32_t polls, int force_expiry);
+
+/*
  * One token per row against a cache of states, updated in place (no workspace).
  *   shape: tokens rows (seqs and cu_seqlens ignored).
  *   states [num_slots, hkv, dk, dv]: in and out.

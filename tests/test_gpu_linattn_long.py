@@ -39,7 +39,6 @@ def whole_numbers(c, seed):
     c.q, c.k, c.v, c.do = (few(x) for x in (c.q, c.k, c.v, c.do))
     if c.s0 is not None:
         c.s0, c.ds = (torch.randint(-3, 4, x.shape, generator=g).to(x.dtype).cuda() for x in (c.s0, c.ds))
-    c.lam.zero_()
     c.scale = 1.0
 
 
