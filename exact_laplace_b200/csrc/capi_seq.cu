@@ -86,7 +86,7 @@ laplex_status check_rows(const char* name, const laplex_rows* r, int64_t tokens,
     return LAPLEX_OK;
 }
 
-laplex_status check_state(const char* name, const void* p, laplex_dtype) {
+laplex_status check_state(const char* name, const void* p) {
     REQ(aligned(p, 16), "%s is not 16-byte aligned", name);
     return LAPLEX_OK;
 }
@@ -232,8 +232,8 @@ laplex_status laplex_linattn(const laplex_linattn_shape* shape, const laplex_row
     TRY(check_rows("k", k, s.tokens, s.hkv, s.dk, s.dtype, false, &rk));
     TRY(check_rows("v", v, s.tokens, s.hkv, s.dv, s.dtype, false, &rv));
     TRY(check_rows("o", o, s.tokens, s.hq, s.dv, s.dtype, true, &ro));
-    TRY(check_state("state_in", state_in, s.dtype));
-    TRY(check_state("state_out", state_out, s.dtype));
+    TRY(check_state("state_in", state_in));
+    TRY(check_state("state_out", state_out));
     TRY(check_ws(ws, ws_bytes, linattn_body(s, LAPLEX_LINATTN_FORWARD)));
     if (s.seqs == 0) return done(cudaSuccess, "");
     cudaStream_t st = (cudaStream_t)stream;
@@ -277,9 +277,9 @@ laplex_status laplex_linattn_backward(const laplex_linattn_shape* shape, const l
     if (dq) TRY(check_rows("dq", dq, s.tokens, s.hq, s.dk, s.dtype, true, &rdq));
     if (dk) TRY(check_rows("dk", dk, s.tokens, s.hkv, s.dk, s.dtype, true, &rdk));
     if (dv) TRY(check_rows("dv", dv, s.tokens, s.hkv, s.dv, s.dtype, true, &rdv));
-    TRY(check_state("state_in", state_in, s.dtype));
-    TRY(check_state("dstate_out", dstate_out, s.dtype));
-    TRY(check_state("dstate_in", dstate_in, s.dtype));
+    TRY(check_state("state_in", state_in));
+    TRY(check_state("dstate_out", dstate_out));
+    TRY(check_state("dstate_in", dstate_in));
     REQ(dstate_in == nullptr || (dstate_in != dstate_out && dstate_in != state_in), "dstate_in overlaps an input");
     REQ(aligned(dlog_decay, lx::acc_bytes(s.dtype)), "dlog_decay is not aligned");
     TRY(check_ws(ws, ws_bytes, linattn_body(s, dlog_decay ? LAPLEX_LINATTN_BACKWARD_DECAY : LAPLEX_LINATTN_BACKWARD)));
@@ -359,7 +359,7 @@ laplex_status laplex_linattn_step(const laplex_linattn_shape* shape, const laple
     TRY(check_rows("o", o, s.tokens, s.hq, s.dv, s.dtype, true, &ro));
     REQ(num_slots >= 0 && num_slots < MAXN, "num_slots = %lld out of range [0, 2^31)", (long long)num_slots);
     REQ(states != nullptr || num_slots == 0, "states is NULL");
-    TRY(check_state("states", states, s.dtype));
+    TRY(check_state("states", states));
     REQ(slots != nullptr || s.tokens <= num_slots, "%lld rows for %lld states", (long long)s.tokens, (long long)num_slots);
     REQ(aligned(slots, 4), "slots is not aligned");
     lx::LinStep P;

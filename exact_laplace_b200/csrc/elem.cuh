@@ -26,7 +26,7 @@ template <typename T> struct VecOf { static constexpr int N = 16 / (int)sizeof(T
 // N elements of T, moved in accesses of at most 16 bytes
 template <typename T, int N> struct alignas(sizeof(T) * N < 16 ? sizeof(T) * N : 16) Pack { T v[N]; };
 
-// The kernels of one call follow one another by programmatic launches (launch_next):
+// The kernels of one call follow one another by programmatic launches (launch in seqop.h):
 // a kernel is placed on the SMs while the last blocks of the one before still run.
 // Its first statement waits for that kernel's end and its writes; then the next one
 // may be placed.  (Without such a launch before or after, both do nothing.)

@@ -403,9 +403,6 @@ __device__ __forceinline__ void embed_write(const EmbedArgs& A, int64_t row, int
 // positions past p: its parts are joined later.  A short one belongs to the tile before p, and
 // *end is where it ends (p: no run crosses).
 constexpr int SUM_H = 16;
-__device__ __forceinline__ bool long_run(const uint32_t* keys, int64_t p, int64_t n) {
-    return p > 0 && p + SUM_H < n && keys[p - 1] == keys[p + SUM_H];  // (keys ascend)
-}
 __device__ __forceinline__ bool border(const uint32_t* keys, int64_t p, int64_t n, int lane, int64_t* end) {
     *end = min(p, n);
     if (p <= 0 || p >= n) return false;

@@ -820,7 +820,7 @@ struct TcBlock {
     // reach them; 8 columns at a time.  (In the chunk of the first such token: afterwards it is
     // in the state.)
     __device__ __forceinline__ void repair(uint32_t O1, uint32_t O2, T* out, int64_t a, int n, int row, int wg, int head,
-                                           bool has_state, float w1, float w2) const {
+                                           bool has_state, float w2) const {
         const T* qr = static_cast<const T*>(R.q) + (a + row) * R.q_ts + (int64_t)(h * nq + head) * R.q_hs;
 #pragma unroll 1
         for (int cb = 0; cb < HV && wg * HV + cb < R.dv; cb += 8) {
@@ -1000,7 +1000,7 @@ struct TcBlock {
                         }
                     }
                     if (__any_sync(FULL, in && (odd & 0x7fff7fffu) != 0))
-                        repair(O1, O2, out, a, n, row, wg, nq > 1 ? i : 0, has_state, w1, w2);
+                        repair(O1, O2, out, a, n, row, wg, nq > 1 ? i : 0, has_state, w2);
                 }
                 tc_fence_before();
                 arrive(&sh.o_read);
