@@ -722,6 +722,11 @@ def linattn(q, k, v, log_decay, scale=None, cu_seqlens=None, state=None, return_
     (unset where this call made the output).  state [seqs, hkv, dk, dv]: the
     states before the first tokens.  scale: dk ** -0.5 by default.
 
+    Expanded tensors (a stride of 0) are refused: pass a copy.  16-bit rows take
+    one rounding more than the output's own inside the products; the same rows
+    in float32 take none.  No autograd graph is recorded, whatever the inputs
+    require: the gradients are linattn_backward's.
+
     Returns o, or (o, states behind the last tokens) with return_state or
     state_out (which may be `state` itself)."""
     dev = _seq_dev(q, k, v, log_decay, cu_seqlens, state, out, state_out)
@@ -749,8 +754,8 @@ def linattn_backward(q, k, v, log_decay, dout, scale=None, cu_seqlens=None, stat
                      return_dstate=None, return_dlog_decay=False, out=None):
     """Gradients of <dout, o> + <dstate, states behind the last tokens> of linattn.
 
-    Arguments as in linattn; dout [tokens, hq, dv], dstate [seqs, hkv, dk, dv] or
-    None (zero).  Returns LinattnGrads(dq, dk, dv, dstate, dlog_decay): dstate,
+    Arguments as in linattn; dout [tokens, hq, dv] (the expanded gradient of a sum
+    as a copy), dstate [seqs, hkv, dk, dv] or None (zero).  Returns LinattnGrads(dq, dk, dv, dstate, dlog_decay): dstate,
     the gradient of `state`, where return_dstate is set (by default where `state`
     is given), dlog_decay [hkv] where return_dlog_decay is set.  out: (dq, dk,
     dv) to write into."""
@@ -789,7 +794,7 @@ def linattn_step(q, k, v, log_decay, states, slots=None, scale=None, out=None):
     hkv, dk, dv] (float32; float64 for float64 rows).  slots: int32 [rows], the
     state of each row (None: row n uses state n); a row whose slot is outside
     the cache gets zeros, rows that name one slot are applied in row order.
-    Returns o [rows, hq, dv]."""
+    Returns o [rows, hq, dv].  No autograd graph is recorded."""
     dev = _seq_dev(q, k, v, log_decay, states, slots, out)
     if q.dim() != 3:
         raise LaplexError(EINVAL, "q must be [rows, heads, dim]")
@@ -825,7 +830,8 @@ def _table(name, x, dim=None):
 def embed(table, tokens, scale=1.0, out=None):
     """scale * table[tokens]: [*tokens.shape, dim]; a row of zeros for a token
     outside the table (padding).  table [rows, dim] of float16, bfloat16,
-    float32 or float64; tokens int32 or int64."""
+    float32 or float64; tokens int32 or int64.  No autograd graph is recorded:
+    the table's gradient is embed_backward's."""
     dev = _seq_dev(table, tokens, out)
     dt, tb, ld = _seq_dt(table, out), _tokens(tokens), _table("table", table)
     shape = tokens.shape + (table.shape[1],)

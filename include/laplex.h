@@ -416,7 +416,8 @@ laplex_status laplex_matvec_sym_noalloc(const float* sorted, const int32_t* perm
  *    16-bit rows: products of 16-bit values summed in fp32; inside a block of
  *    tokens the weights e^{lam (t - s)} <q_t, k_s> and the state that q_t reads
  *    are rounded once to the rows' type (fp16: times a power of two that keeps
- *    them in its range); the states that go on and leave are fp32.  Long
+ *    them in its range), one rounding more than the output's own; rows converted
+ *    to fp32 take none.  The states that go on and leave are fp32.  Long
  *    sequences are cut into segments by a rule on the sizes and on whether
  *    cu_seqlens is NULL, so the last bits of a result may differ between the two
  *    ways to pass the same lengths.  The same call gives the same bits.
@@ -428,8 +429,9 @@ laplex_status laplex_matvec_sym_noalloc(const float* sorted, const int32_t* perm
  *    outside the tensors.)
  *  - hq q-heads share hkv k/v-heads in groups of hq / hkv (at most 32); decay
  *    and state belong to the k/v-head.  dk, dv: multiples of 8 up to 128.
- *  - Strides are in elements and at least dim; rows start on 16 bytes.  Integer
- *    arrays need only the alignment of their elements.
+ *  - Strides are in elements and at least dim (0, an expanded tensor's, is
+ *    refused); rows start on 16 bytes.  Integer arrays need only the alignment
+ *    of their elements.
  *  - A token never reaches an earlier output: NaN and Inf in row s of k or v
  *    leave the rows t < s of o as they are.  Of the rows t >= s they may make
  *    any NaN (with 16-bit rows also where the definition gives Inf).
