@@ -314,9 +314,11 @@ __global__ void __launch_bounds__(TS_NT) k_token_sort(const __grid_constant__ To
 }
 
 // Rows of the table that the sort's launch zeroes on the SMs beside its cluster: as many as its time (9 us for
-// 4000 tokens, 31 for 65536) lets write at 3.5 TB/s.  Rows with a token are written again by the sums; the
-// others are left to k_embed_sum's blocks.  (All of them there: 197 us for 65536 tokens and 131072 rows of 2048
-// bf16 values, 26.5 for 4000 and 8192 of 520 fp32; so 189 and 24.5.)
+// 4000 tokens, 31 for 65536, in the two digits of 1024 to 2^20 rows) lets write at 3.5 TB/s.  (The sort alone,
+// in one, two and three digits: 7.4, 10.2, 12.5 us for 4000 tokens, 17, 29, 39 for 65536.  The line is for two:
+// a table of one digit is mostly zeroed as a whole, one of three leaves a fifth of the time unused.)  Rows with
+// a token are written again by the sums; the others are left to k_embed_sum's blocks.  (All of them there: 197 us
+// for 65536 tokens and 131072 rows of 2048 bf16 values, 26.5 for 4000 and 8192 of 520 fp32; so 189 and 24.5.)
 static int64_t zeroed_early(const EmbedArgs& A, int64_t es) {
     const int64_t bytes = A.dim * es;
     if (A.accumulate || bytes % 16 != 0 || (A.rows > 1 && A.dst_ld * es % 16 != 0)) return 0;

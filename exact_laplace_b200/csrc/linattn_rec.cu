@@ -22,9 +22,9 @@
 // the state's rows): half the instructions to issue.
 //
 // Bound by those multiply-adds (4 dk dv flops a token and head) and the latencies
-// around them: 32768 tokens, 16 heads of 128 x 128 take 972 us for the outputs, 499
-// for the states alone, 35 Tflop/s of the 72 that 128 fp32 units an SM give.  (6000
-// tokens, 6 heads of 72 x 104: 75 and 37 us; with one multiply-add an instruction and
+// around them: 32768 tokens, 16 heads of 128 x 128 take 942 us for the outputs, 477
+// for the states alone, 36 Tflop/s of the 72 that 128 fp32 units an SM give.  (6000
+// tokens, 6 heads of 72 x 104: 72 and 37 us; with one multiply-add an instruction and
 // outputs reduced token by token 119 and 54.)
 // Long sequences are cut into segments (see LinSeqs): a first pass sums each
 // segment's own state, carry_run joins them, and the product starts each segment

@@ -13,7 +13,11 @@
 // 4096 states of 128 x 128 (543 MB in all): 101 us, 5.4 TB/s, five blocks of 256
 // threads on an SM (48 registers; without that limit four: 107 us; two: 154).
 // TC = 128: 111 us, and 62 against 35 us for 64 x 64, whose blocks were half idle;
-// TC = 32: 142 us.  One row of 16 states: 3.5 us, launch and latency.
+// TC = 32: 142 us.  One row of 16 states: 3.5 us, launch and latency.  fp64 states,
+// two blocks on an SM: 4096 of 128 x 128 in 311 us, 3.5 TB/s.
+// With slots every block looks through all of them for its own: nothing beside the
+// states of a few hundred rows, but 186 against 138 us for 8192 rows of 2 states of
+// 64 x 64.
 #include <algorithm>
 
 #include "devcache.h"

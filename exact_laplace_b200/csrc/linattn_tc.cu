@@ -47,9 +47,21 @@
 // shared memory, whose bandwidth the products need.)
 //
 // Bounds of a chunk of dk = dv = 128: 128 KB of device memory (2.8 us of an SM's
-// share of the measured bandwidth), 2560 cycles of tensor work, about 5000 cycles
-// of shared memory (operands of the products 2300, copies 770, K's parts 770, the
-// state 256, outputs, tables).
+// share of the measured bandwidth), 2560 cycles of tensor work, by count about 5000
+// cycles of shared memory (operands of the products 2300, copies 770, K's parts 770,
+// the state 256, outputs, tables).  A chunk takes about 8000, and nothing is
+// saturated (32768 tokens, 16 heads: DRAM 46 %, tensor pipe 32 %, issue 40 %, the
+// warps' shared accesses 23 %; fp16, four q-heads: 21, 21, 37 and 10 %): what bounds
+// it is the chain P, weights, O1, outputs of one item after another, with one buffer
+// of each.
+//
+// Rounding to 16 bits: P's weights and the state that O2 reads, once each, because a
+// product of the tensor cores takes 16-bit operands (a second part of each would cost
+// half as many products again and 32 KB that the tiles do not leave at 128 x 128).
+// Independent roundings add in the mean square, so an output is off by about sqrt(2)
+// times its own rounding: rms 2.3e-3 in bf16 and 2.9e-4 in fp16, against 1.65e-3 and
+// 2.1e-4 of an output rounded once.  Rows given in fp32 take linattn_rec.cu, which
+// rounds neither.
 #include <algorithm>
 #include <atomic>
 
@@ -1173,6 +1185,15 @@ static cudaError_t encode(CUtensorMap* m, laplex_dtype dt, const LinRows& x, int
 // number of cuts by that count.  Lengths that only the device knows: pieces of a third (with three
 // roles a quarter) of an SM's share of all tokens, so that the longest sequence does not decide
 // (24 ragged sequences, 16384 tokens, 8 heads of 4 q-heads: 259 us against 490 us with cuts of 2816).
+// Known lengths, bf16, heads of 128 x 128, us; the rule's choice in brackets:
+//     1 x 65536 tokens, 16 heads: whole 1863, 16384 815, 7424 397, [3712 362], 1920 458
+//     1 x 4096, 8 heads:          whole 129, 1024 68, 512 48, [256 47]
+//     4 x 8192, 16 heads:         whole 247, 4096 240, [2048 214], 1024 241
+//     8 x 8192, 16 heads:         [whole 256], 4096 396, 2048 450
+//     10 x 4096, 16 heads:        whole 261, 2048 283, [1024 292]: 15 % off, the worst of 20
+//     gradients, 1 x 65536:       whole 1987, 14592 1263, [7296 928], 3712 1103
+//     gradients, 4 x 8192:        whole 551, 4096 530, [2816 475], 2048 604
+//     gradients, 16 x 4096:       [whole 865], 2048 1055, 1024 1058
 int tc_segment(int64_t T, int N, int H, int roles, bool equal) {
     const int64_t whole = std::min<int64_t>(std::max<int64_t>(T, 1) + 1, INT32_MAX);
     if (N == 0 || T == 0) return (int)whole;
