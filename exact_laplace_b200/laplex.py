@@ -544,6 +544,7 @@ def gram_matrix(sa, sb, D=None, pa=None, pb=None, out=None):
     return M
 
 
+@_serial
 def matvec_sym_noalloc(sorted_anchors: torch.Tensor, x: torch.Tensor, perm=None, out=None):
     """y = K x through laplex_matvec_sym_noalloc: fp32, x of shape [n], n <= 2^30.
 

@@ -1,6 +1,7 @@
-"""Host threads that share a stream, and therefore its workspace: the passes of
-one call are enqueued without another call's between them (no GPU needed: the
-library is replaced by one that records when a call starts and ends)."""
+"""Host threads that share a stream, and therefore its workspace (or the library's
+fixed scratch): the passes of one call are enqueued without another call's between
+them (no GPU needed: the library is replaced by one that records when a call starts
+and ends)."""
 import threading
 import time
 
@@ -72,6 +73,7 @@ def calls():
         "backward_general": lambda: X.backward_general(a, a, a, a),
         "backward_phased": lambda: X.backward_phased(a, a, a, a),
         "gram_matrix": lambda: X.gram_matrix(a, a),
+        "matvec_sym_noalloc": lambda: X.matvec_sym_noalloc(a, a),
     }
 
 
